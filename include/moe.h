@@ -367,6 +367,104 @@ int moe_experts_grouped(const moe_layer* layer, const void* x, int rows, const i
  * area), MOE_EHIP. */
 int moe_route_failures(void* ws, uint64_t ws_bytes, int clear, uint32_t* count, void* stream);
 
+/* ------------------------------------------- dense feed-forward operators
+ *
+ * The gated block of an unrouted expert, a shared expert in training or a
+ * dense layer, in 16 bits with its gradients, and 8-bit integer products
+ * with a scale per token and per channel. Same conventions as above: device
+ * pointers of the current device, nothing enqueued on an error, work enqueued
+ * on `stream`, no device allocation. Sizes: rows 1..2^20, hidden / inter / in
+ * / out 1..65536 (any value; rows of 16-byte multiples at 16-byte aligned
+ * addresses are read in place, others through a zero-padded copy in the
+ * workspace), row strides (ld*, in elements) from the row length to 2^22.
+ * Outputs must not overlap inputs or the workspace. Workspaces need no
+ * clearing and keep nothing between calls; calls that overlap in time need
+ * one each, and so do two captured graphs that may run at once. Every result
+ * depends on its inputs alone: sums have a fixed order, no atomics. */
+
+/* dtype of moe_quant_rows only (beside MOE_BF16 and MOE_FP16) */
+enum { MOE_FP32 = 16 };
+/* silu(g) = g / (1 + e^-g);
+ * gelu_tanh(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+enum moe_act { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 };
+enum moe_glu_kind { MOE_GLU_FORWARD = 0, MOE_GLU_BACKWARD = 1, MOE_GLU_I8 = 2 };
+
+/* The gated block h = act(x Wg^T) * (x Wu^T).
+ *   dtype   MOE_BF16 or MOE_FP16: x, h, gu, dh and the gradients; the weights
+ *           of the 16-bit form
+ *   w_gate, w_up  [inter, hidden], row strides ldw_gate and ldw_up; int8 for
+ *           moe_glu_i8, with s_gate, s_up [inter] fp32 (NULL otherwise)
+ *   x       [rows, hidden], row stride ldx
+ *   s_x     moe_glu_i8: NULL (x is of dtype and quantised inside the call, as
+ *           moe_quant_rows does), or [rows] fp32 (x is int8 with these scales) */
+typedef struct moe_glu {
+  int32_t rows, hidden, inter, dtype, act;
+  const void* w_gate;
+  const void* w_up;
+  int64_t ldw_gate, ldw_up;
+  const float* s_gate;
+  const float* s_up;
+  const void* x;
+  int64_t ldx;
+  const float* s_x;
+} moe_glu;
+
+/* Workspace bytes of one call (256-byte aligned device memory; 0: none, and
+ * ws may be NULL). The pointers and strides of *a count: rows the kernels
+ * cannot read in place need room for their copy. MOE_GLU_BACKWARD covers
+ * every choice of gradients. */
+int moe_glu_workspace_size(const moe_glu* a, int kind, uint64_t* bytes);
+
+/* h [rows, inter] (row stride ldh). With gu != NULL also the products before
+ * the activation, gu [rows, 2, inter] contiguous (g then u of each row), which
+ * moe_glu_backward reads. Sums, activation and product are fp32, rounded once.
+ * Up to 16 rows run in one launch that reads each weight once from memory.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESHAPE, MOE_ENOSPACE, MOE_EHIP. */
+int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes, void* stream);
+
+/* Gradients of the block from dh [rows, inter] (row stride lddh) and the gu of
+ * the forward call:
+ *   dg = dh * u * act'(g), du = dh * act(g)       (rounded to dtype once)
+ *   dx = dg Wg + du Wu   [rows, hidden], row stride lddx
+ *   dw_gate = dg^T x, dw_up = du^T x   [inter, hidden] contiguous
+ * dx may be NULL, or dw_gate and dw_up both (not wanted, not computed).
+ * fp16: dg and du beyond 65504 become infinite, as h does. */
+int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+                     void* dw_gate, void* dw_up, void* ws, uint64_t ws_bytes, void* stream);
+
+/* The gated block on 8-bit weights (see moe_glu): int32 sums, exact, times
+ * s_x[r] s_gate[i] (s_up[i]) in fp32, h rounded once to dtype. */
+int moe_glu_i8(const moe_glu* a, void* h, int64_t ldh, void* ws, uint64_t ws_bytes, void* stream);
+
+/* Rows to 8 bits: scale[r] = fp32(max|x[r]| / 127), q = round-half-even of the
+ * exact x / scale, within -127..127. A row of zeros: scale 0, q 0. A row
+ * holding an infinity or NaN: scale NaN, q 0 (so its products are NaN).
+ * The rows are tokens, or the channels of a weight matrix [out, in].
+ *   x [rows, cols] of dtype MOE_BF16, MOE_FP16 or MOE_FP32, row stride ldx
+ *   q [rows, cols], row stride ldq; q behind cols up to ldq is set to zero */
+int moe_quant_rows(const void* x, int dtype, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                   void* stream);
+
+/* y[r, o] = s_x[r] s_w[o] sum_i xq[r, i] w[o, i] (+ bias[o]), rounded once to
+ * dtype; the sums are exact int32.
+ *   w [out, in] int8, row stride ldw; s_w [out] fp32; bias [out] fp32 or NULL
+ *   x [rows, in] of dtype, quantised inside the call (s_x NULL), or int8 with
+ *   s_x [rows] fp32; row stride ldx */
+typedef struct moe_linear {
+  int32_t rows, in, out, dtype;
+  const int8_t* w;
+  int64_t ldw;
+  const float* s_w;
+  const float* bias;
+  const void* x;
+  int64_t ldx;
+  const float* s_x;
+} moe_linear;
+
+int moe_linear_i8_workspace_size(const moe_linear* a, uint64_t* bytes);
+/* y [rows, out], row stride ldy. Errors as moe_glu_forward. */
+int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t ws_bytes, void* stream);
+
 /* ----------------------------------------------------------- diagnostics */
 const char* moe_status_string(int status);
 const char* moe_last_error(void);   /* thread-local detail of the last failed call */

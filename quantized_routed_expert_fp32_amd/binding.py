@@ -65,12 +65,30 @@ class TapsC(C.Structure):
                 ("kernel_events", C.c_void_p * 8), ("route_wait_limit", C.c_int32)]
 
 
+class GluC(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("hidden", C.c_int32), ("inter", C.c_int32), ("dtype", C.c_int32),
+                ("act", C.c_int32), ("w_gate", C.c_void_p), ("w_up", C.c_void_p), ("ldw_gate", C.c_int64),
+                ("ldw_up", C.c_int64), ("s_gate", C.c_void_p), ("s_up", C.c_void_p), ("x", C.c_void_p),
+                ("ldx", C.c_int64), ("s_x", C.c_void_p)]
+
+
+class LinearC(C.Structure):
+    # `in` is a keyword of the language: the member is in_
+    _fields_ = [("rows", C.c_int32), ("in_", C.c_int32), ("out", C.c_int32), ("dtype", C.c_int32),
+                ("w", C.c_void_p), ("ldw", C.c_int64), ("s_w", C.c_void_p), ("bias", C.c_void_p),
+                ("x", C.c_void_p), ("ldx", C.c_int64), ("s_x", C.c_void_p)]
+
+
 EXPORTS = ["moe_pack_size", "moe_pack_layer_host", "moe_layer_bind", "moe_pack_layer",
            "moe_workspace_size", "moe_route", "moe_experts_decode", "moe_experts_grouped",
            "moe_forward_windows", "moe_forward_windows_noalloc", "moe_route_failures",
-           "moe_forward_exact", "moe_status_string", "moe_last_error", "moe_version"]
+           "moe_forward_exact", "moe_glu_workspace_size", "moe_glu_forward", "moe_glu_backward", "moe_glu_i8",
+           "moe_quant_rows", "moe_linear_i8_workspace_size", "moe_linear_i8", "moe_status_string", "moe_last_error", "moe_version"]
 
 MOE_WS_DECODE, MOE_WS_GROUPED, MOE_WS_EXACT = 0, 1, 2
+MOE_FP32 = 16
+MOE_GLU_FORWARD, MOE_GLU_BACKWARD, MOE_GLU_I8 = 0, 1, 2
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 _lib = None
 
@@ -102,6 +120,17 @@ def lib() -> C.CDLL:
     L.moe_forward_windows_noalloc.argtypes = [C.POINTER(LayerC), vp, i32, vp, vp, vp, vp, vp, vp]
     L.moe_forward_exact.argtypes = [C.POINTER(LayerC), vp, i32, vp, vp, vp, vp, vp, vp, u64,
                                     C.POINTER(TapsC), vp]
+    i64 = C.c_int64
+    L.moe_glu_workspace_size.argtypes = [C.POINTER(GluC), i32, C.POINTER(u64)]
+    L.moe_glu_forward.argtypes = [C.POINTER(GluC), vp, i64, vp, vp, u64, vp]
+    L.moe_glu_backward.argtypes = [C.POINTER(GluC), vp, vp, i64, vp, i64, vp, vp, vp, u64, vp]
+    L.moe_glu_i8.argtypes = [C.POINTER(GluC), vp, i64, vp, u64, vp]
+    L.moe_quant_rows.argtypes = [vp, i32, i32, i32, i64, vp, i64, vp, vp]
+    L.moe_linear_i8_workspace_size.argtypes = [C.POINTER(LinearC), C.POINTER(u64)]
+    L.moe_linear_i8.argtypes = [C.POINTER(LinearC), vp, i64, vp, u64, vp]
+    for f in ("moe_glu_workspace_size", "moe_glu_forward", "moe_glu_backward", "moe_glu_i8", "moe_quant_rows",
+              "moe_linear_i8_workspace_size", "moe_linear_i8"):
+        getattr(L, f).restype = C.c_int
     for f in ("moe_pack_size", "moe_pack_layer_host", "moe_layer_bind", "moe_pack_layer",
               "moe_workspace_size", "moe_route", "moe_experts_decode", "moe_experts_grouped",
               "moe_forward_windows", "moe_forward_windows_noalloc", "moe_route_failures",
@@ -377,3 +406,246 @@ def experts_decode(layer, x, ids, p, sg, **kw):
 
 def experts_grouped(layer, x, ids, p, sg, **kw):
     return experts(layer, x, ids, p, sg, True, **kw)
+
+
+# ------------------------------------------------- dense feed-forward operators
+def _rows2d(t, name, dtypes, shape=None, like=None):
+    """Checks a 2-D operand whose rows are contiguous (any row stride); its row
+    stride in elements (of a single row: the row length)."""
+    if t.dim() != 2:
+        raise MoeError(f"{name}: {t.dim()}-D tensor, needs 2 dimensions")
+    if t.dtype not in dtypes:
+        raise MoeError(f"{name}: dtype {t.dtype} is not {' or '.join(str(d) for d in dtypes)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise MoeError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
+    _same_device(t, name, like)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise MoeError(f"{name}: the elements of a row must be contiguous (strides {tuple(t.stride())})")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _same_device(t, name, like):
+    if not t.is_cuda:
+        raise MoeError(f"{name}: on {t.device}, needs device memory")
+    if like is not None and t.device != like.device:
+        raise MoeError(f"{name}: on {t.device}, x is on {like.device}")
+
+
+def _flat(t, name, n, dtype, like):
+    """Checks a contiguous vector of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise MoeError(f"{name}: {t.dtype} of shape {tuple(t.shape)}, needs contiguous {dtype} ({n},)")
+    _same_device(t, name, like)
+    return t.data_ptr()
+
+
+def _dtype_code(t):
+    import torch
+    return MOE_BF16 if t == torch.bfloat16 else MOE_FP16
+
+
+def _act_code(act):
+    if act not in ACTIVATIONS:
+        raise MoeError(f"act: {act!r} is not one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+class _call:
+    """The device of x current, and `stream` too where one is given: outputs and
+    the workspace of a call are allocated on the stream that uses them."""
+
+    def __init__(self, x, stream):
+        import torch
+        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.device)
+        if stream is not None and stream.device != x.device:
+            raise MoeError(f"stream: on {stream.device}, x is on {x.device}")
+
+    def __enter__(self):
+        self.ctx.__enter__()
+
+    def __exit__(self, *a):
+        return self.ctx.__exit__(*a)
+
+
+def _ws_for(n, ws, x):
+    import torch
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    if ws is None:
+        return None, 0, None
+    if not ws.is_contiguous():
+        raise MoeError("ws: needs contiguous memory")
+    _same_device(ws, "ws", x)
+    return C.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+
+
+def _glu_args(x, w_gate, w_up, act, s_gate=None, s_up=None, x_scale=None, out_dtype=None):
+    import torch
+    half = (torch.bfloat16, torch.float16)
+    i8 = s_gate is not None
+    ldx = _rows2d(x, "x", (torch.int8,) if x_scale is not None else half)
+    wt = (torch.int8,) if i8 else (x.dtype,)
+    ldg = _rows2d(w_gate, "w_gate", wt, like=x)
+    I, H = w_gate.shape
+    if x.shape[1] != H:
+        raise MoeError(f"x: rows of {x.shape[1]} elements, w_gate has {H} columns")
+    ldu = _rows2d(w_up, "w_up", wt, shape=(I, H), like=x)
+    dt = out_dtype if x_scale is not None else x.dtype
+    a = GluC(x.shape[0], H, I, _dtype_code(dt), _act_code(act), w_gate.data_ptr(), w_up.data_ptr(), ldg, ldu,
+             None, None, x.data_ptr(), ldx, None)
+    if i8:
+        a.s_gate = _flat(s_gate, "s_gate", I, torch.float32, x)
+        a.s_up = _flat(s_up, "s_up", I, torch.float32, x)
+        a.s_x = _flat(x_scale, "x_scale", x.shape[0], torch.float32, x)
+    return a, dt
+
+
+def glu_workspace_size(x, w_gate, w_up, kind=MOE_GLU_FORWARD, s_gate=None, s_up=None, x_scale=None) -> int:
+    """moe_glu_workspace_size of a call on these tensors, in bytes."""
+    import torch
+    a, _ = _glu_args(x, w_gate, w_up, "silu", s_gate, s_up, x_scale, torch.bfloat16)
+    n = C.c_uint64()
+    _check(lib().moe_glu_workspace_size(C.byref(a), kind, C.byref(n)), "moe_glu_workspace_size")
+    return n.value
+
+
+def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=None, stream=None):
+    """moe_glu_forward: h = act(x w_gate^T) * (x w_up^T), [rows, inter] of x's
+    dtype (bf16 or fp16); with save=True (h, gu), gu [rows, 2, inter] being what
+    glu_backward takes."""
+    import torch
+    a, dt = _glu_args(x, w_gate, w_up, act)
+    R, I = a.rows, a.inter
+    with _call(x, stream):
+        if h is None:
+            h = torch.empty((R, I), dtype=dt, device=x.device)
+        ldh = _rows2d(h, "h", (dt,), (R, I), x)
+        if save and gu is None:
+            gu = torch.empty((R, 2, I), dtype=dt, device=x.device)
+        if gu is not None:
+            _gu_ok(gu, R, I, dt, x)
+        n = C.c_uint64()
+        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_FORWARD, C.byref(n)), "moe_glu_workspace_size")
+        wp, wn, ws = _ws_for(n.value, ws, x)
+        _check(lib().moe_glu_forward(C.byref(a), _ptr(h), ldh, _ptr(gu), wp, wn, _stream_ptr(stream)),
+               "moe_glu_forward")
+    return (h, gu) if gu is not None else h
+
+
+def _gu_ok(gu, R, I, dt, x):
+    if gu.dtype != dt or tuple(gu.shape) != (R, 2, I) or not gu.is_contiguous():
+        raise MoeError(f"gu: {gu.dtype} of shape {tuple(gu.shape)}, needs contiguous {dt} ({R}, 2, {I})")
+    _same_device(gu, "gu", x)
+
+
+def glu_backward(dh, x, w_gate, w_up, gu, act="silu", need_dx=True, need_dw=True, dx=None, dw_gate=None,
+                 dw_up=None, ws=None, stream=None):
+    """moe_glu_backward: (dx, dw_gate, dw_up) of glu_forward(..., save=True) from
+    dh and its gu; None in the place of a gradient that is not needed."""
+    import torch
+    a, dt = _glu_args(x, w_gate, w_up, act)
+    R, H, I = a.rows, a.hidden, a.inter
+    _gu_ok(gu, R, I, dt, x)
+    lddh = _rows2d(dh, "dh", (dt,), (R, I), x)
+    if not need_dx and not need_dw:
+        raise MoeError("glu_backward: neither need_dx nor need_dw")
+    with _call(x, stream):
+        lddx = 0
+        if need_dx:
+            if dx is None:
+                dx = torch.empty((R, H), dtype=dt, device=x.device)
+            lddx = _rows2d(dx, "dx", (dt,), (R, H), x)
+        if need_dw:
+            if dw_gate is None:
+                dw_gate = torch.empty((I, H), dtype=dt, device=x.device)
+            if dw_up is None:
+                dw_up = torch.empty((I, H), dtype=dt, device=x.device)
+            for t, nm in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
+                if _rows2d(t, nm, (dt,), (I, H), x) != H:
+                    raise MoeError(f"{nm}: needs contiguous memory")
+        dx, dw_gate, dw_up = dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None
+        n = C.c_uint64()
+        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_BACKWARD, C.byref(n)), "moe_glu_workspace_size")
+        wp, wn, ws = _ws_for(n.value, ws, x)
+        _check(lib().moe_glu_backward(C.byref(a), _ptr(gu), _ptr(dh), lddh, _ptr(dx), lddx, _ptr(dw_gate),
+                                      _ptr(dw_up), wp, wn, _stream_ptr(stream)), "moe_glu_backward")
+    return dx, dw_gate, dw_up
+
+
+def glu_i8(x, w_gate, s_gate, w_up, s_up, act="silu", x_scale=None, out_dtype=None, h=None, ws=None, stream=None):
+    """moe_glu_i8: the gated block on int8 weights [inter, hidden] with fp32
+    channel scales [inter]; x in bf16/fp16 (quantised a token inside the call),
+    or int8 with x_scale [rows] (then out_dtype is h's type, bf16 by default)."""
+    import torch
+    a, dt = _glu_args(x, w_gate, w_up, act, s_gate, s_up, x_scale, _out_dtype(out_dtype, x, x_scale))
+    R, I = a.rows, a.inter
+    with _call(x, stream):
+        if h is None:
+            h = torch.empty((R, I), dtype=dt, device=x.device)
+        ldh = _rows2d(h, "h", (dt,), (R, I), x)
+        n = C.c_uint64()
+        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_I8, C.byref(n)), "moe_glu_workspace_size")
+        wp, wn, ws = _ws_for(n.value, ws, x)
+        _check(lib().moe_glu_i8(C.byref(a), _ptr(h), ldh, wp, wn, _stream_ptr(stream)), "moe_glu_i8")
+    return h
+
+
+def _out_dtype(out_dtype, x, x_scale):
+    import torch
+    if out_dtype is None:
+        return torch.bfloat16
+    if x_scale is None and out_dtype != x.dtype:
+        raise MoeError(f"out_dtype: {out_dtype} with x of {x.dtype} (it is a choice for int8 x only)")
+    if out_dtype not in (torch.bfloat16, torch.float16):
+        raise MoeError(f"out_dtype: {out_dtype} is not torch.bfloat16 or torch.float16")
+    return out_dtype
+
+
+def quant_rows(x, q=None, scale=None, stream=None):
+    """moe_quant_rows: rows of x (bf16, fp16 or fp32) as (int8 [rows, cols],
+    fp32 scale [rows]); of a weight matrix [out, in] the rows are its channels."""
+    import torch
+    ldx = _rows2d(x, "x", (torch.bfloat16, torch.float16, torch.float32))
+    R, K = x.shape
+    with _call(x, stream):
+        if q is None:
+            q = torch.empty((R, K), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty((R,), dtype=torch.float32, device=x.device)
+        ldq = _rows2d(q, "q", (torch.int8,), (R, K), x)
+        if ldq != K:
+            raise MoeError("q: needs contiguous memory")
+        sp = _flat(scale, "scale", R, torch.float32, x)
+        code = MOE_FP32 if x.dtype == torch.float32 else _dtype_code(x.dtype)
+        _check(lib().moe_quant_rows(_ptr(x), code, R, K, ldx, _ptr(q), ldq, C.c_void_p(sp), _stream_ptr(stream)),
+               "moe_quant_rows")
+    return q, scale
+
+
+def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=None, stream=None):
+    """moe_linear_i8: y = x w^T (+ bias) for int8 w [out, in] with fp32 channel
+    scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
+    int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default)."""
+    import torch
+    ldx = _rows2d(x, "x", (torch.int8,) if x_scale is not None else (torch.bfloat16, torch.float16))
+    ldw = _rows2d(w, "w", (torch.int8,), like=x)
+    N, K = w.shape
+    if x.shape[1] != K:
+        raise MoeError(f"x: rows of {x.shape[1]} elements, w has {K} columns")
+    R = x.shape[0]
+    dt = _out_dtype(out_dtype, x, x_scale)
+    dt = dt if x_scale is not None else x.dtype
+    a = LinearC(R, K, N, _dtype_code(dt), w.data_ptr(), ldw, _flat(s_w, "s_w", N, torch.float32, x),
+                _flat(bias, "bias", N, torch.float32, x), x.data_ptr(), ldx,
+                _flat(x_scale, "x_scale", R, torch.float32, x))
+    with _call(x, stream):
+        if y is None:
+            y = torch.empty((R, N), dtype=dt, device=x.device)
+        ldy = _rows2d(y, "y", (dt,), (R, N), x)
+        n = C.c_uint64()
+        _check(lib().moe_linear_i8_workspace_size(C.byref(a), C.byref(n)), "moe_linear_i8_workspace_size")
+        wp, wn, ws = _ws_for(n.value, ws, x)
+        _check(lib().moe_linear_i8(C.byref(a), _ptr(y), ldy, wp, wn, _stream_ptr(stream)), "moe_linear_i8")
+    return y

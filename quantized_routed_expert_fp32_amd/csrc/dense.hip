@@ -1,0 +1,717 @@
+// Dense feed-forward products beside the routed experts: the gated block
+// h = act(x Wg^T) * (x Wu^T) in 16 bits with its gradients, and products of
+// 8-bit integers with a scale per token and per channel.
+#include "dense_launch.h"
+
+#include <algorithm>
+
+namespace moe {
+
+typedef _Float16 f16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------ element types
+template <int T> struct Elem;
+template <> struct Elem<DT_BF16> {
+  typedef __bf16 type;
+  typedef f32x16 acc;
+  typedef f32x4 acc4;
+  static constexpr int SIZE = 2;
+  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c,
+                                                   0, 0, 0);
+  }
+  static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c,
+                                                   0, 0, 0);
+  }
+};
+template <> struct Elem<DT_F16> {
+  typedef f16 type;
+  typedef f32x16 acc;
+  typedef f32x4 acc4;
+  static constexpr int SIZE = 2;
+  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0,
+                                                  0, 0);
+  }
+  static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0,
+                                                  0, 0);
+  }
+};
+template <> struct Elem<DT_I8> {
+  typedef int8_t type;
+  typedef i32x16 acc;
+  typedef i32x4 acc4;
+  static constexpr int SIZE = 1;
+  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, q), c, 0, 0,
+                                                 0);
+  }
+  static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, q), c, 0, 0,
+                                                 0);
+  }
+};
+
+// ------------------------------------------------------------- activations
+// silu(g) = g s(g); gelu_tanh(g) = g s(w(g)) with w = 2 sqrt(2/pi) (g +
+// 0.044715 g^3), since (1 + tanh(w/2)) / 2 = s(w): one sigmoid for both.
+constexpr float GELU_C = 1.5957691216057308f;
+__device__ __forceinline__ float sigmoid_f(float w) { return 1.f / (1.f + __expf(-w)); }
+__device__ __forceinline__ float act_f(float g, int act) {
+  const float w = act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
+  return g * sigmoid_f(w);
+}
+// value and derivative: p + g p (1 - p) w'; where p (1 - p) is zero the
+// second term is (w' may overflow there)
+__device__ __forceinline__ void act_grad_f(float g, int act, float* v, float* d) {
+  const float w = act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
+  const float dw = act == ACT_SILU ? 1.f : GELU_C * (1.f + 0.134145f * g * g);
+  const float p = sigmoid_f(w);
+  const float pp = p * sigmoid_f(-w);
+  *v = g * p;
+  *d = p + (pp > 0.f ? g * pp * dw : 0.f * pp);
+}
+
+// ------------------------------------------------------------------ stores
+template <int T> __device__ __forceinline__ uint16_t to16(float v) {
+  if constexpr (T == DT_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return __builtin_bit_cast(uint16_t, (f16)v);
+}
+__device__ __forceinline__ uint16_t to16_rt(float v, int dt) {
+  return dt == DT_BF16 ? to16<DT_BF16>(v) : to16<DT_F16>(v);
+}
+__device__ __forceinline__ float from16_rt(uint16_t b, int dt) {
+  return dt == DT_BF16 ? __uint_as_float((uint32_t)b << 16) : (float)__builtin_bit_cast(f16, b);
+}
+// four consecutive outputs of a row, the first at column p of np
+__device__ __forceinline__ void store4(void* row, int p, int np, int dt, bool vec, const float* v) {
+  if (dt == DT_F32) {
+    float* o = static_cast<float*>(row) + p;
+    if (vec && p + 4 <= np) *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      for (int i = 0; i < 4; ++i)
+        if (p + i < np) o[i] = v[i];
+    return;
+  }
+  uint16_t* o = static_cast<uint16_t*>(row) + p;
+  uint16_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = to16_rt(v[i], dt);
+  if (vec && p + 4 <= np)
+    *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+  else
+    for (int i = 0; i < 4; ++i)
+      if (p + i < np) o[i] = b[i];
+}
+// row q of the product's output, or null when q is padding between the two
+__device__ __forceinline__ char* out_row(const DenseArgs& a, int q) {
+  const int64_t es = a.out_dt == DT_F32 ? 4 : 2;
+  if (!a.qpad) return static_cast<char*>(a.out0) + q * a.ldo * es;
+  if (q < a.qseg) return static_cast<char*>(a.out0) + q * a.ldo * es;
+  if (q >= a.qpad && q < a.qpad + a.qseg) return static_cast<char*>(a.out1) + (q - a.qpad) * a.ldo * es;
+  return nullptr;
+}
+__device__ __forceinline__ bool vec_ok(const void* p, int64_t ld, int es) {
+  return ((uintptr_t)p % (4 * es) == 0) && (ld % 4 == 0);
+}
+
+// The epilogues on four consecutive columns p.. of row q. `s0` and `s1` are
+// the sums (gate and up for GLU) as fp32 or int32.
+template <int T, int EPI, typename V>
+__device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const V* s0, const V* s1) {
+  if (q >= a.nq || p >= a.np) return;
+  float v[4], g[4], u[4];
+  if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (T == DT_I8) {
+        const float sq = a.sq[q];
+        const int pi = min(p + i, a.np - 1);
+        g[i] = (float)s0[i] * (sq * a.sp0[pi]);
+        u[i] = (float)s1[i] * (sq * a.sp1[pi]);
+      } else {
+        g[i] = s0[i];
+        u[i] = s1[i];
+      }
+      v[i] = act_f(g[i], a.act) * u[i];
+    }
+    if (a.save) {
+      uint16_t* sv = static_cast<uint16_t*>(a.save) + (int64_t)q * 2 * a.np;
+      const bool vec = a.np % 4 == 0 && (uintptr_t)a.save % 8 == 0;
+      store4(sv, p, a.np, a.out_dt, vec, g);
+      store4(sv + a.np, p, a.np, a.out_dt, vec, u);
+    }
+  } else if constexpr (EPI == EPI_SCALE) {
+    const float sq = a.sq[q];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pi = min(p + i, a.np - 1);
+      v[i] = (float)s0[i] * (sq * a.sp0[pi]) + (a.bias ? a.bias[pi] : 0.f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = s0[i];
+  }
+  char* row = out_row(a, q);
+  if (row) store4(row, p, a.np, a.out_dt, vec_ok(a.out0, a.ldo, a.out_dt == DT_F32 ? 4 : 2) &&
+                  (!a.qpad || vec_ok(a.out1, a.ldo, a.out_dt == DT_F32 ? 4 : 2)), v);
+}
+
+// ------------------------------------------------------- loads into the ring
+// 64 x 16 bytes from base + off (a lane's own) to LDS [lds, lds + 1024). The
+// compiler does not see it, so a read of the ring is ordered by step_wait.
+__device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const uint8_t* base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
+}
+// the same with a whole address per lane (the last step's masked loads)
+__device__ __forceinline__ void dma16_at(uint32_t lds, const uint8_t* src) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
+}
+// the wave's own loads but the newest N have landed, its LDS reads are done;
+// then every wave's
+template <int N> __device__ __forceinline__ void step_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 zero bytes: what a masked load reads (K behind the operand's end)
+__device__ const u32x4 g_zero16 = {0, 0, 0, 0};
+
+// ---------------------------------------------------------------- the product
+// Workgroup tile BP x BQ, K step 128 bytes (k-contiguous) = 64 k (16-bit).
+// k-contiguous operand in LDS: row r of 128 bytes, its 16-byte chunk c at
+// position c ^ (r & 7). k-major operand: row k of B*2 bytes, its 32-byte
+// segment s at s ^ (k & 3 | (k >> 3 & 1) << 2).
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+struct Dense {
+  static constexpr bool PKM = FORM != FORM_NT, QKM = FORM == FORM_TN;
+  static constexpr int NW = WP * WQ;
+  static constexpr int TP = BP / WP, TQ = BQ / WQ, FP = TP / 32, FQ = TQ / 32;
+  static constexpr int PB = BP * 128, QB = BQ * 128, STAGE = PB + QB;
+  static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
+  typedef typename Elem<T>::acc acc_t;
+
+  // k-major rows: what the segment index is xor-ed with (the same for k and k + 4)
+  template <int B> static __device__ __forceinline__ int swz_km(int k) {
+    return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
+  }
+  // source offset of load i of a lane: k-contiguous rows (row0 + r clamped
+  // below n), GLU rows interleaved 32 gate, 32 up
+  template <bool KM, int B, int L>
+  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld, bool glu) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int seg = i * NW + w;
+      if constexpr (!KM) {
+        const int r = seg * 8 + (lane >> 3);
+        const int c = (lane & 7) ^ (r & 7);
+        const int idx = glu ? c0 + (r >> 6) * 32 + (r & 31) : c0 + r;
+        off[i] = (uint32_t)(min(idx, n - 1) - c0) * (uint32_t)ld + c * 16;
+      } else {
+        constexpr int CPR = B * 2 / 16;                 // chunks per k row
+        const int q = seg * 64 + lane;
+        const int k = q / CPR, pos = q % CPR;
+        const int s = (pos >> 1) ^ swz_km<B>(k);
+        const int col = c0 + (s * 2 + (pos & 1)) * 8;
+        off[i] = (uint32_t)k * (uint32_t)ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
+      }
+    }
+  }
+
+  // LDS byte address (relative to the operand's tile) of fragment f's lane data at kk (0..3)
+  static __device__ __forceinline__ u32x4 frag_kc(const uint8_t* tile, int row, int kk, int half) {
+    return *reinterpret_cast<const u32x4*>(tile + row * 128 + (((kk * 2 + half) ^ (row & 7)) << 4));
+  }
+  // k-major: the lane's 8 k of column col0 + lane % 32: two 4-row transposed
+  // reads; a 16-lane group reads 4 rows of 16 columns, lane i supplying the
+  // address of row i / 4, columns 4 (i % 4).. and getting column i's 4 rows
+  template <int B>
+  static __device__ __forceinline__ u32x4 frag_km(const uint8_t* tile, int col0, int kk, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
+    const int col = col0 + (g & 1) * 16 + (i & 3) * 4;
+    const uint8_t* ad = tile + k * (B * 2) + ((((col >> 4) ^ swz_km<B>(k)) << 5) | ((col & 15) << 1));
+    typedef __attribute__((address_space(3))) i16x4* lp;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(ad));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(ad + 4 * (B * 2)));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return u32x4{a.x, a.y, b.x, b.y};
+  }
+
+  static __device__ __forceinline__ void run(const DenseArgs& a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = w % WP, wq = w / WP;
+    constexpr int OP = EPI == EPI_GLU ? BP / 2 : BP;    // output columns of a tile
+    const int tp = (a.np + OP - 1) / OP, tq = (a.nq + BQ - 1) / BQ;
+    // workgroup i runs on XCD i mod 8: each XCD takes a contiguous run of
+    // tiles, in bands of GQ tile rows, so that its L2 serves both operands
+    int id = blockIdx.x;
+    const int tiles = tp * tq;
+    {
+      const int x = id & 7, j = id >> 3, per = tiles >> 3, rem = tiles & 7;
+      id = x * per + min(x, rem) + j;
+    }
+    constexpr int GQ = 4;
+    const int band = id / (GQ * tp), inb = id % (GQ * tp);
+    const int gh = min(GQ, tq - band * GQ);
+    const int iq = band * GQ + inb % gh, ip = inb / gh;
+    const int c0p = ip * OP, c0q = iq * BQ;
+    // K steps of this workgroup
+    const int z = blockIdx.y;
+    const int t0 = (int)((int64_t)a.steps * z / a.splits), t1 = (int)((int64_t)a.steps * (z + 1) / a.splits);
+
+    uint32_t offp[LP], offq[LQ];
+    offsets<PKM, BP, LP>(offp, w, lane, c0p, a.np, a.ldp0, EPI == EPI_GLU);
+    offsets<QKM, BQ, LQ>(offq, w, lane, c0q, a.nq, a.ldq, false);
+    const uint8_t* pb0 = a.p0 + (PKM ? (int64_t)c0p * 2 : (int64_t)c0p * a.ldp0);
+    const uint8_t* pb1 = a.p1 ? a.p1 + (PKM ? (int64_t)c0p * 2 : (int64_t)c0p * a.ldp1) : nullptr;
+    const uint8_t* qb = a.q0 + (QKM ? (int64_t)c0q * 2 : (int64_t)c0q * a.ldq);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)smem);
+
+    auto issue = [&](int t, int slot) {
+      const uint32_t ldst = lds0 + slot * STAGE;
+      // P
+      if constexpr (!PKM) {
+        const bool full = (t + 1) * 128 <= a.kbytes;
+#pragma unroll
+        for (int i = 0; i < LP; ++i) {
+          const uint32_t l = ldst + (i * NW + w) * 1024;
+          const bool up = EPI == EPI_GLU && (((i * NW + w) >> 2) & 1);
+          const uint8_t* b = (up ? pb1 : pb0) + (int64_t)t * 128;
+          if (full) dma16(l, offp[i], b);
+          else {
+            const int c = (lane & 7) ^ (lane >> 3);
+            dma16_at(l, t * 128 + c * 16 < a.kbytes ? b + offp[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
+          }
+        }
+      } else {
+        const bool second = FORM == FORM_NN && t >= a.seg;
+        const int tt = second ? t - a.seg : t;
+        const uint8_t* b = (second ? pb1 : pb0) + (int64_t)tt * 64 * a.ldp0;
+        const bool full = (tt + 1) * 64 <= a.krows;
+#pragma unroll
+        for (int i = 0; i < LP; ++i) {
+          const uint32_t l = ldst + (i * NW + w) * 1024;
+          if (full) dma16(l, offp[i], b);
+          else {
+            const int k = ((i * NW + w) * 64 + lane) / (BP * 2 / 16);
+            dma16_at(l, tt * 64 + k < a.krows ? b + offp[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
+          }
+        }
+      }
+      // Q
+      if constexpr (!QKM) {
+        const uint8_t* b = qb + (int64_t)t * 128;
+        const bool full = (t + 1) * 128 <= a.kbytes;
+#pragma unroll
+        for (int i = 0; i < LQ; ++i) {
+          const uint32_t l = ldst + PB + (i * NW + w) * 1024;
+          if (full) dma16(l, offq[i], b);
+          else {
+            const int c = (lane & 7) ^ (lane >> 3);
+            dma16_at(l, t * 128 + c * 16 < a.kbytes ? b + offq[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
+          }
+        }
+      } else {
+        const uint8_t* b = qb + (int64_t)t * 64 * a.ldq;
+        const bool full = (t + 1) * 64 <= a.krows;
+#pragma unroll
+        for (int i = 0; i < LQ; ++i) {
+          const uint32_t l = ldst + PB + (i * NW + w) * 1024;
+          if (full) dma16(l, offq[i], b);
+          else {
+            const int k = ((i * NW + w) * 64 + lane) / (BQ * 2 / 16);
+            dma16_at(l, t * 64 + k < a.krows ? b + offq[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
+          }
+        }
+      }
+    };
+
+    acc_t acc[FP][FQ];
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) acc[i][j] = acc_t{};
+
+    const int col = lane & 31, half = lane >> 5;
+    auto compute = [&](int slot) {
+      const uint8_t* pt = smem + slot * STAGE;
+      const uint8_t* qt = pt + PB;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        u32x4 fp[FP], fq[FQ];
+#pragma unroll
+        for (int i = 0; i < FP; ++i) {
+          if constexpr (PKM) fp[i] = frag_km<BP>(pt, wp * TP + i * 32, kk, lane);
+          else fp[i] = frag_kc(pt, wp * TP + i * 32 + col, kk, half);
+        }
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+          if constexpr (QKM) fq[j] = frag_km<BQ>(qt, wq * TQ + j * 32, kk, lane);
+          else fq[j] = frag_kc(qt, wq * TQ + j * 32 + col, kk, half);
+        }
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+          for (int j = 0; j < FQ; ++j) acc[i][j] = Elem<T>::mma(fp[i], fq[j], acc[i][j]);
+      }
+    };
+
+    // ring of NS stages, loads NS - 1 steps ahead. At step t the wave waits
+    // for its loads of step t, the barrier makes every wave's part visible
+    // and tells that all have finished step t - 1, whose stage is refilled.
+    int issued = t0, ws = 0, rs = 0;
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i)
+      if (issued < t1) {
+        issue(issued++, ws);
+        ws = ws + 1 == NS ? 0 : ws + 1;
+      }
+    for (int t = t0; t < t1; ++t) {
+      if (t + NS - 1 <= t1) step_wait<(NS - 2) * (LP + LQ)>();
+      else step_wait<0>();
+      if (issued < t1) {
+        issue(issued++, ws);
+        ws = ws + 1 == NS ? 0 : ws + 1;
+      }
+      compute(rs);
+      rs = rs + 1 == NS ? 0 : rs + 1;
+    }
+
+    // epilogue: lane holds column q = col, rows p = 8 (i / 4) + 4 half + i % 4
+    const int q0 = c0q + wq * TQ + col;
+    if (a.splits > 1) {
+      const int64_t zoff = (int64_t)z * a.nq * a.pcols;
+#pragma unroll
+      for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+          const int q = q0 + j * 32;
+          if (q >= a.nq) continue;
+          const bool up = EPI == EPI_GLU && (i & 1);
+          const int pbase = EPI == EPI_GLU ? c0p + ((wp * TP + i * 32) >> 6) * 32 : c0p + wp * TP + i * 32;
+          typename Elem<T>::acc4* row = reinterpret_cast<typename Elem<T>::acc4*>(
+              a.part + zoff + q * a.pcols + (up ? a.pcols / 2 : 0));
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int p = pbase + b * 8 + half * 4;
+            if (p < a.np)
+              row[p >> 2] = {acc[i][j][b * 4], acc[i][j][b * 4 + 1], acc[i][j][b * 4 + 2], acc[i][j][b * 4 + 3]};
+          }
+        }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int q = q0 + j * 32;
+#pragma unroll
+      for (int i = 0; i < FP; i += EPI == EPI_GLU ? 2 : 1) {
+        const int pbase = EPI == EPI_GLU ? c0p + ((wp * TP + i * 32) >> 6) * 32 : c0p + wp * TP + i * 32;
+        constexpr int I1 = EPI == EPI_GLU ? 1 : 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          decltype(acc[0][0][0] + 0) s0[4], s1[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s0[e] = acc[i][j][b * 4 + e];
+            s1[e] = acc[i + I1][j][b * 4 + e];
+          }
+          finish4<T, EPI>(a, q, pbase + b * 8 + half * 4, s0, s1);
+        }
+      }
+    }
+  }
+};
+
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+__global__ __launch_bounds__(WP * WQ * 64) void k_dense(DenseArgs a) {
+  Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS>::run(a);
+}
+
+// Joins the K ranges of a split product, range 0 first, and runs its epilogue.
+template <int T, int EPI>
+__global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
+  const int p = (blockIdx.x * 256 + threadIdx.x) * 4, q = blockIdx.y;
+  if (p >= a.np) return;
+  typedef typename Elem<T>::acc4 acc4;
+  const int64_t stride = (int64_t)a.nq * a.pcols;
+  const float* r0 = a.part + q * a.pcols + p;
+  const float* r1 = r0 + (EPI == EPI_GLU ? a.pcols / 2 : 0);
+  acc4 v0 = *reinterpret_cast<const acc4*>(r0), v1 = *reinterpret_cast<const acc4*>(r1);
+  for (int z = 1; z < a.splits; ++z) {
+    v0 += *reinterpret_cast<const acc4*>(r0 + z * stride);
+    if constexpr (EPI == EPI_GLU) v1 += *reinterpret_cast<const acc4*>(r1 + z * stride);
+  }
+  decltype(v0[0] + 0) s0[4], s1[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    s0[e] = v0[e];
+    s1[e] = v1[e];
+  }
+  finish4<T, EPI>(a, q, p, s0, s1);
+}
+
+// --------------------------------------------------------------- decode rows
+// nq <= 16: a workgroup of 16 waves computes 16 weight rows (GLU: 8 gate and
+// 8 up) against every activation row on 16x16 matrix instructions; the waves
+// take 64-byte K blocks in turn and their sums join through LDS.
+template <int T>
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int64_t byte, int64_t end) {
+  u32x4 v = {0, 0, 0, 0};
+  if (byte + 16 <= end) {
+    __builtin_memcpy(&v, row + byte, 16);
+  } else {
+    uint8_t* b = reinterpret_cast<uint8_t*>(&v);
+    constexpr int ES = Elem<T>::SIZE;
+#pragma unroll
+    for (int i = 0; i < 16; i += ES)
+      if (byte + i < end) __builtin_memcpy(b + i, row + byte + i, ES);
+  }
+  return v;
+}
+
+template <int T, int EPI>
+__global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
+  const DenseArgs& a = da.d;
+  typedef typename Elem<T>::acc4 acc4;
+  __shared__ __align__(16) uint8_t red[16 * 1024];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int r = lane & 15, c = lane >> 4;
+  constexpr int OP = EPI == EPI_GLU ? 8 : 16;
+  const int p0 = blockIdx.x * OP;
+  const uint8_t* pr;
+  if (EPI == EPI_GLU) {
+    const int p = min(p0 + (r & 7), a.np - 1);
+    pr = r < 8 ? a.p0 + (int64_t)p * a.ldp0 : a.p1 + (int64_t)p * a.ldp1;
+  } else {
+    pr = a.p0 + (int64_t)min(p0 + r, a.np - 1) * a.ldp0;
+  }
+  const uint8_t* qr = a.q0 + (int64_t)min(r, a.nq - 1) * a.ldq;
+  const int64_t kb = (int64_t)da.k * Elem<T>::SIZE;
+  const int nblk = (int)((kb + 63) / 64);
+  acc4 acc = {};
+  constexpr int U = 4;
+  for (int b = w; b < nblk; b += 16 * U) {
+    u32x4 pv[U], qv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t byte = (int64_t)(b + u * 16) * 64 + c * 16;
+      pv[u] = load_chunk<T>(pr, byte, kb);
+      qv[u] = load_chunk<T>(qr, byte, kb);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc = Elem<T>::mma16(pv[u], qv[u], acc);
+  }
+  // lane: q = lane % 16, p = 4 (lane / 16) + e; red[w][q][p]
+  acc4* rd = reinterpret_cast<acc4*>(red);
+  rd[w * 64 + r * 4 + c] = acc;
+  __syncthreads();
+  typedef decltype(acc[0] + 0) V;
+  if (threadIdx.x < (EPI == EPI_GLU ? 32 : 64)) {
+    constexpr int PG = OP / 4;
+    const int q = threadIdx.x / PG, g = threadIdx.x % PG;
+    acc4 v0 = {}, v1 = {};
+    for (int i = 0; i < 16; ++i) {
+      v0 += rd[i * 64 + q * 4 + g];
+      if constexpr (EPI == EPI_GLU) v1 += rd[i * 64 + q * 4 + 2 + g];
+    }
+    V s0[4], s1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s0[e] = v0[e];
+      s1[e] = v1[e];
+    }
+    finish4<T, EPI>(a, q, p0 + g * 4, s0, s1);
+  }
+}
+
+// ----------------------------------------------------------- small kernels
+template <typename E>
+__global__ __launch_bounds__(256) void k_dense_pad(const E* src, int64_t ld, int cols, E* dst, int64_t ldd) {
+  const int64_t r = blockIdx.x;
+  for (int64_t i = threadIdx.x; i < ldd; i += 256) dst[r * ldd + i] = i < cols ? src[r * ld + i] : (E)0;
+}
+
+template <int T> struct Row;
+template <> struct Row<DT_BF16> {
+  typedef uint16_t type;
+  static __device__ __forceinline__ float f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+};
+template <> struct Row<DT_F16> {
+  typedef uint16_t type;
+  static __device__ __forceinline__ float f(uint16_t b) { return (float)__builtin_bit_cast(f16, b); }
+};
+template <> struct Row<DT_F32> {
+  typedef float type;
+  static __device__ __forceinline__ float f(float b) { return b; }
+};
+
+// q = round-half-even(x / s) of the exact quotient, |q| <= 127. The fp32
+// quotient decides unless it lies next to a half-integer; there the 53-bit
+// quotient of the two 24-bit numbers does (x - s (n + 1/2) is either zero or
+// at least 2^-32 of x, so 53 bits tell the two apart).
+__device__ __forceinline__ int quant1(float x, float s, float inv) {
+  float t = x * inv;
+  float n = __builtin_rintf(t);
+  if (__builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < 1e-3f) n = (float)__builtin_rint((double)x / (double)s);
+  return (int)__builtin_fminf(__builtin_fmaxf(n, -127.f), 127.f);
+}
+
+template <int T>
+__global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type* x, int64_t ldx, int cols, int8_t* q,
+                                                    int64_t ldq, float* scale) {
+  __shared__ uint32_t red[4];
+  const int64_t r = blockIdx.x;
+  const typename Row<T>::type* xr = x + r * ldx;
+  // |x| as bits: ordered as the values, infinity and NaN above them all
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < cols; i += 256) m = max(m, __float_as_uint(Row<T>::f(xr[i])) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = max(max(red[0], red[1]), max(red[2], red[3]));
+  const bool fin = m < 0x7F800000u;
+  const float s = fin ? __uint_as_float(m) / 127.f : __builtin_nanf("");
+  if (threadIdx.x == 0) scale[r] = s;
+  const float inv = s > 0.f ? 1.f / s : 0.f;
+  const bool wide = inv < 3e38f;    // a subnormal scale: its reciprocal may overflow
+  for (int64_t i = threadIdx.x; i < ldq; i += 256) {
+    int v = 0;
+    if (i < cols && s > 0.f) {
+      const float xv = Row<T>::f(xr[i]);
+      v = wide ? quant1(xv, s, inv)
+               : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)xv / (double)s), -127.0), 127.0);
+    }
+    q[r * ldq + i] = (int8_t)v;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gu,
+                                                  int inter, int ip, uint16_t* d) {
+  const int64_t r = blockIdx.x;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < ip; i += gridDim.y * 256) {
+    float dg = 0.f, du = 0.f;
+    if (i < inter) {
+      const float e = from16_rt(dh[r * lddh + i], dt);
+      const float g = from16_rt(gu[r * 2 * inter + i], dt);
+      const float u = from16_rt(gu[r * 2 * inter + inter + i], dt);
+      float v, dv;
+      act_grad_f(g, act, &v, &dv);
+      dg = e * u * dv;
+      du = e * v;
+    }
+    d[r * 2 * ip + i] = to16_rt(dg, dt);
+    d[r * 2 * ip + ip + i] = to16_rt(du, dt);
+  }
+}
+
+// --------------------------------------------------------------- launchers
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
+  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS> K;
+  constexpr int lds = NS * K::STAGE;
+  constexpr int OP = EPI == EPI_GLU ? BP / 2 : BP;
+  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, NS>;
+  const int64_t tiles = (int64_t)((a.np + OP - 1) / OP) * ((a.nq + BQ - 1) / BQ);
+  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (lds > 65536) {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, dim3((uint32_t)tiles, a.splits), dim3(WP * WQ * 64), lds, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((k_dense_join<T, EPI>), dim3((a.np + 1023) / 1024, a.nq), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// tiles: 0 large (256 x 256), 1 medium (128 x 128), 2 small (64 x 64)
+template <int T, int EPI, int FORM>
+static hipError_t launch_form(int tile, const DenseArgs& a, hipStream_t s) {
+  switch (tile) {
+    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 2>(a, s);
+    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 2>(a, s);
+    case 2:
+      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 4>(a, s);
+      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 4>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a, hipStream_t s) {
+  if (form == FORM_NT && epi == EPI_GLU) {
+    if (dt == DT_BF16) return launch_form<DT_BF16, EPI_GLU, FORM_NT>(tile, a, s);
+    if (dt == DT_F16) return launch_form<DT_F16, EPI_GLU, FORM_NT>(tile, a, s);
+    if (dt == DT_I8) return launch_form<DT_I8, EPI_GLU, FORM_NT>(tile, a, s);
+  }
+  if (form == FORM_NT && epi == EPI_SCALE && dt == DT_I8) return launch_form<DT_I8, EPI_SCALE, FORM_NT>(tile, a, s);
+  if (epi == EPI_OUT) {
+    if (dt == DT_BF16 && form == FORM_NN) return launch_form<DT_BF16, EPI_OUT, FORM_NN>(tile, a, s);
+    if (dt == DT_F16 && form == FORM_NN) return launch_form<DT_F16, EPI_OUT, FORM_NN>(tile, a, s);
+    if (dt == DT_BF16 && form == FORM_TN) return launch_form<DT_BF16, EPI_OUT, FORM_TN>(tile, a, s);
+    if (dt == DT_F16 && form == FORM_TN) return launch_form<DT_F16, EPI_OUT, FORM_TN>(tile, a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_dense_decode(int dt, int epi, const DenseDecodeArgs& a, hipStream_t s) {
+  const int op = epi == EPI_GLU ? 8 : 16;
+  const dim3 grid((a.d.np + op - 1) / op), block(1024);
+  if (epi == EPI_GLU && dt == DT_BF16) hipLaunchKernelGGL((k_dense_decode<DT_BF16, EPI_GLU>), grid, block, 0, s, a);
+  else if (epi == EPI_GLU && dt == DT_F16) hipLaunchKernelGGL((k_dense_decode<DT_F16, EPI_GLU>), grid, block, 0, s, a);
+  else if (epi == EPI_GLU && dt == DT_I8) hipLaunchKernelGGL((k_dense_decode<DT_I8, EPI_GLU>), grid, block, 0, s, a);
+  else if (epi == EPI_SCALE && dt == DT_I8)
+    hipLaunchKernelGGL((k_dense_decode<DT_I8, EPI_SCALE>), grid, block, 0, s, a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,
+                            hipStream_t s) {
+  if (esize == 1)
+    hipLaunchKernelGGL((k_dense_pad<uint8_t>), dim3(rows), dim3(256), 0, s, static_cast<const uint8_t*>(src), ld, cols,
+                       static_cast<uint8_t*>(dst), ldd);
+  else
+    hipLaunchKernelGGL((k_dense_pad<uint16_t>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(src), ld,
+                       cols, static_cast<uint16_t*>(dst), ldd);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
+                             float* scale, hipStream_t s) {
+  if (dt == DT_BF16)
+    hipLaunchKernelGGL((k_quant_rows<DT_BF16>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(x), ldx, cols,
+                       q, ldq, scale);
+  else if (dt == DT_F16)
+    hipLaunchKernelGGL((k_quant_rows<DT_F16>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(x), ldx, cols,
+                       q, ldq, scale);
+  else if (dt == DT_F32)
+    hipLaunchKernelGGL((k_quant_rows<DT_F32>), dim3(rows), dim3(256), 0, s, static_cast<const float*>(x), ldx, cols, q,
+                       ldq, scale);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const void* gu, int rows, int inter,
+                           int ip, void* d, hipStream_t s) {
+  hipLaunchKernelGGL(k_glu_grad, dim3(rows, std::min((ip + 255) / 256, 1024)), dim3(256), 0, s, dt, act,
+                     static_cast<const uint16_t*>(dh), lddh, static_cast<const uint16_t*>(gu), inter, ip,
+                     static_cast<uint16_t*>(d));
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,445 @@
+// C entry points of the dense feed-forward operators: argument validation,
+// workspace layout, tile choice, then the kernel launches.
+#include <algorithm>
+#include <string>
+
+#include <hip/hip_runtime.h>
+
+#include "dense_launch.h"
+#include "moe_host.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kDecodeRows = 16;          // rows the decode form takes
+constexpr int kMaxDim = 65536;           // hidden, inter, out: int32 sums of 127^2 stay below 2^31
+constexpr int kMaxRows = 1 << 20;
+constexpr int64_t kMaxLd = 1 << 22;      // 255 rows of 16-bit elements stay below 2^32 bytes
+
+int bad(const std::string& m, int st = MOE_EINVAL) {
+  set_error(m);
+  return st;
+}
+int hip_bad(const char* what, hipError_t e) {
+  return bad(std::string(what) + ": " + hipGetErrorName(e) + " (" + hipGetErrorString(e) + ")", MOE_EHIP);
+}
+
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+int check_dim(const char* fn, const char* name, int64_t v, int64_t hi) {
+  if (v >= 1 && v <= hi) return MOE_OK;
+  return bad(std::string(fn) + ": " + name + "=" + std::to_string(v) + " outside 1.." + std::to_string(hi));
+}
+int check_ld(const char* fn, const char* name, int64_t ld, int64_t cols) {
+  if (ld >= cols && ld <= kMaxLd) return MOE_OK;
+  return bad(std::string(fn) + ": " + name + "=" + std::to_string(ld) + " outside " + std::to_string(cols) + ".." +
+             std::to_string(kMaxLd), MOE_ESHAPE);
+}
+int check_dtype(const char* fn, int dt) {
+  if (dt == MOE_BF16 || dt == MOE_FP16) return MOE_OK;
+  return bad(std::string(fn) + ": dtype " + std::to_string(dt) + " is not MOE_BF16 or MOE_FP16", MOE_EUNSUPPORTED);
+}
+
+// Rows the tile kernels read as they are: 16-byte aligned, whole 16-byte
+// chunks. Others are copied to zero-padded rows in the workspace first.
+bool plain_rows(const void* p, int64_t ld, int64_t cols, int es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && cols * es % 16 == 0;
+}
+
+struct Bump {
+  uint64_t at = 0;
+  uint64_t take(uint64_t bytes) {
+    const uint64_t o = at;
+    at = align256(at + bytes);
+    return o;
+  }
+};
+
+// K steps (128 bytes) of a contiguous contraction
+int steps_of(int64_t kbytes) { return (int)((kbytes + 127) / 128); }
+
+uint64_t part_bytes(int splits, int64_t nq, int64_t pcols) {
+  return splits > 1 ? (uint64_t)splits * nq * pcols * 4 : 0;
+}
+
+struct GluPlan {
+  bool decode, pad_x, pad_g, pad_u, quant;
+  int64_t kp;             // padded row length (elements)
+  int tile, splits;
+  uint64_t x_off, g_off, u_off, sx_off, part_off, total;
+};
+
+GluPlan plan_forward(const moe_glu* a, int dt) {
+  GluPlan p{};
+  const int es = dt == DT_I8 ? 1 : 2;
+  p.quant = dt == DT_I8 && !a->s_x;
+  p.decode = a->rows <= kDecodeRows;
+  p.kp = up(a->hidden, 16 / es);
+  Bump b;
+  p.pad_x = !p.quant && !p.decode && !plain_rows(a->x, a->ldx, a->hidden, es);
+  p.pad_g = !p.decode && !plain_rows(a->w_gate, a->ldw_gate, a->hidden, es);
+  p.pad_u = !p.decode && !plain_rows(a->w_up, a->ldw_up, a->hidden, es);
+  if (p.quant || p.pad_x) p.x_off = b.take((uint64_t)a->rows * p.kp * es);
+  if (p.quant) p.sx_off = b.take((uint64_t)a->rows * 4);
+  if (p.pad_g) p.g_off = b.take((uint64_t)a->inter * p.kp * es);
+  if (p.pad_u) p.u_off = b.take((uint64_t)a->inter * p.kp * es);
+  p.splits = 1;
+  if (!p.decode) {
+    p.tile = dense_tile(dt, EPI_GLU, FORM_NT, a->inter, a->rows, steps_of(p.kp * es), &p.splits);
+    p.part_off = b.take(part_bytes(p.splits, a->rows, 2 * up(a->inter, 4)));
+  }
+  p.total = b.at;
+  return p;
+}
+
+struct GradPlan {
+  bool pad_x, pad_g, pad_u;
+  int64_t kp, ip;
+  int tile_x, splits_x, tile_w, splits_w;
+  uint64_t d_off, x_off, g_off, u_off, part_off, total;
+};
+
+GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
+  GradPlan p{};
+  p.kp = up(a->hidden, 8);
+  p.ip = up(a->inter, 64);
+  Bump b;
+  p.d_off = b.take((uint64_t)a->rows * 2 * p.ip * 2);
+  p.pad_x = dw && !plain_rows(a->x, a->ldx, a->hidden, 2);
+  p.pad_g = dx && !plain_rows(a->w_gate, a->ldw_gate, a->hidden, 2);
+  p.pad_u = dx && !plain_rows(a->w_up, a->ldw_up, a->hidden, 2);
+  if (p.pad_x) p.x_off = b.take((uint64_t)a->rows * p.kp * 2);
+  if (p.pad_g) p.g_off = b.take((uint64_t)a->inter * p.kp * 2);
+  if (p.pad_u) p.u_off = b.take((uint64_t)a->inter * p.kp * 2);
+  p.splits_x = p.splits_w = 1;
+  uint64_t part = 0;
+  if (dx) {
+    p.tile_x = dense_tile(a->dtype, EPI_OUT, FORM_NN, a->hidden, a->rows, (int)(2 * p.ip / 64), &p.splits_x);
+    part = std::max(part, part_bytes(p.splits_x, a->rows, up(a->hidden, 4)));
+  }
+  if (dw) {
+    p.tile_w = dense_tile(a->dtype, EPI_OUT, FORM_TN, a->hidden, (int)(2 * p.ip), (a->rows + 63) / 64, &p.splits_w);
+    part = std::max(part, part_bytes(p.splits_w, 2 * p.ip, up(a->hidden, 4)));
+  }
+  p.part_off = b.take(part);
+  p.total = b.at;
+  return p;
+}
+
+int check_glu(const char* fn, const moe_glu* a, bool i8) {
+  if (!a) return bad(std::string(fn) + ": NULL argument block");
+  int st;
+  if ((st = check_dim(fn, "rows", a->rows, kMaxRows)) || (st = check_dim(fn, "hidden", a->hidden, kMaxDim)) ||
+      (st = check_dim(fn, "inter", a->inter, kMaxDim)) || (st = check_dtype(fn, a->dtype)))
+    return st;
+  if (a->act != MOE_ACT_SILU && a->act != MOE_ACT_GELU_TANH)
+    return bad(std::string(fn) + ": act " + std::to_string(a->act) + " is not MOE_ACT_SILU or MOE_ACT_GELU_TANH",
+               MOE_EUNSUPPORTED);
+  if (!a->x || !a->w_gate || !a->w_up) return bad(std::string(fn) + ": NULL x/w_gate/w_up");
+  if (i8 && (!a->s_gate || !a->s_up)) return bad(std::string(fn) + ": NULL s_gate/s_up");
+  if (!i8 && (a->s_gate || a->s_up || a->s_x))
+    return bad(std::string(fn) + ": scales given to the 16-bit form (moe_glu_i8 takes them)");
+  if ((st = check_ld(fn, "ldx", a->ldx, a->hidden)) || (st = check_ld(fn, "ldw_gate", a->ldw_gate, a->hidden)) ||
+      (st = check_ld(fn, "ldw_up", a->ldw_up, a->hidden)))
+    return st;
+  return MOE_OK;
+}
+
+int check_ws(const char* fn, const void* ws, uint64_t have, uint64_t need) {
+  if (!need) return MOE_OK;
+  if (!ws) return bad(std::string(fn) + ": NULL ws");
+  if (reinterpret_cast<uintptr_t>(ws) % 256) return bad(std::string(fn) + ": ws is not 256-byte aligned");
+  if (have < need)
+    return bad(std::string(fn) + ": workspace of " + std::to_string(have) + " bytes, needs " + std::to_string(need),
+               MOE_ENOSPACE);
+  return MOE_OK;
+}
+
+// Copies rows to the workspace where the plan says so; the operand as the
+// tile kernels read it.
+struct Rows {
+  const uint8_t* p;
+  int64_t ld;   // bytes
+};
+hipError_t padded(bool pad, const void* src, int64_t ld, int rows, int cols, int es, uint8_t* dst, int64_t kp,
+                  hipStream_t s, Rows* out) {
+  if (!pad) {
+    *out = {static_cast<const uint8_t*>(src), ld * es};
+    return hipSuccess;
+  }
+  *out = {dst, kp * es};
+  return launch_dense_pad(src, ld, rows, cols, es, dst, kp, s);
+}
+
+int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes,
+            void* stream) {
+  if (!h) return bad(std::string(fn) + ": NULL h");
+  int st = check_ld(fn, "ldh", ldh, a->inter);
+  if (st) return st;
+  const GluPlan p = plan_forward(a, dt);
+  if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int es = dt == DT_I8 ? 1 : 2;
+  Rows x, g, u;
+  hipError_t e;
+  if (p.quant) {
+    e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->hidden, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
+                          reinterpret_cast<float*>(w + p.sx_off), s);
+    x = {w + p.x_off, p.kp};
+  } else {
+    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, es, w + p.x_off, p.kp, s, &x);
+  }
+  if (e == hipSuccess) e = padded(p.pad_g, a->w_gate, a->ldw_gate, a->inter, a->hidden, es, w + p.g_off, p.kp, s, &g);
+  if (e == hipSuccess) e = padded(p.pad_u, a->w_up, a->ldw_up, a->inter, a->hidden, es, w + p.u_off, p.kp, s, &u);
+  if (e != hipSuccess) return hip_bad(fn, e);
+  DenseArgs d{};
+  d.p0 = g.p;
+  d.p1 = u.p;
+  d.q0 = x.p;
+  d.ldp0 = g.ld;
+  d.ldp1 = u.ld;
+  d.ldq = x.ld;
+  d.np = a->inter;
+  d.nq = a->rows;
+  d.kbytes = (int)(p.kp * es);
+  d.steps = d.seg = steps_of(p.kp * es);
+  d.splits = p.splits;
+  d.act = a->act;
+  d.out0 = h;
+  d.ldo = ldh;
+  d.out_dt = a->dtype;
+  d.save = gu;
+  if (dt == DT_I8) {
+    d.sq = p.quant ? reinterpret_cast<const float*>(w + p.sx_off) : a->s_x;
+    d.sp0 = a->s_gate;
+    d.sp1 = a->s_up;
+  }
+  d.part = reinterpret_cast<float*>(w + p.part_off);
+  d.pcols = 2 * up(a->inter, 4);
+  if (p.decode) e = launch_dense_decode(dt, EPI_GLU, DenseDecodeArgs{d, a->hidden}, s);
+  else e = launch_dense(dt, EPI_GLU, FORM_NT, p.tile, d, s);
+  return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
+}
+
+struct LinPlan {
+  bool decode, pad_x, pad_w, quant;
+  int64_t kp;
+  int tile, splits;
+  uint64_t x_off, sx_off, w_off, part_off, total;
+};
+
+LinPlan plan_linear(const moe_linear* a) {
+  LinPlan p{};
+  p.quant = !a->s_x;
+  p.decode = a->rows <= kDecodeRows;
+  p.kp = up(a->in, 16);
+  Bump b;
+  p.pad_x = !p.quant && !p.decode && !plain_rows(a->x, a->ldx, a->in, 1);
+  p.pad_w = !p.decode && !plain_rows(a->w, a->ldw, a->in, 1);
+  if (p.quant || p.pad_x) p.x_off = b.take((uint64_t)a->rows * p.kp);
+  if (p.quant) p.sx_off = b.take((uint64_t)a->rows * 4);
+  if (p.pad_w) p.w_off = b.take((uint64_t)a->out * p.kp);
+  p.splits = 1;
+  if (!p.decode) {
+    p.tile = dense_tile(DT_I8, EPI_SCALE, FORM_NT, a->out, a->rows, steps_of(p.kp), &p.splits);
+    p.part_off = b.take(part_bytes(p.splits, a->rows, up(a->out, 4)));
+  }
+  p.total = b.at;
+  return p;
+}
+
+int check_linear(const char* fn, const moe_linear* a) {
+  if (!a) return bad(std::string(fn) + ": NULL argument block");
+  int st;
+  if ((st = check_dim(fn, "rows", a->rows, kMaxRows)) || (st = check_dim(fn, "in", a->in, kMaxDim)) ||
+      (st = check_dim(fn, "out", a->out, kMaxDim)) || (st = check_dtype(fn, a->dtype)))
+    return st;
+  if (!a->x || !a->w || !a->s_w) return bad(std::string(fn) + ": NULL x/w/s_w");
+  if ((st = check_ld(fn, "ldx", a->ldx, a->in)) || (st = check_ld(fn, "ldw", a->ldw, a->in))) return st;
+  return MOE_OK;
+}
+
+}  // namespace
+
+// Tile (0: 256 x 256, 1: 128 x 128, 2: 64 x 64) and K ranges of a product:
+// the largest tile whose workgroups fill the 256 CUs, else the small one
+// with the contraction cut until they do (at least 8 steps a range).
+int moe::dense_tile(int dt, int epi, int form, int np, int nq, int steps, int* splits) {
+  (void)dt;
+  (void)form;
+  auto count = [&](int bp, int bq) {
+    const int op = epi == EPI_GLU ? bp / 2 : bp;
+    return (int64_t)((np + op - 1) / op) * ((nq + bq - 1) / bq);
+  };
+  *splits = 1;
+  if (count(256, 256) >= 200) return 0;
+  if (count(128, 128) >= 200) return 1;
+  const int64_t n = count(64, 64);
+  if (nq <= 32768) *splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / n, steps / 8));
+  return 2;
+}
+
+extern "C" {
+
+int moe_glu_workspace_size(const moe_glu* a, int kind, uint64_t* bytes) {
+  const char* fn = "moe_glu_workspace_size";
+  if (!bytes) return bad(std::string(fn) + ": NULL bytes");
+  if (kind < MOE_GLU_FORWARD || kind > MOE_GLU_I8)
+    return bad(std::string(fn) + ": kind " + std::to_string(kind) +
+               " is not MOE_GLU_FORWARD, MOE_GLU_BACKWARD or MOE_GLU_I8");
+  int st = check_glu(fn, a, kind == MOE_GLU_I8);
+  if (st) return st;
+  *bytes = kind == MOE_GLU_BACKWARD ? plan_backward(a, true, true).total
+                                    : plan_forward(a, kind == MOE_GLU_I8 ? DT_I8 : a->dtype).total;
+  return MOE_OK;
+}
+
+int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes, void* stream) {
+  int st = check_glu("moe_glu_forward", a, false);
+  return st ? st : glu_run("moe_glu_forward", a, a->dtype, h, ldh, gu, ws, ws_bytes, stream);
+}
+
+int moe_glu_i8(const moe_glu* a, void* h, int64_t ldh, void* ws, uint64_t ws_bytes, void* stream) {
+  int st = check_glu("moe_glu_i8", a, true);
+  return st ? st : glu_run("moe_glu_i8", a, DT_I8, h, ldh, nullptr, ws, ws_bytes, stream);
+}
+
+int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+                     void* dw_gate, void* dw_up, void* ws, uint64_t ws_bytes, void* stream) {
+  const char* fn = "moe_glu_backward";
+  int st = check_glu(fn, a, false);
+  if (st) return st;
+  if (!gu || !dh) return bad(std::string(fn) + ": NULL gu/dh");
+  if (!dw_gate != !dw_up) return bad(std::string(fn) + ": dw_gate and dw_up are both given or both NULL");
+  if (!dx && !dw_gate) return bad(std::string(fn) + ": no gradient asked for (dx and dw_gate/dw_up are NULL)");
+  if ((st = check_ld(fn, "lddh", lddh, a->inter)) || (dx && (st = check_ld(fn, "lddx", lddx, a->hidden)))) return st;
+  const GradPlan p = plan_backward(a, dx != nullptr, dw_gate != nullptr);
+  if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_glu_grad(a->dtype, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off, s);
+  if (e != hipSuccess) return hip_bad(fn, e);
+  DenseArgs d{};
+  d.q0 = w + p.d_off;
+  d.ldq = 2 * p.ip * 2;
+  d.np = a->hidden;
+  d.out_dt = a->dtype;
+  d.part = reinterpret_cast<float*>(w + p.part_off);
+  d.pcols = up(a->hidden, 4);
+  if (dx) {
+    // dx[r] = sum_i dg[r, i] Wg[i] + du[r, i] Wu[i]: both sums one contraction
+    Rows g, u;
+    e = padded(p.pad_g, a->w_gate, a->ldw_gate, a->inter, a->hidden, 2, w + p.g_off, p.kp, s, &g);
+    if (e == hipSuccess) e = padded(p.pad_u, a->w_up, a->ldw_up, a->inter, a->hidden, 2, w + p.u_off, p.kp, s, &u);
+    if (e != hipSuccess) return hip_bad(fn, e);
+    DenseArgs dd = d;
+    dd.p0 = g.p;
+    dd.p1 = u.p;
+    dd.ldp0 = g.ld;
+    dd.ldp1 = u.ld;
+    dd.nq = a->rows;
+    dd.kbytes = (int)(2 * p.ip * 2);
+    dd.krows = a->inter;
+    dd.steps = (int)(2 * p.ip / 64);
+    dd.seg = (int)(p.ip / 64);
+    dd.splits = p.splits_x;
+    dd.out0 = dx;
+    dd.ldo = lddx;
+    e = launch_dense(a->dtype, EPI_OUT, FORM_NN, p.tile_x, dd, s);
+    if (e != hipSuccess) return hip_bad(fn, e);
+  }
+  if (dw_gate) {
+    // [dWg; dWu] = D^T x
+    Rows x;
+    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, 2, w + p.x_off, p.kp, s, &x);
+    if (e != hipSuccess) return hip_bad(fn, e);
+    DenseArgs dd = d;
+    dd.p0 = x.p;
+    dd.ldp0 = x.ld;
+    dd.nq = (int)(2 * p.ip);
+    dd.krows = a->rows;
+    dd.steps = dd.seg = (a->rows + 63) / 64;
+    dd.splits = p.splits_w;
+    dd.out0 = dw_gate;
+    dd.out1 = dw_up;
+    dd.ldo = a->hidden;
+    dd.qseg = a->inter;
+    dd.qpad = (int)p.ip;
+    e = launch_dense(a->dtype, EPI_OUT, FORM_TN, p.tile_w, dd, s);
+    if (e != hipSuccess) return hip_bad(fn, e);
+  }
+  return MOE_OK;
+}
+
+int moe_quant_rows(const void* x, int dtype, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                   void* stream) {
+  const char* fn = "moe_quant_rows";
+  if (!x || !q || !scale) return bad(std::string(fn) + ": NULL x/q/scale");
+  if (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32)
+    return bad(std::string(fn) + ": dtype " + std::to_string(dtype) + " is not MOE_BF16, MOE_FP16 or MOE_FP32",
+               MOE_EUNSUPPORTED);
+  int st;
+  if ((st = check_dim(fn, "rows", rows, kMaxRows)) || (st = check_dim(fn, "cols", cols, kMaxDim)) ||
+      (st = check_ld(fn, "ldx", ldx, cols)) || (st = check_ld(fn, "ldq", ldq, cols)))
+    return st;
+  hipError_t e = launch_quant_rows(dtype == MOE_FP32 ? DT_F32 : dtype, x, ldx, rows, cols, q, ldq, scale,
+                                   static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
+}
+
+int moe_linear_i8_workspace_size(const moe_linear* a, uint64_t* bytes) {
+  const char* fn = "moe_linear_i8_workspace_size";
+  if (!bytes) return bad(std::string(fn) + ": NULL bytes");
+  int st = check_linear(fn, a);
+  if (st) return st;
+  *bytes = plan_linear(a).total;
+  return MOE_OK;
+}
+
+int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t ws_bytes, void* stream) {
+  const char* fn = "moe_linear_i8";
+  int st = check_linear(fn, a);
+  if (st) return st;
+  if (!y) return bad(std::string(fn) + ": NULL y");
+  if ((st = check_ld(fn, "ldy", ldy, a->out))) return st;
+  const LinPlan p = plan_linear(a);
+  if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  Rows x, m;
+  hipError_t e;
+  if (p.quant) {
+    e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->in, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
+                          reinterpret_cast<float*>(w + p.sx_off), s);
+    x = {w + p.x_off, p.kp};
+  } else {
+    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->in, 1, w + p.x_off, p.kp, s, &x);
+  }
+  if (e == hipSuccess) e = padded(p.pad_w, a->w, a->ldw, a->out, a->in, 1, w + p.w_off, p.kp, s, &m);
+  if (e != hipSuccess) return hip_bad(fn, e);
+  DenseArgs d{};
+  d.p0 = m.p;
+  d.q0 = x.p;
+  d.ldp0 = m.ld;
+  d.ldq = x.ld;
+  d.np = a->out;
+  d.nq = a->rows;
+  d.kbytes = (int)p.kp;
+  d.steps = d.seg = steps_of(p.kp);
+  d.splits = p.splits;
+  d.out0 = y;
+  d.ldo = ldy;
+  d.out_dt = a->dtype;
+  d.sq = p.quant ? reinterpret_cast<const float*>(w + p.sx_off) : a->s_x;
+  d.sp0 = a->s_w;
+  d.bias = a->bias;
+  d.part = reinterpret_cast<float*>(w + p.part_off);
+  d.pcols = up(a->out, 4);
+  if (p.decode) e = launch_dense_decode(DT_I8, EPI_SCALE, DenseDecodeArgs{d, a->in}, s);
+  else e = launch_dense(DT_I8, EPI_SCALE, FORM_NT, p.tile, d, s);
+  return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
+}
+
+}  // extern "C"

@@ -1,0 +1,69 @@
+// Argument blocks and launchers of the dense feed-forward operators
+// (internal to the library).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+enum { DT_BF16 = 0, DT_F16 = 1, DT_I8 = 2, DT_F32 = 3 };   // element types
+enum { ACT_SILU = 0, ACT_GELU_TANH = 1 };
+// What a product does with its sums: store them (OUT), scale and add the
+// bias first (SCALE, 8-bit operands), gate them (GLU)
+enum { EPI_OUT = 0, EPI_SCALE = 1, EPI_GLU = 2 };
+// Operand forms: NT both with the contraction contiguous; NN the P operand
+// with it as the row index; TN both
+enum { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };
+
+// One product out[q, p] = sum_k Q[q, k] P[p, k]. P is the operand whose
+// index runs along the output's rows of memory (weights, or x for the weight
+// gradients), Q the other one. Every operand row starts at a 16-byte
+// boundary and is 16-byte granular (the padding zero along k).
+struct DenseArgs {
+  const uint8_t* p0;      // NT: P rows (GLU: gate rows); NN/TN: rows of k
+  const uint8_t* p1;      // GLU: up rows; NN: rows of the second segment
+  const uint8_t* q0;
+  int64_t ldp0, ldp1, ldq;   // bytes
+  int np, nq;             // output columns and rows (GLU: np of gate and of up)
+  int kbytes;             // NT / NN: bytes of a k-contiguous row in use (multiple of 16)
+  int krows;              // NN: k rows of one segment in use; TN: k rows
+  int steps;              // K steps in all
+  int seg;                // NN: K steps of the first segment (steps when single)
+  int splits;             // K ranges (1: the epilogue runs in the product)
+  int act;
+  // outputs
+  void* out0;             // [nq, np] (weight gradients: rows below qseg)
+  void* out1;             // weight gradients: rows from qpad on
+  int64_t ldo;            // elements
+  int out_dt;             // DT_BF16 / DT_F16 / DT_F32
+  int qseg, qpad;         // rows of out0, first row index of out1 (0: one output)
+  void* save;             // GLU: [nq, 2 np] pre-activations, or null
+  const float* sq;        // 8-bit: scale of each Q row
+  const float* sp0;       // 8-bit: scale of each P row (GLU: gate)
+  const float* sp1;       // 8-bit GLU: up
+  const float* bias;      // SCALE: [np] or null
+  float* part;            // splits > 1: [splits, nq, pcols] sums (int32 for 8-bit)
+  int64_t pcols;
+};
+
+// Decode rows (nq <= 16), any alignment: K elements per row.
+struct DenseDecodeArgs {
+  DenseArgs d;
+  int k;
+};
+
+int dense_tile(int dt, int epi, int form, int np, int nq, int steps, int* splits);
+hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a, hipStream_t s);
+hipError_t launch_dense_decode(int dt, int epi, const DenseDecodeArgs& a, hipStream_t s);
+// rows of `cols` elements (esize bytes, row stride ld elements) copied to
+// rows of ldd elements, zero behind cols
+hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,
+                            hipStream_t s);
+// q[r, 0..ldq) (zero behind cols), scale[r]
+hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
+                             float* scale, hipStream_t s);
+// D[r] = [dg | du], each ip wide (zero behind inter)
+hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const void* gu, int rows, int inter,
+                           int ip, void* d, hipStream_t s);
+
+}  // namespace moe

@@ -5,6 +5,7 @@
 // the host tests exercise all host code paths without a GPU or GPU code.
 #include <hip/hip_runtime.h>
 
+#include "dense_launch.h"
 #include "moe_host.h"
 #include "moe_launch.h"
 
@@ -16,6 +17,18 @@ hipError_t launch_grouped(int, int, const GroupedArgs&, hipStream_t, hipEvent_t*
 hipError_t launch_grp_sort(const GroupedArgs&, hipStream_t, hipEvent_t*) { return hipErrorNoDevice; }
 hipError_t launch_route_exact(int, int, const RouteArgs&, hipStream_t, hipEvent_t*) { return hipErrorNoDevice; }
 hipError_t launch_exact_experts(int, int, const DecodeArgs&, hipStream_t, hipEvent_t*) { return hipErrorNoDevice; }
+
+hipError_t launch_dense(int, int, int, int, const DenseArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_dense_decode(int, int, const DenseDecodeArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_dense_pad(const void*, int64_t, int, int, int, void*, int64_t, hipStream_t) {
+  return hipErrorNoDevice;
+}
+hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64_t, float*, hipStream_t) {
+  return hipErrorNoDevice;
+}
+hipError_t launch_glu_grad(int, int, const void*, int64_t, const void*, int, int, int, void*, hipStream_t) {
+  return hipErrorNoDevice;
+}
 
 }  // namespace moe
 
