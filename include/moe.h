@@ -390,7 +390,7 @@ enum moe_act { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 };
 enum moe_glu_kind { MOE_GLU_FORWARD = 0, MOE_GLU_BACKWARD = 1, MOE_GLU_I8 = 2 };
 
 /* The gated block h = act(x Wg^T) * (x Wu^T).
- *   dtype   MOE_BF16 or MOE_FP16: x, h, gu, dh and the gradients; the weights
+ *   dtype   MOE_BF16 or MOE_FP16: x, h, dh and the gradients; the weights
  *           of the 16-bit form
  *   w_gate, w_up  [inter, hidden], row strides ldw_gate and ldw_up; int8 for
  *           moe_glu_i8, with s_gate, s_up [inter] fp32 (NULL otherwise)
@@ -416,11 +416,11 @@ typedef struct moe_glu {
 int moe_glu_workspace_size(const moe_glu* a, int kind, uint64_t* bytes);
 
 /* h [rows, inter] (row stride ldh). With gu != NULL also the products before
- * the activation, gu [rows, 2, inter] contiguous (g then u of each row), which
- * moe_glu_backward reads. Sums, activation and product are fp32, rounded once.
+ * the activation, gu fp32 [rows, 2, inter] contiguous (g then u of each row),
+ * which moe_glu_backward reads. Sums, activation and product are fp32, rounded once.
  * Up to 16 rows run in one launch that reads each weight once from memory.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESHAPE, MOE_ENOSPACE, MOE_EHIP. */
-int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes, void* stream);
+int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, float* gu, void* ws, uint64_t ws_bytes, void* stream);
 
 /* Gradients of the block from dh [rows, inter] (row stride lddh) and the gu of
  * the forward call:
@@ -429,7 +429,7 @@ int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, void* gu, void* ws, 
  *   dw_gate = dg^T x, dw_up = du^T x   [inter, hidden] contiguous
  * dx may be NULL, or dw_gate and dw_up both (not wanted, not computed).
  * fp16: dg and du beyond 65504 become infinite, as h does. */
-int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                      void* dw_gate, void* dw_up, void* ws, uint64_t ws_bytes, void* stream);
 
 /* The gated block on 8-bit weights (see moe_glu): int32 sums, exact, times

@@ -513,7 +513,7 @@ def glu_workspace_size(x, w_gate, w_up, kind=MOE_GLU_FORWARD, s_gate=None, s_up=
 
 def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=None, stream=None):
     """moe_glu_forward: h = act(x w_gate^T) * (x w_up^T), [rows, inter] of x's
-    dtype (bf16 or fp16); with save=True (h, gu), gu [rows, 2, inter] being what
+    dtype (bf16 or fp16); with save=True (h, gu), gu fp32 [rows, 2, inter] being what
     glu_backward takes."""
     import torch
     a, dt = _glu_args(x, w_gate, w_up, act)
@@ -523,9 +523,9 @@ def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=Non
             h = torch.empty((R, I), dtype=dt, device=x.device)
         ldh = _rows2d(h, "h", (dt,), (R, I), x)
         if save and gu is None:
-            gu = torch.empty((R, 2, I), dtype=dt, device=x.device)
+            gu = torch.empty((R, 2, I), dtype=torch.float32, device=x.device)
         if gu is not None:
-            _gu_ok(gu, R, I, dt, x)
+            _gu_ok(gu, R, I, x)
         n = C.c_uint64()
         _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_FORWARD, C.byref(n)), "moe_glu_workspace_size")
         wp, wn, ws = _ws_for(n.value, ws, x)
@@ -534,9 +534,10 @@ def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=Non
     return (h, gu) if gu is not None else h
 
 
-def _gu_ok(gu, R, I, dt, x):
-    if gu.dtype != dt or tuple(gu.shape) != (R, 2, I) or not gu.is_contiguous():
-        raise MoeError(f"gu: {gu.dtype} of shape {tuple(gu.shape)}, needs contiguous {dt} ({R}, 2, {I})")
+def _gu_ok(gu, R, I, x):
+    import torch
+    if gu.dtype != torch.float32 or tuple(gu.shape) != (R, 2, I) or not gu.is_contiguous():
+        raise MoeError(f"gu: {gu.dtype} of shape {tuple(gu.shape)}, needs contiguous torch.float32 ({R}, 2, {I})")
     _same_device(gu, "gu", x)
 
 
@@ -547,7 +548,7 @@ def glu_backward(dh, x, w_gate, w_up, gu, act="silu", need_dx=True, need_dw=True
     import torch
     a, dt = _glu_args(x, w_gate, w_up, act)
     R, H, I = a.rows, a.hidden, a.inter
-    _gu_ok(gu, R, I, dt, x)
+    _gu_ok(gu, R, I, x)
     lddh = _rows2d(dh, "dh", (dt,), (R, I), x)
     if not need_dx and not need_dw:
         raise MoeError("glu_backward: neither need_dx nor need_dw")

@@ -4,6 +4,7 @@
 #include "dense_launch.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
@@ -66,7 +67,8 @@ template <> struct Elem<DT_I8> {
 // silu(g) = g s(g); gelu_tanh(g) = g s(w(g)) with w = 2 sqrt(2/pi) (g +
 // 0.044715 g^3), since (1 + tanh(w/2)) / 2 = s(w): one sigmoid for both.
 constexpr float GELU_C = 1.5957691216057308f;
-__device__ __forceinline__ float sigmoid_f(float w) { return 1.f / (1.f + __expf(-w)); }
+// v_rcp_f32 is good to one ulp; 1 + e^-w = inf gives 0
+__device__ __forceinline__ float sigmoid_f(float w) { return __builtin_amdgcn_rcpf(1.f + __expf(-w)); }
 __device__ __forceinline__ float act_f(float g, int act) {
   const float w = act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
   return g * sigmoid_f(w);
@@ -115,10 +117,8 @@ __device__ __forceinline__ void store4(void* row, int p, int np, int dt, bool ve
 }
 // row q of the product's output, or null when q is padding between the two
 __device__ __forceinline__ char* out_row(const DenseArgs& a, int q) {
-  const int64_t es = a.out_dt == DT_F32 ? 4 : 2;
-  if (!a.qpad) return static_cast<char*>(a.out0) + q * a.ldo * es;
-  if (q < a.qseg) return static_cast<char*>(a.out0) + q * a.ldo * es;
-  if (q >= a.qpad && q < a.qpad + a.qseg) return static_cast<char*>(a.out1) + (q - a.qpad) * a.ldo * es;
+  if (!a.qpad || q < a.qseg) return static_cast<char*>(a.out0) + q * a.ldo * 2;
+  if (q >= a.qpad && q < a.qpad + a.qseg) return static_cast<char*>(a.out1) + (q - a.qpad) * a.ldo * 2;
   return nullptr;
 }
 __device__ __forceinline__ bool vec_ok(const void* p, int64_t ld, int es) {
@@ -146,10 +146,10 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
       v[i] = act_f(g[i], a.act) * u[i];
     }
     if (a.save) {
-      uint16_t* sv = static_cast<uint16_t*>(a.save) + (int64_t)q * 2 * a.np;
-      const bool vec = a.np % 4 == 0 && (uintptr_t)a.save % 8 == 0;
-      store4(sv, p, a.np, a.out_dt, vec, g);
-      store4(sv + a.np, p, a.np, a.out_dt, vec, u);
+      float* sv = static_cast<float*>(a.save) + (int64_t)q * 2 * a.np;
+      const bool vec = vec_ok(a.save, a.np, 4);
+      store4(sv, p, a.np, DT_F32, vec, g);
+      store4(sv + a.np, p, a.np, DT_F32, vec, u);
     }
   } else if constexpr (EPI == EPI_SCALE) {
     const float sq = a.sq[q];
@@ -163,13 +163,17 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
     for (int i = 0; i < 4; ++i) v[i] = s0[i];
   }
   char* row = out_row(a, q);
-  if (row) store4(row, p, a.np, a.out_dt, vec_ok(a.out0, a.ldo, a.out_dt == DT_F32 ? 4 : 2) &&
-                  (!a.qpad || vec_ok(a.out1, a.ldo, a.out_dt == DT_F32 ? 4 : 2)), v);
+  if (row) store4(row, p, a.np, a.out_dt, vec_ok(a.out0, a.ldo, 2) && (!a.qpad || vec_ok(a.out1, a.ldo, 2)), v);
 }
 
 // ------------------------------------------------------- loads into the ring
 // 64 x 16 bytes from base + off (a lane's own) to LDS [lds, lds + 1024). The
 // compiler does not see it, so a read of the ring is ordered by step_wait.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const uint8_t* base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
 }
@@ -187,49 +191,57 @@ template <int N> __device__ __forceinline__ void step_wait() {
 __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 
 // ---------------------------------------------------------------- the product
-// Workgroup tile BP x BQ, K step 128 bytes (k-contiguous) = 64 k (16-bit).
-// k-contiguous operand in LDS: row r of 128 bytes, its 16-byte chunk c at
-// position c ^ (r & 7). k-major operand: row k of B*2 bytes, its 32-byte
-// segment s at s ^ (k & 3 | (k >> 3 & 1) << 2).
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+// Workgroup tile BP x BQ; a K step is KB bytes of a k-contiguous row (KB / 2
+// k of 16 bits), KB = 128 or 64. k-contiguous operand in LDS: rows of KB
+// bytes, 16-byte chunk c of row r at position c ^ swz_kc(r), so 16 lanes
+// reading one chunk of 16 rows meet 16 different bank groups. k-major
+// operand: rows k of 2 B bytes, 32-byte segment s at s ^ swz_km(k), so the 4
+// rows of a transposed read do.
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
 struct Dense {
   static constexpr bool PKM = FORM != FORM_NT, QKM = FORM == FORM_TN;
   static constexpr int NW = WP * WQ;
   static constexpr int TP = BP / WP, TQ = BQ / WQ, FP = TP / 32, FQ = TQ / 32;
-  static constexpr int PB = BP * 128, QB = BQ * 128, STAGE = PB + QB;
+  static constexpr int PB = BP * KB, QB = BQ * KB, STAGE = PB + QB;
   static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
+  static constexpr int NK = KB / 32;               // matrix-instruction k blocks of a step
+  static constexpr int CPR = KB / 16, KR = KB / 2;  // chunks of a k-contiguous row; k rows of a step
   typedef typename Elem<T>::acc acc_t;
+  static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB, "whole loads");
 
-  // k-major rows: what the segment index is xor-ed with (the same for k and k + 4)
+  static __device__ __forceinline__ int swz_kc(int r) { return KB == 128 ? r & 7 : (r >> 2) & 3; }
+  // the same for k and k + 4
   template <int B> static __device__ __forceinline__ int swz_km(int k) {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
   }
-  // source offset of load i of a lane: k-contiguous rows (row0 + r clamped
-  // below n), GLU rows interleaved 32 gate, 32 up
-  template <bool KM, int B, int L>
-  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld, bool glu) {
+  // whether load i of wave w holds up rows (GLU: rows interleaved 32 gate, 32 up)
+  static __device__ __forceinline__ bool is_up(int i, int w) {
+    return EPI == EPI_GLU && (((i * NW + w) * (64 / CPR)) >> 5 & 1);
+  }
+  // source offset of load i of a lane, k-contiguous rows clamped below n
+  template <bool KM, int B, int L, bool GLU>
+  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld0, int64_t ld1) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      const int seg = i * NW + w;
+      const int q = (i * NW + w) * 64 + lane;
+      const uint32_t ld = (uint32_t)(GLU && is_up(i, w) ? ld1 : ld0);
       if constexpr (!KM) {
-        const int r = seg * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ (r & 7);
-        const int idx = glu ? c0 + (r >> 6) * 32 + (r & 31) : c0 + r;
-        off[i] = (uint32_t)(min(idx, n - 1) - c0) * (uint32_t)ld + c * 16;
+        const int r = q / CPR;
+        const int c = (q % CPR) ^ swz_kc(r);
+        const int idx = GLU ? c0 + (r >> 6) * 32 + (r & 31) : c0 + r;
+        off[i] = (uint32_t)(min(idx, n - 1) - c0) * ld + c * 16;
       } else {
-        constexpr int CPR = B * 2 / 16;                 // chunks per k row
-        const int q = seg * 64 + lane;
-        const int k = q / CPR, pos = q % CPR;
+        constexpr int RC = B * 2 / 16;                 // chunks of a k row
+        const int k = q / RC, pos = q % RC;
         const int s = (pos >> 1) ^ swz_km<B>(k);
         const int col = c0 + (s * 2 + (pos & 1)) * 8;
-        off[i] = (uint32_t)k * (uint32_t)ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
+        off[i] = (uint32_t)k * ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
       }
     }
   }
 
-  // LDS byte address (relative to the operand's tile) of fragment f's lane data at kk (0..3)
   static __device__ __forceinline__ u32x4 frag_kc(const uint8_t* tile, int row, int kk, int half) {
-    return *reinterpret_cast<const u32x4*>(tile + row * 128 + (((kk * 2 + half) ^ (row & 7)) << 4));
+    return *reinterpret_cast<const u32x4*>(tile + row * KB + (((kk * 2 + half) ^ swz_kc(row)) << 4));
   }
   // k-major: the lane's 8 k of column col0 + lane % 32: two 4-row transposed
   // reads; a 16-lane group reads 4 rows of 16 columns, lane i supplying the
@@ -267,75 +279,79 @@ struct Dense {
     const int gh = min(GQ, tq - band * GQ);
     const int iq = band * GQ + inb % gh, ip = inb / gh;
     const int c0p = ip * OP, c0q = iq * BQ;
-    // K steps of this workgroup
+    // K steps that lie whole inside the operands, this workgroup's range of
+    // them, and the masked rest (up to one step a segment), which the last
+    // range takes. NN: two segments of P rows, gate then up.
     const int z = blockIdx.y;
-    const int t0 = (int)((int64_t)a.steps * z / a.splits), t1 = (int)((int64_t)a.steps * (z + 1) / a.splits);
+    const int nws = PKM ? a.krows / KR : a.kbytes / KB;
+    const bool rest = PKM ? a.krows % KR != 0 : a.kbytes % KB != 0;
+    constexpr int NSEG = FORM == FORM_NN ? 2 : 1;
+    const int t0 = (int)((int64_t)NSEG * nws * z / a.splits), t1 = (int)((int64_t)NSEG * nws * (z + 1) / a.splits);
 
     uint32_t offp[LP], offq[LQ];
-    offsets<PKM, BP, LP>(offp, w, lane, c0p, a.np, a.ldp0, EPI == EPI_GLU);
-    offsets<QKM, BQ, LQ>(offq, w, lane, c0q, a.nq, a.ldq, false);
+    offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1);
+    offsets<QKM, BQ, LQ, false>(offq, w, lane, c0q, a.nq, a.ldq, a.ldq);
+    // NN's second segment counts its offsets in its own stride
+    uint32_t offp1[FORM == FORM_NN ? LP : 1];
+    if constexpr (FORM == FORM_NN) offsets<PKM, BP, LP, false>(offp1, w, lane, c0p, a.np, a.ldp1, a.ldp1);
     const uint8_t* pb0 = a.p0 + (PKM ? (int64_t)c0p * 2 : (int64_t)c0p * a.ldp0);
     const uint8_t* pb1 = a.p1 ? a.p1 + (PKM ? (int64_t)c0p * 2 : (int64_t)c0p * a.ldp1) : nullptr;
+    // GLU: the operand each load of this wave reads
+    const uint8_t* pbn[LP];
+#pragma unroll
+    for (int i = 0; i < LP; ++i) pbn[i] = uniform(is_up(i, w) ? pb1 : pb0);
     const uint8_t* qb = a.q0 + (QKM ? (int64_t)c0q * 2 : (int64_t)c0q * a.ldq);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)smem);
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&g_zero16);
 
-    auto issue = [&](int t, int slot) {
-      const uint32_t ldst = lds0 + slot * STAGE;
-      // P
-      if constexpr (!PKM) {
-        const bool full = (t + 1) * 128 <= a.kbytes;
+    // load n of the LP + LQ of a step into its slot: step t of segment sg
+    struct Src {
+      const uint8_t *p, *q;
+      int64_t dp;
+      uint32_t lds;
+      bool second;
+    };
+    auto source_at = [&](int sg, int t, int slot) {
+      Src r;
+      r.lds = lds0 + slot * STAGE + w * 1024;
+      r.second = sg;
+      r.dp = PKM ? (int64_t)t * KR * (sg ? a.ldp1 : a.ldp0) : (int64_t)t * KB;
+      r.p = sg ? pb1 : pb0;
+      r.q = qb + (QKM ? (int64_t)t * KR * a.ldq : (int64_t)t * KB + (sg ? a.segbytes : 0));
+      return r;
+    };
+    auto source = [&](int t, int slot) {
+      const int sg = NSEG == 2 && t >= nws;
+      return source_at(sg, sg ? t - nws : t, slot);
+    };
+    auto base_of = [&](const Src& r, int n) -> const uint8_t* {
+      if (n >= LP) return r.q;
+      return (EPI == EPI_GLU ? pbn[n < LP ? n : 0] : r.p) + r.dp;
+    };
+    auto off_of = [&](const Src& r, int n) {
+      if (n >= LP) return offq[n < LP ? 0 : n - LP];
+      if constexpr (FORM == FORM_NN) return r.second ? offp1[n < LP ? n : 0] : offp[n < LP ? n : 0];
+      else return offp[n < LP ? n : 0];
+    };
+    auto lds_of = [&](const Src& r, int n) { return r.lds + (n < LP ? n * NW * 1024 : PB + (n - LP) * NW * 1024); };
+    auto load1 = [&](const Src& r, int n) { dma16(lds_of(r, n), off_of(r, n), uniform(base_of(r, n))); };
+    auto load = [&](int t, int slot) {
+      const Src r = source(t, slot);
 #pragma unroll
-        for (int i = 0; i < LP; ++i) {
-          const uint32_t l = ldst + (i * NW + w) * 1024;
-          const bool up = EPI == EPI_GLU && (((i * NW + w) >> 2) & 1);
-          const uint8_t* b = (up ? pb1 : pb0) + (int64_t)t * 128;
-          if (full) dma16(l, offp[i], b);
-          else {
-            const int c = (lane & 7) ^ (lane >> 3);
-            dma16_at(l, t * 128 + c * 16 < a.kbytes ? b + offp[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
-          }
-        }
-      } else {
-        const bool second = FORM == FORM_NN && t >= a.seg;
-        const int tt = second ? t - a.seg : t;
-        const uint8_t* b = (second ? pb1 : pb0) + (int64_t)tt * 64 * a.ldp0;
-        const bool full = (tt + 1) * 64 <= a.krows;
+      for (int n = 0; n < LP + LQ; ++n) load1(r, n);
+    };
+    // the step behind segment sg's whole ones, zero past the operands' end
+    auto load_rest = [&](int sg) {
+      const Src r = source_at(sg, nws, 0);
 #pragma unroll
-        for (int i = 0; i < LP; ++i) {
-          const uint32_t l = ldst + (i * NW + w) * 1024;
-          if (full) dma16(l, offp[i], b);
-          else {
-            const int k = ((i * NW + w) * 64 + lane) / (BP * 2 / 16);
-            dma16_at(l, tt * 64 + k < a.krows ? b + offp[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
-          }
-        }
-      }
-      // Q
-      if constexpr (!QKM) {
-        const uint8_t* b = qb + (int64_t)t * 128;
-        const bool full = (t + 1) * 128 <= a.kbytes;
-#pragma unroll
-        for (int i = 0; i < LQ; ++i) {
-          const uint32_t l = ldst + PB + (i * NW + w) * 1024;
-          if (full) dma16(l, offq[i], b);
-          else {
-            const int c = (lane & 7) ^ (lane >> 3);
-            dma16_at(l, t * 128 + c * 16 < a.kbytes ? b + offq[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
-          }
-        }
-      } else {
-        const uint8_t* b = qb + (int64_t)t * 64 * a.ldq;
-        const bool full = (t + 1) * 64 <= a.krows;
-#pragma unroll
-        for (int i = 0; i < LQ; ++i) {
-          const uint32_t l = ldst + PB + (i * NW + w) * 1024;
-          if (full) dma16(l, offq[i], b);
-          else {
-            const int k = ((i * NW + w) * 64 + lane) / (BQ * 2 / 16);
-            dma16_at(l, t * 64 + k < a.krows ? b + offq[i] : reinterpret_cast<const uint8_t*>(&g_zero16));
-          }
-        }
+      for (int n = 0; n < LP + LQ; ++n) {
+        const bool isp = n < LP;
+        const int q = ((isp ? n : n - LP) * NW + w) * 64 + lane;
+        bool in;
+        if (isp ? PKM : QKM) in = q / ((isp ? BP : BQ) * 2 / 16) < a.krows - nws * KR;
+        else in = (sg ? a.segbytes : 0) + nws * KB + (((q % CPR) ^ swz_kc(q / CPR)) * 16) < a.kbytes;
+        dma16_at(lds_of(r, n), in ? base_of(r, n) + off_of(r, n) : zero);
       }
     };
 
@@ -346,98 +362,238 @@ struct Dense {
       for (int j = 0; j < FQ; ++j) acc[i][j] = acc_t{};
 
     const int col = lane & 31, half = lane >> 5;
-    auto compute = [&](int slot) {
+    u32x4 fp[2][FP], fq[2][FQ];
+    auto frags = [&](int buf, int slot, int kk) {
       const uint8_t* pt = smem + slot * STAGE;
       const uint8_t* qt = pt + PB;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        u32x4 fp[FP], fq[FQ];
+      for (int i = 0; i < FP; ++i) {
+        if constexpr (PKM) fp[buf][i] = frag_km<BP>(pt, wp * TP + i * 32, kk, lane);
+        else fp[buf][i] = frag_kc(pt, wp * TP + i * 32 + col, kk, half);
+      }
 #pragma unroll
-        for (int i = 0; i < FP; ++i) {
-          if constexpr (PKM) fp[i] = frag_km<BP>(pt, wp * TP + i * 32, kk, lane);
-          else fp[i] = frag_kc(pt, wp * TP + i * 32 + col, kk, half);
-        }
-#pragma unroll
-        for (int j = 0; j < FQ; ++j) {
-          if constexpr (QKM) fq[j] = frag_km<BQ>(qt, wq * TQ + j * 32, kk, lane);
-          else fq[j] = frag_kc(qt, wq * TQ + j * 32 + col, kk, half);
-        }
-#pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-          for (int j = 0; j < FQ; ++j) acc[i][j] = Elem<T>::mma(fp[i], fq[j], acc[i][j]);
+      for (int j = 0; j < FQ; ++j) {
+        if constexpr (QKM) fq[buf][j] = frag_km<BQ>(qt, wq * TQ + j * 32, kk, lane);
+        else fq[buf][j] = frag_kc(qt, wq * TQ + j * 32 + col, kk, half);
       }
     };
-
-    // ring of NS stages, loads NS - 1 steps ahead. At step t the wave waits
-    // for its loads of step t, the barrier makes every wave's part visible
-    // and tells that all have finished step t - 1, whose stage is refilled.
-    int issued = t0, ws = 0, rs = 0;
+    auto mma1 = [&](int buf, int n) {
+      const int i = n / FQ, j = n % FQ;
+      acc[i][j] = Elem<T>::mma(fp[buf][i], fq[buf][j], acc[i][j]);
+    };
+    auto mma = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i)
-      if (issued < t1) {
-        issue(issued++, ws);
-        ws = ws + 1 == NS ? 0 : ws + 1;
-      }
-    for (int t = t0; t < t1; ++t) {
-      if (t + NS - 1 <= t1) step_wait<(NS - 2) * (LP + LQ)>();
+      for (int n = 0; n < FP * FQ; ++n) mma1(buf, n);
+    };
+
+    // Ring of NS stages. Before a step's last k block the wave waits for its
+    // own loads of the next step and for its LDS reads; the barrier then
+    // makes the next stage visible and tells that every wave has read the
+    // whole of this one, which the loads of step t + NS refill between the
+    // last block's matrix instructions. The fragments of a k block are read
+    // while the block before it is multiplied; the scheduling barriers keep
+    // the compiler from pulling the two together.
+    if (t0 < t1) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (t0 + i < t1) load(t0 + i, i);
+      if (t0 + NS <= t1) step_wait<(NS - 1) * (LP + LQ)>();
       else step_wait<0>();
-      if (issued < t1) {
-        issue(issued++, ws);
-        ws = ws + 1 == NS ? 0 : ws + 1;
+      frags(0, 0, 0);
+      // opaque, or the compiler merges these reads with the loop's own
+#pragma unroll
+      for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fp[0][i]));
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) asm volatile("" : "+v"(fq[0][j]));
+      int slot = 0;
+      for (int t = t0; t < t1; ++t) {
+        const int next = slot + 1 == NS ? 0 : slot + 1;
+#pragma unroll
+        for (int kk = 0; kk + 1 < NK; ++kk) {
+          frags((kk + 1) & 1, slot, kk + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          mma(kk & 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (NS == 2 || t + NS > t1) step_wait<0>();
+        else step_wait<(NS - 2) * (LP + LQ)>();
+        frags(0, next, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool more = t + NS < t1;
+        const Src r = source(t + NS, slot);
+        constexpr int NM = FP * FQ, NL = LP + LQ;
+#pragma unroll
+        for (int n = 0; n < NM; ++n) {
+          mma1((NK - 1) & 1, n);
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) {
+#pragma unroll
+            for (int l = n * NL / NM; l < (n + 1) * NL / NM; ++l) load1(r, l);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        slot = next;
       }
-      compute(rs);
-      rs = rs + 1 == NS ? 0 : rs + 1;
+      step_wait<0>();
+    }
+    if (rest && z == a.splits - 1) {
+#pragma unroll 1
+      for (int sg = 0; sg < NSEG; ++sg) {
+        load_rest(sg);
+        step_wait<0>();
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+          frags(0, 0, kk);
+          mma(0);
+        }
+        step_wait<0>();
+      }
     }
 
-    // epilogue: lane holds column q = col, rows p = 8 (i / 4) + 4 half + i % 4
-    const int q0 = c0q + wq * TQ + col;
-    if (a.splits > 1) {
-      const int64_t zoff = (int64_t)z * a.nq * a.pcols;
+    epilogue(a, acc, smem + w * (NS * STAGE / NW), lane, c0p + (EPI == EPI_GLU ? wp * (TP / 2) : wp * TP),
+             c0q + wq * TQ, z);
+  }
+
+  // 32 rows of COLS elements of ES bytes, staged by the wave in LDS (rows
+  // padded by 16 bytes), to memory: 16 bytes a lane, whole rows, so that a
+  // store covers 64-byte runs and more (straight from the accumulators it
+  // would be 16 bytes of 32 rows)
+  template <int ES, int COLS> static constexpr int row_bytes() { return COLS * ES + 16; }
+  template <int ES, int COLS, typename R>
+  static __device__ __forceinline__ void flush(const uint8_t* buf, int lane, int q0, int nq, int p0, int np, bool vec,
+                                               R row) {
+    constexpr int CH = COLS * ES / 16, N = 16 / ES;
+    asm volatile("" ::: "memory");     // other lanes' writes: LDS runs in order
 #pragma unroll
-      for (int i = 0; i < FP; ++i)
+    for (int it = 0; it < 32 * CH / 64; ++it) {
+      const int r = (it * 64 + lane) / CH, c = (it * 64 + lane) % CH;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * row_bytes<ES, COLS>() + c * 16);
+      const int q = q0 + r, p = p0 + c * N;
+      if (q >= nq || p >= np) continue;
+      char* o = row(q);
+      if (!o) continue;
+      o += (int64_t)p * ES;
+      if (vec && p + N <= np) *reinterpret_cast<u32x4*>(o) = v;
+      else
 #pragma unroll
-        for (int j = 0; j < FQ; ++j) {
-          const int q = q0 + j * 32;
-          if (q >= a.nq) continue;
-          const bool up = EPI == EPI_GLU && (i & 1);
-          const int pbase = EPI == EPI_GLU ? c0p + ((wp * TP + i * 32) >> 6) * 32 : c0p + wp * TP + i * 32;
-          typename Elem<T>::acc4* row = reinterpret_cast<typename Elem<T>::acc4*>(
-              a.part + zoff + q * a.pcols + (up ? a.pcols / 2 : 0));
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int p = pbase + b * 8 + half * 4;
-            if (p < a.np)
-              row[p >> 2] = {acc[i][j][b * 4], acc[i][j][b * 4 + 1], acc[i][j][b * 4 + 2], acc[i][j][b * 4 + 3]};
+        for (int e = 0; e < N; ++e)
+          if (p + e < np) {
+            if constexpr (ES == 4) reinterpret_cast<uint32_t*>(o)[e] = v[e];
+            else reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
           }
+    }
+    asm volatile("" ::: "memory");
+  }
+  template <int DT> static __device__ __forceinline__ void put4(uint8_t* at, const float* v) {
+    if constexpr (DT == DT_F32) *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+    else
+      *reinterpret_cast<uint2*>(at) = make_uint2(to16<DT>(v[0]) | (uint32_t)to16<DT>(v[1]) << 16,
+                                                 to16<DT>(v[2]) | (uint32_t)to16<DT>(v[3]) << 16);
+  }
+  static __device__ __forceinline__ bool whole16(const void* p, int64_t ld, int es) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
+  }
+
+  // The wave's TP x TQ part of the tile: in acc[i][j] a lane holds column
+  // q = q0 + 32 j + lane % 32, rows p = p0 + 32 i + 8 b + 4 (lane / 32) + e
+  // (GLU: i even gate, i odd up of p0 + 16 i ...).
+  static __device__ __forceinline__ void epilogue(const DenseArgs& a, acc_t (&acc)[FP][FQ], uint8_t* buf, int lane,
+                                                  int p0, int q0, int z) {
+    constexpr bool GLU = EPI == EPI_GLU;
+    constexpr int OC = GLU ? TP / 2 : TP;              // output columns of the wave
+    constexpr int OG = OC / 32;                        // groups of 32
+    const int col = lane & 31, half = lane >> 5;
+    if (a.splits > 1) {
+      float* part = a.part + (int64_t)z * a.nq * a.pcols;
+      const int lim = (int)(GLU ? a.pcols / 2 : a.pcols);
+#pragma unroll
+      for (int j = 0; j < FQ; ++j)
+#pragma unroll
+        for (int i = 0; i < FP; ++i) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 1; ++e) {
+              typename Elem<T>::acc4 v = {acc[i][j][b * 4], acc[i][j][b * 4 + 1], acc[i][j][b * 4 + 2],
+                                          acc[i][j][b * 4 + 3]};
+              *reinterpret_cast<typename Elem<T>::acc4*>(buf + col * row_bytes<4, 32>() + (b * 8 + half * 4) * 4) = v;
+            }
+          float* base = part + (GLU && (i & 1) ? a.pcols / 2 : 0);
+          flush<4, 32>(buf, lane, q0 + 32 * j, a.nq, p0 + (GLU ? i / 2 : i) * 32, lim, true,
+                       [&](int q) { return reinterpret_cast<char*>(base + (int64_t)q * a.pcols); });
         }
       return;
     }
+    // the lane's column scales (and bias), all at once
+    float sp0[T == DT_I8 ? OG : 1][16], sp1[T == DT_I8 ? OG : 1][16];
+    if constexpr (T == DT_I8) {
+      const float* second = GLU ? a.sp1 : a.bias;
+#pragma unroll
+      for (int g = 0; g < OG; ++g)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int p = min(p0 + g * 32 + (r >> 2) * 8 + half * 4 + (r & 3), a.np - 1);
+          sp0[g][r] = a.sp0[p];
+          sp1[g][r] = second ? second[p] : 0.f;
+        }
+    }
+    const bool vec = whole16(a.out0, a.ldo, 2) && (!a.qpad || whole16(a.out1, a.ldo, 2));
+    const bool vecs = GLU && whole16(a.save, a.np, 4);
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
-      const int q = q0 + j * 32;
+      const int q = q0 + 32 * j;
+      float sq = 1.f;
+      if constexpr (T == DT_I8) sq = a.sq[min(q + col, a.nq - 1)];
+      float v[OG][16];
 #pragma unroll
-      for (int i = 0; i < FP; i += EPI == EPI_GLU ? 2 : 1) {
-        const int pbase = EPI == EPI_GLU ? c0p + ((wp * TP + i * 32) >> 6) * 32 : c0p + wp * TP + i * 32;
-        constexpr int I1 = EPI == EPI_GLU ? 1 : 0;
+      for (int g = 0; g < OG; ++g) {
+        float s0[16], s1[16];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          decltype(acc[0][0][0] + 0) s0[4], s1[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s0[e] = acc[i][j][b * 4 + e];
-            s1[e] = acc[i + I1][j][b * 4 + e];
+        for (int r = 0; r < 16; ++r) {
+          if constexpr (GLU) {
+            s0[r] = (float)acc[2 * g][j][r];
+            s1[r] = (float)acc[2 * g + 1][j][r];
+            if constexpr (T == DT_I8) {
+              s0[r] *= sq * sp0[g][r];
+              s1[r] *= sq * sp1[g][r];
+            }
+            v[g][r] = act_f(s0[r], a.act) * s1[r];
+          } else if constexpr (EPI == EPI_SCALE) {
+            v[g][r] = (float)acc[g][j][r] * (sq * sp0[g][r]) + sp1[g][r];
+          } else {
+            v[g][r] = acc[g][j][r];
           }
-          finish4<T, EPI>(a, q, pbase + b * 8 + half * 4, s0, s1);
+        }
+        if constexpr (GLU && T != DT_I8) {
+          if (a.save) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                put4<DT_F32>(buf + col * row_bytes<4, 32>() + (b * 8 + half * 4) * 4, (k ? s1 : s0) + b * 4);
+              float* base = static_cast<float*>(a.save) + k * a.np;
+              flush<4, 32>(buf, lane, q, a.nq, p0 + g * 32, a.np, vecs,
+                           [&](int qq) { return reinterpret_cast<char*>(base + (int64_t)qq * 2 * a.np); });
+            }
+          }
         }
       }
+#pragma unroll
+      for (int g = 0; g < OG; ++g)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint8_t* at = buf + col * row_bytes<2, OC>() + (g * 32 + b * 8 + half * 4) * 2;
+          if (a.out_dt == DT_BF16) put4<DT_BF16>(at, &v[g][b * 4]);
+          else put4<DT_F16>(at, &v[g][b * 4]);
+        }
+      flush<2, OC>(buf, lane, q, a.nq, p0, a.np, vec, [&](int qq) { return out_row(a, qq); });
     }
   }
 };
 
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
 __global__ __launch_bounds__(WP * WQ * 64) void k_dense(DenseArgs a) {
-  Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS>::run(a);
+  Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB>::run(a);
 }
 
 // Joins the K ranges of a split product, range 0 first, and runs its epilogue.
@@ -599,15 +755,14 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   }
 }
 
-__global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_t* dh, int64_t lddh, const uint16_t* gu,
+__global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_t* dh, int64_t lddh, const float* gu,
                                                   int inter, int ip, uint16_t* d) {
   const int64_t r = blockIdx.x;
   for (int i = blockIdx.y * 256 + threadIdx.x; i < ip; i += gridDim.y * 256) {
     float dg = 0.f, du = 0.f;
     if (i < inter) {
       const float e = from16_rt(dh[r * lddh + i], dt);
-      const float g = from16_rt(gu[r * 2 * inter + i], dt);
-      const float u = from16_rt(gu[r * 2 * inter + inter + i], dt);
+      const float g = gu[r * 2 * inter + i], u = gu[r * 2 * inter + inter + i];
       float v, dv;
       act_grad_f(g, act, &v, &dv);
       dg = e * u * dv;
@@ -619,12 +774,12 @@ __global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_
 }
 
 // --------------------------------------------------------------- launchers
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
 static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS> K;
+  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB> K;
   constexpr int lds = NS * K::STAGE;
   constexpr int OP = EPI == EPI_GLU ? BP / 2 : BP;
-  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, NS>;
+  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB>;
   const int64_t tiles = (int64_t)((a.np + OP - 1) / OP) * ((a.nq + BQ - 1) / BQ);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lds > 65536) {
@@ -643,11 +798,11 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
 template <int T, int EPI, int FORM>
 static hipError_t launch_form(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 2>(a, s);
-    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 2>(a, s);
+    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 2, 128>(a, s);
+    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 2, 128>(a, s);
     case 2:
-      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 4>(a, s);
-      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 4>(a, s);
+      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 4, 128>(a, s);
+      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 4, 128>(a, s);
   }
   return hipErrorInvalidValue;
 }
@@ -706,10 +861,10 @@ hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int c
   return hipGetLastError();
 }
 
-hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const void* gu, int rows, int inter,
+hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
                            int ip, void* d, hipStream_t s) {
   hipLaunchKernelGGL(k_glu_grad, dim3(rows, std::min((ip + 255) / 256, 1024)), dim3(256), 0, s, dt, act,
-                     static_cast<const uint16_t*>(dh), lddh, static_cast<const uint16_t*>(gu), inter, ip,
+                     static_cast<const uint16_t*>(dh), lddh, gu, inter, ip,
                      static_cast<uint16_t*>(d));
   return hipGetLastError();
 }

@@ -172,7 +172,7 @@ hipError_t padded(bool pad, const void* src, int64_t ld, int rows, int cols, int
   return launch_dense_pad(src, ld, rows, cols, es, dst, kp, s);
 }
 
-int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes,
+int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, float* gu, void* ws, uint64_t ws_bytes,
             void* stream) {
   if (!h) return bad(std::string(fn) + ": NULL h");
   int st = check_ld(fn, "ldh", ldh, a->inter);
@@ -204,7 +204,6 @@ int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, void
   d.np = a->inter;
   d.nq = a->rows;
   d.kbytes = (int)(p.kp * es);
-  d.steps = d.seg = steps_of(p.kp * es);
   d.splits = p.splits;
   d.act = a->act;
   d.out0 = h;
@@ -296,7 +295,7 @@ int moe_glu_workspace_size(const moe_glu* a, int kind, uint64_t* bytes) {
   return MOE_OK;
 }
 
-int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, void* gu, void* ws, uint64_t ws_bytes, void* stream) {
+int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, float* gu, void* ws, uint64_t ws_bytes, void* stream) {
   int st = check_glu("moe_glu_forward", a, false);
   return st ? st : glu_run("moe_glu_forward", a, a->dtype, h, ldh, gu, ws, ws_bytes, stream);
 }
@@ -306,7 +305,7 @@ int moe_glu_i8(const moe_glu* a, void* h, int64_t ldh, void* ws, uint64_t ws_byt
   return st ? st : glu_run("moe_glu_i8", a, DT_I8, h, ldh, nullptr, ws, ws_bytes, stream);
 }
 
-int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                      void* dw_gate, void* dw_up, void* ws, uint64_t ws_bytes, void* stream) {
   const char* fn = "moe_glu_backward";
   int st = check_glu(fn, a, false);
@@ -342,8 +341,7 @@ int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t l
     dd.nq = a->rows;
     dd.kbytes = (int)(2 * p.ip * 2);
     dd.krows = a->inter;
-    dd.steps = (int)(2 * p.ip / 64);
-    dd.seg = (int)(p.ip / 64);
+    dd.segbytes = (int)(p.ip * 2);
     dd.splits = p.splits_x;
     dd.out0 = dx;
     dd.ldo = lddx;
@@ -360,7 +358,6 @@ int moe_glu_backward(const moe_glu* a, const void* gu, const void* dh, int64_t l
     dd.ldp0 = x.ld;
     dd.nq = (int)(2 * p.ip);
     dd.krows = a->rows;
-    dd.steps = dd.seg = (a->rows + 63) / 64;
     dd.splits = p.splits_w;
     dd.out0 = dw_gate;
     dd.out1 = dw_up;
@@ -427,7 +424,6 @@ int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t 
   d.np = a->out;
   d.nq = a->rows;
   d.kbytes = (int)p.kp;
-  d.steps = d.seg = steps_of(p.kp);
   d.splits = p.splits;
   d.out0 = y;
   d.ldo = ldy;

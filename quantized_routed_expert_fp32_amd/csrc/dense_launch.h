@@ -27,17 +27,16 @@ struct DenseArgs {
   int np, nq;             // output columns and rows (GLU: np of gate and of up)
   int kbytes;             // NT / NN: bytes of a k-contiguous row in use (multiple of 16)
   int krows;              // NN: k rows of one segment in use; TN: k rows
-  int steps;              // K steps in all
-  int seg;                // NN: K steps of the first segment (steps when single)
+  int segbytes;           // NN: Q bytes of the first segment
   int splits;             // K ranges (1: the epilogue runs in the product)
   int act;
   // outputs
   void* out0;             // [nq, np] (weight gradients: rows below qseg)
   void* out1;             // weight gradients: rows from qpad on
   int64_t ldo;            // elements
-  int out_dt;             // DT_BF16 / DT_F16 / DT_F32
+  int out_dt;             // DT_BF16 / DT_F16
   int qseg, qpad;         // rows of out0, first row index of out1 (0: one output)
-  void* save;             // GLU: [nq, 2 np] pre-activations, or null
+  void* save;             // GLU: fp32 [nq, 2 np] pre-activations, or null
   const float* sq;        // 8-bit: scale of each Q row
   const float* sp0;       // 8-bit: scale of each P row (GLU: gate)
   const float* sp1;       // 8-bit GLU: up
@@ -63,7 +62,7 @@ hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, hipStream_t s);
 // D[r] = [dg | du], each ip wide (zero behind inter)
-hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const void* gu, int rows, int inter,
+hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
                            int ip, void* d, hipStream_t s);
 
 }  // namespace moe

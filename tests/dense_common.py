@@ -79,8 +79,8 @@ def quant(x):
 
 
 def grads(x, wg, wu, gu, dh, name, dt):
-    """The gradients and their bounds, from the g and u that the forward call
-    kept (so their rounding is part of the input here)."""
+    """The gradients and their bounds, from the fp32 g and u that the forward
+    call kept (so their rounding is part of the input here)."""
     g, u = gu[:, 0].double(), gu[:, 1].double()
     x, wg, wu, e = x.double(), wg.double(), wu.double(), dh.double()
     dg, du = e * u * act_d(g, name), e * act(g, name)
