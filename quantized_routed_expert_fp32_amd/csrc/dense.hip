@@ -197,17 +197,18 @@ __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 // reading one chunk of 16 rows meet 16 different bank groups. k-major
 // operand: rows k of 2 B bytes, 32-byte segment s at s ^ swz_km(k), so the 4
 // rows of a transposed read do.
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
 struct Dense {
   static constexpr bool PKM = FORM != FORM_NT, QKM = FORM == FORM_TN;
   static constexpr int NW = WP * WQ;
   static constexpr int TP = BP / WP, TQ = BQ / WQ, FP = TP / 32, FQ = TQ / 32;
-  static constexpr int PB = BP * KB, QB = BQ * KB, STAGE = PB + QB;
+  static constexpr int PB = BP * KB, QB = BQ * KB, UNIT = PB > QB ? PB : QB;   // R ring slots of UNIT bytes
   static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
   static constexpr int NK = KB / 32;               // matrix-instruction k blocks of a step
   static constexpr int CPR = KB / 16, KR = KB / 2;  // chunks of a k-contiguous row; k rows of a step
   typedef typename Elem<T>::acc acc_t;
-  static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB, "whole loads");
+  static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB && LP == LQ, "whole loads");
+  static_assert(R % 2 == 1 && R >= 5, "ring");
 
   static __device__ __forceinline__ int swz_kc(int r) { return KB == 128 ? r & 7 : (r >> 2) & 3; }
   // the same for k and k + 4
@@ -305,53 +306,52 @@ struct Dense {
         (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)smem);
     const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&g_zero16);
 
-    // load n of the LP + LQ of a step into its slot: step t of segment sg
+    // load n of a step's P or Q half into ring slot `slot`: step t of segment sg
     struct Src {
-      const uint8_t *p, *q;
-      int64_t dp;
+      const uint8_t* b;
       uint32_t lds;
       bool second;
     };
-    auto source_at = [&](int sg, int t, int slot) {
+    auto source_p = [&](int sg, int t, int slot) {
       Src r;
-      r.lds = lds0 + slot * STAGE + w * 1024;
+      r.lds = lds0 + slot * UNIT + w * 1024;
       r.second = sg;
-      r.dp = PKM ? (int64_t)t * KR * (sg ? a.ldp1 : a.ldp0) : (int64_t)t * KB;
-      r.p = sg ? pb1 : pb0;
-      r.q = qb + (QKM ? (int64_t)t * KR * a.ldq : (int64_t)t * KB + (sg ? a.segbytes : 0));
+      r.b = (EPI == EPI_GLU ? nullptr : sg ? pb1 : pb0) +
+            (PKM ? (int64_t)t * KR * (sg ? a.ldp1 : a.ldp0) : (int64_t)t * KB);
       return r;
     };
-    auto source = [&](int t, int slot) {
-      const int sg = NSEG == 2 && t >= nws;
-      return source_at(sg, sg ? t - nws : t, slot);
+    auto source_q = [&](int sg, int t, int slot) {
+      Src r;
+      r.lds = lds0 + slot * UNIT + w * 1024;
+      r.second = sg;
+      r.b = qb + (QKM ? (int64_t)t * KR * a.ldq : (int64_t)t * KB + (sg ? a.segbytes : 0));
+      return r;
     };
-    auto base_of = [&](const Src& r, int n) -> const uint8_t* {
-      if (n >= LP) return r.q;
-      return (EPI == EPI_GLU ? pbn[n < LP ? n : 0] : r.p) + r.dp;
+    auto seg_of = [&](int t) { return NSEG == 2 && t >= nws ? 1 : 0; };
+    auto src = [&](bool isp, int t, int slot) {
+      const int sg = seg_of(t);
+      return isp ? source_p(sg, sg ? t - nws : t, slot) : source_q(sg, sg ? t - nws : t, slot);
     };
-    auto off_of = [&](const Src& r, int n) {
-      if (n >= LP) return offq[n < LP ? 0 : n - LP];
-      if constexpr (FORM == FORM_NN) return r.second ? offp1[n < LP ? n : 0] : offp[n < LP ? n : 0];
-      else return offp[n < LP ? n : 0];
+    auto base_p = [&](const Src& r, int n) -> const uint8_t* {
+      return EPI == EPI_GLU ? pbn[n] + reinterpret_cast<intptr_t>(r.b) : r.b;
     };
-    auto lds_of = [&](const Src& r, int n) { return r.lds + (n < LP ? n * NW * 1024 : PB + (n - LP) * NW * 1024); };
-    auto load1 = [&](const Src& r, int n) { dma16(lds_of(r, n), off_of(r, n), uniform(base_of(r, n))); };
-    auto load = [&](int t, int slot) {
-      const Src r = source(t, slot);
-#pragma unroll
-      for (int n = 0; n < LP + LQ; ++n) load1(r, n);
+    auto off_p = [&](const Src& r, int n) {
+      if constexpr (FORM == FORM_NN) return r.second ? offp1[n] : offp[n];
+      else return offp[n];
     };
-    // the step behind segment sg's whole ones, zero past the operands' end
+    auto load_p = [&](const Src& r, int n) { dma16(r.lds + n * NW * 1024, off_p(r, n), uniform(base_p(r, n))); };
+    auto load_q = [&](const Src& r, int n) { dma16(r.lds + n * NW * 1024, offq[n], uniform(r.b)); };
+    // the step behind segment sg's whole ones into slots 0 and 1, zero past the operands' end
     auto load_rest = [&](int sg) {
-      const Src r = source_at(sg, nws, 0);
+      const Src rp = source_p(sg, nws, 0), rq = source_q(sg, nws, 1);
+      const int kr = a.krows - nws * KR, kb = a.kbytes - nws * KB - (sg ? a.segbytes : 0);
 #pragma unroll
-      for (int n = 0; n < LP + LQ; ++n) {
-        const bool isp = n < LP;
-        const int q = ((isp ? n : n - LP) * NW + w) * 64 + lane;
-        bool in;
-        if (isp ? PKM : QKM) in = q / ((isp ? BP : BQ) * 2 / 16) < a.krows - nws * KR;
-        else in = (sg ? a.segbytes : 0) + nws * KB + (((q % CPR) ^ swz_kc(q / CPR)) * 16) < a.kbytes;
-        dma16_at(lds_of(r, n), in ? base_of(r, n) + off_of(r, n) : zero);
+      for (int n = 0; n < LP; ++n) {
+        const int q = (n * NW + w) * 64 + lane;
+        const bool inp = PKM ? q / (BP * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
+        const bool inq = QKM ? q / (BQ * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
+        dma16_at(rp.lds + n * NW * 1024, inp ? base_p(rp, n) + off_p(rp, n) : zero);
+        dma16_at(rq.lds + n * NW * 1024, inq ? rq.b + offq[n] : zero);
       }
     };
 
@@ -363,9 +363,9 @@ struct Dense {
 
     const int col = lane & 31, half = lane >> 5;
     u32x4 fp[2][FP], fq[2][FQ];
-    auto frags = [&](int buf, int slot, int kk) {
-      const uint8_t* pt = smem + slot * STAGE;
-      const uint8_t* qt = pt + PB;
+    auto frags = [&](int buf, int sp, int sq, int kk) {
+      const uint8_t* pt = smem + sp * UNIT;
+      const uint8_t* qt = smem + sq * UNIT;
 #pragma unroll
       for (int i = 0; i < FP; ++i) {
         if constexpr (PKM) fp[buf][i] = frag_km<BP>(pt, wp * TP + i * 32, kk, lane);
@@ -386,53 +386,86 @@ struct Dense {
       for (int n = 0; n < FP * FQ; ++n) mma1(buf, n);
     };
 
-    // Ring of NS stages. Before a step's last k block the wave waits for its
-    // own loads of the next step and for its LDS reads; the barrier then
-    // makes the next stage visible and tells that every wave has read the
-    // whole of this one, which the loads of step t + NS refill between the
-    // last block's matrix instructions. The fragments of a k block are read
-    // while the block before it is multiplied; the scheduling barriers keep
-    // the compiler from pulling the two together.
+    // Ring of R slots, a step's P and Q halves in turn: half 2 t (P) and 2 t + 1
+    // (Q) of step t in slots of their number mod R. Before a step's last k
+    // block the wave waits for its own loads of the next step and for its LDS
+    // reads; the barrier then makes the next step visible and tells that every
+    // wave has read the whole of this one, whose two slots halves 2 t + R (a Q)
+    // and 2 t + R + 1 (a P) refill: the Q loads go out between that block's
+    // matrix instructions, the P loads (needed a step later) between those of
+    // the next step's blocks. An odd R keeps half a step more in flight than
+    // whole stages in the same memory. The fragments of a k block are read
+    // while the block before it is multiplied; the scheduling barriers keep the
+    // compiler from pulling the two together.
+    constexpr int NM = FP * FQ;
+    const int halves = 2 * (t1 - t0);
     if (t0 < t1) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (t0 + i < t1) load(t0 + i, i);
-      if (t0 + NS <= t1) step_wait<(NS - 1) * (LP + LQ)>();
+      for (int h = 0; h < R; ++h)
+        if (h < halves) {
+          const Src r = src(h % 2 == 0, t0 + h / 2, h);
+#pragma unroll
+          for (int n = 0; n < LP; ++n) {
+            if (h % 2 == 0) load_p(r, n);
+            else load_q(r, n);
+          }
+        }
+      if (halves >= R) step_wait<(R - 2) * LP>();
       else step_wait<0>();
-      frags(0, 0, 0);
+      frags(0, 0, 1, 0);
       // opaque, or the compiler merges these reads with the loop's own
 #pragma unroll
       for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fp[0][i]));
 #pragma unroll
       for (int j = 0; j < FQ; ++j) asm volatile("" : "+v"(fq[0][j]));
-      int slot = 0;
+      int sp = 0, sq = 1;
+      Src rp = src(true, t0, 0);
+      bool more_p = false;
       for (int t = t0; t < t1; ++t) {
-        const int next = slot + 1 == NS ? 0 : slot + 1;
+        const int np_ = sp + 2 >= R ? sp + 2 - R : sp + 2, nq_ = sq + 2 >= R ? sq + 2 - R : sq + 2;
+        constexpr int PHN = (NK - 1) * NM;      // matrix instructions the P loads spread over
 #pragma unroll
         for (int kk = 0; kk + 1 < NK; ++kk) {
-          frags((kk + 1) & 1, slot, kk + 1);
+          frags((kk + 1) & 1, sp, sq, kk + 1);
           __builtin_amdgcn_sched_barrier(0);
-          mma(kk & 1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (NS == 2 || t + NS > t1) step_wait<0>();
-        else step_wait<(NS - 2) * (LP + LQ)>();
-        frags(0, next, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        const bool more = t + NS < t1;
-        const Src r = source(t + NS, slot);
-        constexpr int NM = FP * FQ, NL = LP + LQ;
 #pragma unroll
-        for (int n = 0; n < NM; ++n) {
-          mma1((NK - 1) & 1, n);
-          __builtin_amdgcn_sched_barrier(0);
-          if (more) {
+          for (int n = 0; n < NM; ++n) {
+            mma1(kk & 1, n);
+            const int m = kk * NM + n;
+            if (m * LP / PHN != (m + 1) * LP / PHN || LP > PHN) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (more_p) {
 #pragma unroll
-            for (int l = n * NL / NM; l < (n + 1) * NL / NM; ++l) load1(r, l);
+                for (int l = m * LP / PHN; l < (m + 1) * LP / PHN; ++l) load_p(rp, l);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        slot = next;
+        const int rel = 2 * (t - t0);
+        if (rel + R <= halves) step_wait<(R - 4) * LP>();
+        else step_wait<0>();
+        frags(0, np_, nq_, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        const bool more_q = rel + R < halves;
+        const Src rq = src(false, t + R / 2, sp);
+        more_p = rel + R + 1 < halves;
+        rp = src(true, t + R / 2 + 1, sq);
+#pragma unroll
+        for (int n = 0; n < NM; ++n) {
+          mma1((NK - 1) & 1, n);
+          if (n * LQ / NM != (n + 1) * LQ / NM || LQ > NM) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (more_q) {
+#pragma unroll
+              for (int l = n * LQ / NM; l < (n + 1) * LQ / NM; ++l) load_q(rq, l);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        sp = np_;
+        sq = nq_;
       }
       step_wait<0>();
     }
@@ -443,14 +476,14 @@ struct Dense {
         step_wait<0>();
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
-          frags(0, 0, kk);
+          frags(0, 0, 1, kk);
           mma(0);
         }
         step_wait<0>();
       }
     }
 
-    epilogue(a, acc, smem + w * (NS * STAGE / NW), lane, c0p + (EPI == EPI_GLU ? wp * (TP / 2) : wp * TP),
+    epilogue(a, acc, smem + w * (R * UNIT / NW / 16 * 16), lane, c0p + (EPI == EPI_GLU ? wp * (TP / 2) : wp * TP),
              c0q + wq * TQ, z);
   }
 
@@ -459,9 +492,9 @@ struct Dense {
   // store covers 64-byte runs and more (straight from the accumulators it
   // would be 16 bytes of 32 rows)
   template <int ES, int COLS> static constexpr int row_bytes() { return COLS * ES + 16; }
-  template <int ES, int COLS, typename R>
+  template <int ES, int COLS, typename RowOf>
   static __device__ __forceinline__ void flush(const uint8_t* buf, int lane, int q0, int nq, int p0, int np, bool vec,
-                                               R row) {
+                                               RowOf row) {
     constexpr int CH = COLS * ES / 16, N = 16 / ES;
     asm volatile("" ::: "memory");     // other lanes' writes: LDS runs in order
 #pragma unroll
@@ -591,9 +624,9 @@ struct Dense {
   }
 };
 
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
 __global__ __launch_bounds__(WP * WQ * 64) void k_dense(DenseArgs a) {
-  Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB>::run(a);
+  Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB>::run(a);
 }
 
 // Joins the K ranges of a split product, range 0 first, and runs its epilogue.
@@ -774,12 +807,12 @@ __global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_
 }
 
 // --------------------------------------------------------------- launchers
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int NS, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
 static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB> K;
-  constexpr int lds = NS * K::STAGE;
+  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB> K;
+  constexpr int lds = R * K::UNIT;
   constexpr int OP = EPI == EPI_GLU ? BP / 2 : BP;
-  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, NS, KB>;
+  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB>;
   const int64_t tiles = (int64_t)((a.np + OP - 1) / OP) * ((a.nq + BQ - 1) / BQ);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lds > 65536) {
@@ -798,11 +831,11 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
 template <int T, int EPI, int FORM>
 static hipError_t launch_form(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 2, 128>(a, s);
-    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 2, 128>(a, s);
+    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 5, 128>(a, s);
+    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 5, 128>(a, s);
     case 2:
-      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 4, 128>(a, s);
-      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 4, 128>(a, s);
+      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 9, 128>(a, s);
+      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 9, 128>(a, s);
   }
   return hipErrorInvalidValue;
 }
