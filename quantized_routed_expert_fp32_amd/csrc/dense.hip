@@ -12,9 +12,7 @@ typedef _Float16 f16;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -22,13 +20,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <int T> struct Elem;
 template <> struct Elem<DT_BF16> {
   typedef __bf16 type;
-  typedef f32x16 acc;
   typedef f32x4 acc4;
   static constexpr int SIZE = 2;
-  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c,
-                                                   0, 0, 0);
-  }
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c,
                                                    0, 0, 0);
@@ -36,13 +29,8 @@ template <> struct Elem<DT_BF16> {
 };
 template <> struct Elem<DT_F16> {
   typedef f16 type;
-  typedef f32x16 acc;
   typedef f32x4 acc4;
   static constexpr int SIZE = 2;
-  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0,
-                                                  0, 0);
-  }
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0,
                                                   0, 0);
@@ -50,13 +38,8 @@ template <> struct Elem<DT_F16> {
 };
 template <> struct Elem<DT_I8> {
   typedef int8_t type;
-  typedef i32x16 acc;
   typedef i32x4 acc4;
   static constexpr int SIZE = 1;
-  static __device__ __forceinline__ acc mma(u32x4 p, u32x4 q, acc c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, q), c, 0, 0,
-                                                 0);
-  }
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, q), c, 0, 0,
                                                  0);
@@ -199,14 +182,17 @@ __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 // rows of a transposed read do.
 template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
 struct Dense {
+  static constexpr int RPM = 1;                    // fragment reads a product
   static constexpr bool PKM = FORM != FORM_NT, QKM = FORM == FORM_TN;
   static constexpr int NW = WP * WQ;
-  static constexpr int TP = BP / WP, TQ = BQ / WQ, FP = TP / 32, FQ = TQ / 32;
+  static constexpr int TP = BP / WP, TQ = BQ / WQ, FP = TP / 16, FQ = TQ / 16;
   static constexpr int PB = BP * KB, QB = BQ * KB, UNIT = PB > QB ? PB : QB;   // R ring slots of UNIT bytes
   static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
-  static constexpr int NK = KB / 32;               // matrix-instruction k blocks of a step
+  static constexpr int NK = KB / 64;               // matrix-instruction k blocks of a step
+  static constexpr int QH = FQ > 4 ? FQ / 4 : 1, QG = FQ / QH, NU = NK * QH;   // units: a k block and QG Q fragments
   static constexpr int CPR = KB / 16, KR = KB / 2;  // chunks of a k-contiguous row; k rows of a step
-  typedef typename Elem<T>::acc acc_t;
+  typedef typename Elem<T>::acc4 acc_t;
+  static_assert(NK % 2 == 0 && NU % 2 == 0 && QG * QH == FQ, "units");
   static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB && LP == LQ, "whole loads");
   static_assert(R % 2 == 1 && R >= 5, "ring");
 
@@ -241,18 +227,18 @@ struct Dense {
     }
   }
 
-  static __device__ __forceinline__ u32x4 frag_kc(const uint8_t* tile, int row, int kk, int half) {
-    return *reinterpret_cast<const u32x4*>(tile + row * KB + (((kk * 2 + half) ^ swz_kc(row)) << 4));
+  // a lane's 16 bytes of row `row`, k block kk: chunk 4 kk + lane / 16
+  static __device__ __forceinline__ u32x4 frag_kc(const uint8_t* tile, int row, int kk, int quad) {
+    return *reinterpret_cast<const u32x4*>(tile + row * KB + (((kk * 4 + quad) ^ swz_kc(row)) << 4));
   }
-  // k-major: the lane's 8 k of column col0 + lane % 32: two 4-row transposed
+  // k-major: the lane's 8 k of column col0 + lane % 16: two 4-row transposed
   // reads; a 16-lane group reads 4 rows of 16 columns, lane i supplying the
   // address of row i / 4, columns 4 (i % 4).. and getting column i's 4 rows
   template <int B>
   static __device__ __forceinline__ u32x4 frag_km(const uint8_t* tile, int col0, int kk, int lane) {
     const int i = lane & 15, g = lane >> 4;
-    const int k = kk * 16 + (g >> 1) * 8 + (i >> 2);
-    const int col = col0 + (g & 1) * 16 + (i & 3) * 4;
-    const uint8_t* ad = tile + k * (B * 2) + ((((col >> 4) ^ swz_km<B>(k)) << 5) | ((col & 15) << 1));
+    const int k = kk * 32 + g * 8 + (i >> 2);
+    const uint8_t* ad = tile + k * (B * 2) + ((((col0 >> 4) ^ swz_km<B>(k)) << 5) | ((i & 3) << 3));
     typedef __attribute__((address_space(3))) i16x4* lp;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(ad));
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(ad + 4 * (B * 2)));
@@ -278,7 +264,8 @@ struct Dense {
     constexpr int GQ = 4;
     const int band = id / (GQ * tp), inb = id % (GQ * tp);
     const int gh = min(GQ, tq - band * GQ);
-    const int iq = band * GQ + inb % gh, ip = inb / gh;
+    // (uniform, but a division leaves its result in a vector register)
+    const int iq = __builtin_amdgcn_readfirstlane(band * GQ + inb % gh), ip = __builtin_amdgcn_readfirstlane(inb / gh);
     const int c0p = ip * OP, c0q = iq * BQ;
     // K steps that lie whole inside the operands, this workgroup's range of
     // them, and the masked rest (up to one step a segment), which the last
@@ -287,7 +274,8 @@ struct Dense {
     const int nws = PKM ? a.krows / KR : a.kbytes / KB;
     const bool rest = PKM ? a.krows % KR != 0 : a.kbytes % KB != 0;
     constexpr int NSEG = FORM == FORM_NN ? 2 : 1;
-    const int t0 = (int)((int64_t)NSEG * nws * z / a.splits), t1 = (int)((int64_t)NSEG * nws * (z + 1) / a.splits);
+    const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * z / a.splits));
+    const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * (z + 1) / a.splits));
 
     uint32_t offp[LP], offq[LQ];
     offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1);
@@ -361,43 +349,43 @@ struct Dense {
 #pragma unroll
       for (int j = 0; j < FQ; ++j) acc[i][j] = acc_t{};
 
-    const int col = lane & 31, half = lane >> 5;
-    u32x4 fp[2][FP], fq[2][FQ];
-    auto frags = [&](int buf, int sp, int sq, int kk) {
+    // A unit is a k block (64 bytes of k) and QG of the wave's Q fragments.
+    const int col = lane & 15, quad = lane >> 4;
+    u32x4 fp[2][FP], fq[2][QG];
+    auto frag_p = [&](int sp, int kk, int i) {
       const uint8_t* pt = smem + sp * UNIT;
+      if constexpr (PKM) fp[kk & 1][i] = frag_km<BP>(pt, wp * TP + i * 16, kk, lane);
+      else fp[kk & 1][i] = frag_kc(pt, wp * TP + i * 16 + col, kk, quad);
+    };
+    auto frag_q = [&](int sq, int u, int j) {
       const uint8_t* qt = smem + sq * UNIT;
-#pragma unroll
-      for (int i = 0; i < FP; ++i) {
-        if constexpr (PKM) fp[buf][i] = frag_km<BP>(pt, wp * TP + i * 32, kk, lane);
-        else fp[buf][i] = frag_kc(pt, wp * TP + i * 32 + col, kk, half);
-      }
-#pragma unroll
-      for (int j = 0; j < FQ; ++j) {
-        if constexpr (QKM) fq[buf][j] = frag_km<BQ>(qt, wq * TQ + j * 32, kk, lane);
-        else fq[buf][j] = frag_kc(qt, wq * TQ + j * 32 + col, kk, half);
-      }
+      const int kk = u / QH, jj = u % QH * QG + j;
+      if constexpr (QKM) fq[u & 1][j] = frag_km<BQ>(qt, wq * TQ + jj * 16, kk, lane);
+      else fq[u & 1][j] = frag_kc(qt, wq * TQ + jj * 16 + col, kk, quad);
     };
-    auto mma1 = [&](int buf, int n) {
-      const int i = n / FQ, j = n % FQ;
-      acc[i][j] = Elem<T>::mma(fp[buf][i], fq[buf][j], acc[i][j]);
+    // read x of unit u, in the order its products need them: P 0, the Qs, the other Ps
+    auto frag1 = [&](int sp, int sq, int u, int x) {
+      if (u % QH != 0) frag_q(sq, u, x);
+      else if (x == 0 || x > QG) frag_p(sp, u / QH, x == 0 ? 0 : x - QG);
+      else frag_q(sq, u, x - 1);
     };
-    auto mma = [&](int buf) {
-#pragma unroll
-      for (int n = 0; n < FP * FQ; ++n) mma1(buf, n);
+    constexpr int NM = FP * QG;
+    auto mma1 = [&](int u, int n) {
+      const int i = n / QG, j = n % QG;
+      acc_t& c = acc[i][u % QH * QG + j];
+      c = Elem<T>::mma16(fp[u / QH & 1][i], fq[u & 1][j], c);
     };
 
     // Ring of R slots, a step's P and Q halves in turn: half 2 t (P) and 2 t + 1
-    // (Q) of step t in slots of their number mod R. Before a step's last k
-    // block the wave waits for its own loads of the next step and for its LDS
-    // reads; the barrier then makes the next step visible and tells that every
-    // wave has read the whole of this one, whose two slots halves 2 t + R (a Q)
-    // and 2 t + R + 1 (a P) refill: the Q loads go out between that block's
-    // matrix instructions, the P loads (needed a step later) between those of
-    // the next step's blocks. An odd R keeps half a step more in flight than
-    // whole stages in the same memory. The fragments of a k block are read
-    // while the block before it is multiplied; the scheduling barriers keep the
-    // compiler from pulling the two together.
-    constexpr int NM = FP * FQ;
+    // (Q) of step t in slots of their number mod R. Before a step's last unit
+    // the wave waits for its own loads of the next step and for its LDS reads;
+    // the barrier then makes the next step visible and tells that every wave
+    // has read the whole of this one, whose two slots halves 2 t + R (a Q) and
+    // 2 t + R + 1 (a P) refill: the Q loads go out between that unit's matrix
+    // instructions, the P loads (needed a step later) between those of the next
+    // step's units. An odd R keeps half a step more in flight than whole stages
+    // in the same memory. The fragments of a unit are read between the products
+    // of the one before it; the scheduling barriers keep that order.
     const int halves = 2 * (t1 - t0);
     if (t0 < t1) {
 #pragma unroll
@@ -412,60 +400,57 @@ struct Dense {
         }
       if (halves >= R) step_wait<(R - 2) * LP>();
       else step_wait<0>();
-      frags(0, 0, 1, 0);
+#pragma unroll
+      for (int x = 0; x < FP + QG; ++x) frag1(0, 1, 0, x);
       // opaque, or the compiler merges these reads with the loop's own
 #pragma unroll
       for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fp[0][i]));
 #pragma unroll
-      for (int j = 0; j < FQ; ++j) asm volatile("" : "+v"(fq[0][j]));
+      for (int j = 0; j < QG; ++j) asm volatile("" : "+v"(fq[0][j]));
       int sp = 0, sq = 1;
       Src rp = src(true, t0, 0);
       bool more_p = false;
       for (int t = t0; t < t1; ++t) {
-        const int np_ = sp + 2 >= R ? sp + 2 - R : sp + 2, nq_ = sq + 2 >= R ? sq + 2 - R : sq + 2;
-        constexpr int PHN = (NK - 1) * NM;      // matrix instructions the P loads spread over
-#pragma unroll
-        for (int kk = 0; kk + 1 < NK; ++kk) {
-          frags((kk + 1) & 1, sp, sq, kk + 1);
-          __builtin_amdgcn_sched_barrier(0);
+        const int sp1 = sp + 2 >= R ? sp + 2 - R : sp + 2, sq1 = sq + 2 >= R ? sq + 2 - R : sq + 2;
+        // unit u's products, between them the reads of unit v of the step in
+        // slots fsp, fsq, and some of the loads
+        auto unit = [&](int u, int fsp, int fsq, int v, auto loads) {
+          const int nf = v % QH ? QG : FP + QG;
 #pragma unroll
           for (int n = 0; n < NM; ++n) {
-            mma1(kk & 1, n);
-            const int m = kk * NM + n;
-            if (m * LP / PHN != (m + 1) * LP / PHN || LP > PHN) {
-              __builtin_amdgcn_sched_barrier(0);
-              if (more_p) {
+            mma1(u, n);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int l = m * LP / PHN; l < (m + 1) * LP / PHN; ++l) load_p(rp, l);
-              }
-              __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int x = n * RPM; x < (n + 1 == NM ? nf : min((n + 1) * RPM, nf)); ++x) frag1(fsp, fsq, v, x);
+            loads(n);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        };
+        constexpr int PHN = (NU - 1) * NM;      // products the P loads spread over
+#pragma unroll
+        for (int u = 0; u + 1 < NU; ++u)
+          unit(u, sp, sq, u + 1, [&](int n) {
+            const int m = u * NM + n;
+            if (m * LP / PHN != (m + 1) * LP / PHN && more_p) {
+#pragma unroll
+              for (int l = m * LP / PHN; l < (m + 1) * LP / PHN; ++l) load_p(rp, l);
+            }
+          });
         const int rel = 2 * (t - t0);
         if (rel + R <= halves) step_wait<(R - 4) * LP>();
         else step_wait<0>();
-        frags(0, np_, nq_, 0);
-        __builtin_amdgcn_sched_barrier(0);
         const bool more_q = rel + R < halves;
         const Src rq = src(false, t + R / 2, sp);
         more_p = rel + R + 1 < halves;
         rp = src(true, t + R / 2 + 1, sq);
+        unit(NU - 1, sp1, sq1, 0, [&](int n) {
+          if (n * LQ / NM != (n + 1) * LQ / NM && more_q) {
 #pragma unroll
-        for (int n = 0; n < NM; ++n) {
-          mma1((NK - 1) & 1, n);
-          if (n * LQ / NM != (n + 1) * LQ / NM || LQ > NM) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (more_q) {
-#pragma unroll
-              for (int l = n * LQ / NM; l < (n + 1) * LQ / NM; ++l) load_q(rq, l);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int l = n * LQ / NM; l < (n + 1) * LQ / NM; ++l) load_q(rq, l);
           }
-        }
-        sp = np_;
-        sq = nq_;
+        });
+        sp = sp1;
+        sq = sq1;
       }
       step_wait<0>();
     }
@@ -475,9 +460,11 @@ struct Dense {
         load_rest(sg);
         step_wait<0>();
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) {
-          frags(0, 0, 1, kk);
-          mma(0);
+        for (int u = 0; u < NU; ++u) {
+#pragma unroll
+          for (int x = 0; x < (u % QH ? QG : FP + QG); ++x) frag1(0, 1, u, x);
+#pragma unroll
+          for (int n = 0; n < NM; ++n) mma1(u, n);
         }
         step_wait<0>();
       }
@@ -487,10 +474,10 @@ struct Dense {
              c0q + wq * TQ, z);
   }
 
-  // 32 rows of COLS elements of ES bytes, staged by the wave in LDS (rows
+  // 16 rows of COLS elements of ES bytes, staged by the wave in LDS (rows
   // padded by 16 bytes), to memory: 16 bytes a lane, whole rows, so that a
   // store covers 64-byte runs and more (straight from the accumulators it
-  // would be 16 bytes of 32 rows)
+  // would be 32 bytes of 16 rows)
   template <int ES, int COLS> static constexpr int row_bytes() { return COLS * ES + 16; }
   template <int ES, int COLS, typename RowOf>
   static __device__ __forceinline__ void flush(const uint8_t* buf, int lane, int q0, int nq, int p0, int np, bool vec,
@@ -498,8 +485,9 @@ struct Dense {
     constexpr int CH = COLS * ES / 16, N = 16 / ES;
     asm volatile("" ::: "memory");     // other lanes' writes: LDS runs in order
 #pragma unroll
-    for (int it = 0; it < 32 * CH / 64; ++it) {
+    for (int it = 0; it < (16 * CH + 63) / 64; ++it) {
       const int r = (it * 64 + lane) / CH, c = (it * 64 + lane) % CH;
+      if (16 * CH % 64 && r >= 16) continue;
       const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * row_bytes<ES, COLS>() + c * 16);
       const int q = q0 + r, p = p0 + c * N;
       if (q >= nq || p >= np) continue;
@@ -528,97 +516,86 @@ struct Dense {
   }
 
   // The wave's TP x TQ part of the tile: in acc[i][j] a lane holds column
-  // q = q0 + 32 j + lane % 32, rows p = p0 + 32 i + 8 b + 4 (lane / 32) + e
-  // (GLU: i even gate, i odd up of p0 + 16 i ...).
+  // q = q0 + 16 j + lane % 16, rows p = p0 + 16 i + 4 (lane / 16) + e (GLU: of
+  // 4 fragments the first 2 are gate, the others up of the same 32 outputs).
   static __device__ __forceinline__ void epilogue(const DenseArgs& a, acc_t (&acc)[FP][FQ], uint8_t* buf, int lane,
                                                   int p0, int q0, int z) {
     constexpr bool GLU = EPI == EPI_GLU;
     constexpr int OC = GLU ? TP / 2 : TP;              // output columns of the wave
-    constexpr int OG = OC / 32;                        // groups of 32
-    const int col = lane & 31, half = lane >> 5;
+    constexpr int OG = OC / 16;                        // groups of 16
+    const int col = lane & 15, quad = lane >> 4;
+    auto gate = [](int g) { return GLU ? g / 2 * 4 + g % 2 : g; };
     if (a.splits > 1) {
       float* part = a.part + (int64_t)z * a.nq * a.pcols;
       const int lim = (int)(GLU ? a.pcols / 2 : a.pcols);
 #pragma unroll
       for (int j = 0; j < FQ; ++j)
 #pragma unroll
-        for (int i = 0; i < FP; ++i) {
+        for (int k = 0; k < (GLU ? 2 : 1); ++k) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 1; ++e) {
-              typename Elem<T>::acc4 v = {acc[i][j][b * 4], acc[i][j][b * 4 + 1], acc[i][j][b * 4 + 2],
-                                          acc[i][j][b * 4 + 3]};
-              *reinterpret_cast<typename Elem<T>::acc4*>(buf + col * row_bytes<4, 32>() + (b * 8 + half * 4) * 4) = v;
-            }
-          float* base = part + (GLU && (i & 1) ? a.pcols / 2 : 0);
-          flush<4, 32>(buf, lane, q0 + 32 * j, a.nq, p0 + (GLU ? i / 2 : i) * 32, lim, true,
+          for (int g = 0; g < OG; ++g)
+            *reinterpret_cast<acc_t*>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4) = acc[gate(g) + 2 * k][j];
+          float* base = part + (k ? a.pcols / 2 : 0);
+          flush<4, OC>(buf, lane, q0 + 16 * j, a.nq, p0, lim, true,
                        [&](int q) { return reinterpret_cast<char*>(base + (int64_t)q * a.pcols); });
         }
       return;
     }
     // the lane's column scales (and bias), all at once
-    float sp0[T == DT_I8 ? OG : 1][16], sp1[T == DT_I8 ? OG : 1][16];
+    float sp0[T == DT_I8 ? OG : 1][4], sp1[T == DT_I8 ? OG : 1][4];
     if constexpr (T == DT_I8) {
       const float* second = GLU ? a.sp1 : a.bias;
 #pragma unroll
       for (int g = 0; g < OG; ++g)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int p = min(p0 + g * 32 + (r >> 2) * 8 + half * 4 + (r & 3), a.np - 1);
-          sp0[g][r] = a.sp0[p];
-          sp1[g][r] = second ? second[p] : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          const int p = min(p0 + g * 16 + quad * 4 + e, a.np - 1);
+          sp0[g][e] = a.sp0[p];
+          sp1[g][e] = second ? second[p] : 0.f;
         }
     }
     const bool vec = whole16(a.out0, a.ldo, 2) && (!a.qpad || whole16(a.out1, a.ldo, 2));
     const bool vecs = GLU && whole16(a.save, a.np, 4);
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
-      const int q = q0 + 32 * j;
+      const int q = q0 + 16 * j;
       float sq = 1.f;
       if constexpr (T == DT_I8) sq = a.sq[min(q + col, a.nq - 1)];
-      float v[OG][16];
+      float s0[OG][4], s1[OG][4];
 #pragma unroll
-      for (int g = 0; g < OG; ++g) {
-        float s0[16], s1[16];
+      for (int g = 0; g < OG; ++g)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if constexpr (GLU) {
-            s0[r] = (float)acc[2 * g][j][r];
-            s1[r] = (float)acc[2 * g + 1][j][r];
-            if constexpr (T == DT_I8) {
-              s0[r] *= sq * sp0[g][r];
-              s1[r] *= sq * sp1[g][r];
-            }
-            v[g][r] = act_f(s0[r], a.act) * s1[r];
-          } else if constexpr (EPI == EPI_SCALE) {
-            v[g][r] = (float)acc[g][j][r] * (sq * sp0[g][r]) + sp1[g][r];
-          } else {
-            v[g][r] = acc[g][j][r];
+        for (int e = 0; e < 4; ++e) {
+          s0[g][e] = (float)acc[gate(g)][j][e];
+          if constexpr (GLU) s1[g][e] = (float)acc[gate(g) + 2][j][e];
+          if constexpr (T == DT_I8) {
+            s0[g][e] *= sq * sp0[g][e];
+            if constexpr (GLU) s1[g][e] *= sq * sp1[g][e];
+            else s0[g][e] += sp1[g][e];
           }
         }
-        if constexpr (GLU && T != DT_I8) {
-          if (a.save) {
+      if constexpr (GLU && T != DT_I8) {
+        if (a.save) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 2; ++k) {
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                put4<DT_F32>(buf + col * row_bytes<4, 32>() + (b * 8 + half * 4) * 4, (k ? s1 : s0) + b * 4);
-              float* base = static_cast<float*>(a.save) + k * a.np;
-              flush<4, 32>(buf, lane, q, a.nq, p0 + g * 32, a.np, vecs,
-                           [&](int qq) { return reinterpret_cast<char*>(base + (int64_t)qq * 2 * a.np); });
-            }
+            for (int g = 0; g < OG; ++g)
+              put4<DT_F32>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4, k ? s1[g] : s0[g]);
+            float* base = static_cast<float*>(a.save) + k * a.np;
+            flush<4, OC>(buf, lane, q, a.nq, p0, a.np, vecs,
+                         [&](int qq) { return reinterpret_cast<char*>(base + (int64_t)qq * 2 * a.np); });
           }
         }
       }
 #pragma unroll
-      for (int g = 0; g < OG; ++g)
+      for (int g = 0; g < OG; ++g) {
+        if constexpr (GLU)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint8_t* at = buf + col * row_bytes<2, OC>() + (g * 32 + b * 8 + half * 4) * 2;
-          if (a.out_dt == DT_BF16) put4<DT_BF16>(at, &v[g][b * 4]);
-          else put4<DT_F16>(at, &v[g][b * 4]);
-        }
+          for (int e = 0; e < 4; ++e) s0[g][e] = act_f(s0[g][e], a.act) * s1[g][e];
+        uint8_t* at = buf + col * row_bytes<2, OC>() + (g * 16 + quad * 4) * 2;
+        if (a.out_dt == DT_BF16) put4<DT_BF16>(at, s0[g]);
+        else put4<DT_F16>(at, s0[g]);
+      }
       flush<2, OC>(buf, lane, q, a.nq, p0, a.np, vec, [&](int qq) { return out_row(a, qq); });
     }
   }
