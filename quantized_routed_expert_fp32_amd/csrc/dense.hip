@@ -189,7 +189,7 @@ struct Dense {
   static constexpr int PB = BP * KB, QB = BQ * KB, UNIT = PB > QB ? PB : QB;   // R ring slots of UNIT bytes
   static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
   static constexpr int NK = KB / 64;               // matrix-instruction k blocks of a step
-  static constexpr int QH = FQ > 4 ? FQ / 4 : 1, QG = FQ / QH, NU = NK * QH;   // units: a k block and QG Q fragments
+  static constexpr int QH = FQ > 2 ? FQ / 2 : 1, QG = FQ / QH, NU = NK * QH;   // units: a k block and QG Q fragments
   static constexpr int CPR = KB / 16, KR = KB / 2;  // chunks of a k-contiguous row; k rows of a step
   typedef typename Elem<T>::acc4 acc_t;
   static_assert(NK % 2 == 0 && NU % 2 == 0 && QG * QH == FQ, "units");
@@ -735,15 +735,53 @@ __device__ __forceinline__ int quant1(float x, float s, float inv) {
   return (int)__builtin_fminf(__builtin_fmaxf(n, -127.f), 127.f);
 }
 
-template <int T>
+template <int T> __device__ __forceinline__ void unpack16(u32x4 v, float* f) {
+  if constexpr (T == DT_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = Row<T>::f((uint16_t)v[i]);
+      f[2 * i + 1] = Row<T>::f((uint16_t)(v[i] >> 16));
+    }
+  }
+}
+
+// One workgroup a row. Whole 16-byte chunks (VEC: rows at 16 bytes, cols and
+// ldq whole chunks) are read once, the first QUANT_HOLD a thread held in
+// registers between the maximum and the codes; longer rows are read twice
+// (from the L2). Bound by memory: 3 bytes an element for 16-bit rows.
+constexpr int QUANT_HOLD = 4;
+template <int T, bool VEC>
 __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type* x, int64_t ldx, int cols, int8_t* q,
                                                     int64_t ldq, float* scale) {
+  constexpr int N = T == DT_F32 ? 4 : 8;
   __shared__ uint32_t red[4];
   const int64_t r = blockIdx.x;
   const typename Row<T>::type* xr = x + r * ldx;
+  const int chunks = VEC ? cols / N : 0;
+  u32x4 hold[VEC ? QUANT_HOLD : 1];
   // |x| as bits: ordered as the values, infinity and NaN above them all
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < cols; i += 256) m = max(m, __float_as_uint(Row<T>::f(xr[i])) & 0x7FFFFFFFu);
+  auto top = [&](u32x4 v) {
+    float f[N];
+    unpack16<T>(v, f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  };
+  if constexpr (VEC) {
+#pragma unroll
+    for (int h = 0; h < QUANT_HOLD; ++h) {
+      const int c = h * 256 + threadIdx.x;
+      hold[h] = c < chunks ? reinterpret_cast<const u32x4*>(xr)[c] : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int h = 0; h < QUANT_HOLD; ++h) top(hold[h]);
+    for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) top(reinterpret_cast<const u32x4*>(xr)[c]);
+  } else {
+    for (int i = threadIdx.x; i < cols; i += 256) m = max(m, __float_as_uint(Row<T>::f(xr[i])) & 0x7FFFFFFFu);
+  }
 #pragma unroll
   for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -753,33 +791,95 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   const float s = fin ? __uint_as_float(m) / 127.f : __builtin_nanf("");
   if (threadIdx.x == 0) scale[r] = s;
   const float inv = s > 0.f ? 1.f / s : 0.f;
-  const bool wide = inv < 3e38f;    // a subnormal scale: its reciprocal may overflow
-  for (int64_t i = threadIdx.x; i < ldq; i += 256) {
-    int v = 0;
-    if (i < cols && s > 0.f) {
-      const float xv = Row<T>::f(xr[i]);
-      v = wide ? quant1(xv, s, inv)
-               : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)xv / (double)s), -127.0), 127.0);
+  const bool some = s > 0.f, wide = inv < 3e38f;    // a subnormal scale: its reciprocal may overflow
+  auto code = [&](float xv) {
+    if (!some) return 0;
+    return wide ? quant1(xv, s, inv)
+                : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)xv / (double)s), -127.0), 127.0);
+  };
+  int8_t* qr = q + r * ldq;
+  if constexpr (VEC) {
+    auto put = [&](int c, u32x4 v) {
+      float f[N];
+      unpack16<T>(v, f);
+      uint32_t o[N / 4];
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        o[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i] |= (uint32_t)(code(f[4 * i + e]) & 255) << (8 * e);
+      }
+      if constexpr (N == 8) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint32_t*>(qr + c * 4) = o[0];
+    };
+#pragma unroll
+    for (int h = 0; h < QUANT_HOLD; ++h) {
+      const int c = h * 256 + threadIdx.x;
+      if (c < chunks) put(c, hold[h]);
     }
-    q[r * ldq + i] = (int8_t)v;
+    for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) put(c, reinterpret_cast<const u32x4*>(xr)[c]);
+    for (int64_t i = cols + threadIdx.x; i < ldq; i += 256) qr[i] = 0;
+  } else {
+    for (int64_t i = threadIdx.x; i < ldq; i += 256) qr[i] = i < cols ? (int8_t)code(Row<T>::f(xr[i])) : (int8_t)0;
   }
 }
 
-__global__ __launch_bounds__(256) void k_glu_grad(int dt, int act, const uint16_t* dh, int64_t lddh, const float* gu,
-                                                  int inter, int ip, uint16_t* d) {
+// [dg | du] from dh and the kept g, u: 14 bytes an element through memory,
+// which bounds it. VEC: 8 elements a thread where every row starts at 16 bytes.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int inter,
+                                                  int ip, uint16_t* d) {
+  constexpr int N = VEC ? 8 : 1;
   const int64_t r = blockIdx.x;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < ip; i += gridDim.y * 256) {
-    float dg = 0.f, du = 0.f;
-    if (i < inter) {
-      const float e = from16_rt(dh[r * lddh + i], dt);
-      const float g = gu[r * 2 * inter + i], u = gu[r * 2 * inter + inter + i];
-      float v, dv;
-      act_grad_f(g, act, &v, &dv);
-      dg = e * u * dv;
-      du = e * v;
+  const float* g = gu + r * 2 * inter;
+  for (int i = (blockIdx.y * 256 + threadIdx.x) * N; i < ip; i += gridDim.y * 256 * N) {
+    float e[N], gv[N], uv[N];
+    uint16_t dg[N], du[N];
+    if constexpr (VEC) {
+      u32x4 ev = {0, 0, 0, 0};
+      f32x4 g0 = {}, g1 = {}, u0 = {}, u1 = {};
+      if (i < inter) {
+        ev = *reinterpret_cast<const u32x4*>(dh + r * lddh + i);
+        g0 = *reinterpret_cast<const f32x4*>(g + i);
+        g1 = *reinterpret_cast<const f32x4*>(g + i + 4);
+        u0 = *reinterpret_cast<const f32x4*>(g + inter + i);
+        u1 = *reinterpret_cast<const f32x4*>(g + inter + i + 4);
+      }
+      unpack16<DT>(ev, e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        gv[k] = g0[k];
+        gv[4 + k] = g1[k];
+        uv[k] = u0[k];
+        uv[4 + k] = u1[k];
+      }
+    } else {
+      const bool in = i < inter;
+      e[0] = in ? Row<DT>::f(dh[r * lddh + i]) : 0.f;
+      gv[0] = in ? g[i] : 0.f;
+      uv[0] = in ? g[inter + i] : 0.f;
     }
-    d[r * 2 * ip + i] = to16_rt(dg, dt);
-    d[r * 2 * ip + ip + i] = to16_rt(du, dt);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float v, dv;
+      act_grad_f(gv[k], act, &v, &dv);
+      dg[k] = to16<DT>(e[k] * uv[k] * dv);
+      du[k] = to16<DT>(e[k] * v);
+    }
+    uint16_t* o = d + r * 2 * ip + i;
+    if constexpr (VEC) {
+      u32x4 a, b;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] = dg[2 * k] | (uint32_t)dg[2 * k + 1] << 16;
+        b[k] = du[2 * k] | (uint32_t)du[2 * k + 1] << 16;
+      }
+      *reinterpret_cast<u32x4*>(o) = a;
+      *reinterpret_cast<u32x4*>(o + ip) = b;
+    } else {
+      o[0] = dg[0];
+      o[ip] = du[0];
+    }
   }
 }
 
@@ -856,26 +956,48 @@ hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int
   return hipGetLastError();
 }
 
+template <int T>
+static void quant_launch(const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq, float* scale,
+                         hipStream_t s) {
+  typedef typename Row<T>::type E;
+  constexpr int N = T == DT_F32 ? 4 : 8;
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % N == 0 && cols % N == 0 &&
+                   reinterpret_cast<uintptr_t>(q) % N == 0 && ldq % N == 0;
+  if (vec)
+    hipLaunchKernelGGL((k_quant_rows<T, true>), dim3(rows), dim3(256), 0, s, static_cast<const E*>(x), ldx, cols, q, ldq,
+                       scale);
+  else
+    hipLaunchKernelGGL((k_quant_rows<T, false>), dim3(rows), dim3(256), 0, s, static_cast<const E*>(x), ldx, cols, q,
+                       ldq, scale);
+}
+
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, hipStream_t s) {
-  if (dt == DT_BF16)
-    hipLaunchKernelGGL((k_quant_rows<DT_BF16>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(x), ldx, cols,
-                       q, ldq, scale);
-  else if (dt == DT_F16)
-    hipLaunchKernelGGL((k_quant_rows<DT_F16>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(x), ldx, cols,
-                       q, ldq, scale);
-  else if (dt == DT_F32)
-    hipLaunchKernelGGL((k_quant_rows<DT_F32>), dim3(rows), dim3(256), 0, s, static_cast<const float*>(x), ldx, cols, q,
-                       ldq, scale);
+  if (dt == DT_BF16) quant_launch<DT_BF16>(x, ldx, rows, cols, q, ldq, scale, s);
+  else if (dt == DT_F16) quant_launch<DT_F16>(x, ldx, rows, cols, q, ldq, scale, s);
+  else if (dt == DT_F32) quant_launch<DT_F32>(x, ldx, rows, cols, q, ldq, scale, s);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
+template <int DT>
+static void grad_launch(int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip, void* d,
+                        hipStream_t s) {
+  const bool vec = reinterpret_cast<uintptr_t>(dh) % 16 == 0 && lddh % 8 == 0 && inter % 8 == 0 &&
+                   reinterpret_cast<uintptr_t>(gu) % 16 == 0;
+  const int per = vec ? 2048 : 256;
+  const dim3 grid(rows, (ip + per - 1) / per);
+  const uint16_t* e = static_cast<const uint16_t*>(dh);
+  uint16_t* o = static_cast<uint16_t*>(d);
+  if (vec) hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
+  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
+}
+
 hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
                            int ip, void* d, hipStream_t s) {
-  hipLaunchKernelGGL(k_glu_grad, dim3(rows, std::min((ip + 255) / 256, 1024)), dim3(256), 0, s, dt, act,
-                     static_cast<const uint16_t*>(dh), lddh, gu, inter, ip,
-                     static_cast<uint16_t*>(d));
+  if (dt == DT_BF16) grad_launch<DT_BF16>(act, dh, lddh, gu, rows, inter, ip, d, s);
+  else if (dt == DT_F16) grad_launch<DT_F16>(act, dh, lddh, gu, rows, inter, ip, d, s);
+  else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
