@@ -409,41 +409,54 @@ def experts_grouped(layer, x, ids, p, sg, **kw):
 
 
 # ------------------------------------------------- dense feed-forward operators
-def _rows2d(t, name, dtypes, shape=None, like=None):
+# These calls are short (a decode step's kernel runs for a few microseconds),
+# so their checks touch each tensor attribute once and enter a device or
+# stream context only where the current one differs.
+def _rows2d(t, name, dtype, shape=None, dev=None):
     """Checks a 2-D operand whose rows are contiguous (any row stride); its row
     stride in elements (of a single row: the row length)."""
     if t.dim() != 2:
         raise MoeError(f"{name}: {t.dim()}-D tensor, needs 2 dimensions")
-    if t.dtype not in dtypes:
-        raise MoeError(f"{name}: dtype {t.dtype} is not {' or '.join(str(d) for d in dtypes)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise MoeError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
-    _same_device(t, name, like)
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise MoeError(f"{name}: the elements of a row must be contiguous (strides {tuple(t.stride())})")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dtype is not dtype:
+        raise MoeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    rows, cols = t.shape
+    if shape is not None and (rows != shape[0] or cols != shape[1]):
+        raise MoeError(f"{name}: shape {(rows, cols)}, needs {tuple(shape)}")
+    _on_device(t, name, dev)
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise MoeError(f"{name}: the elements of a row must be contiguous (strides {(ld, one)})")
+    return ld if rows > 1 else cols
 
 
-def _same_device(t, name, like):
+def _on_device(t, name, dev):
+    """Checks that t is in device memory, of device `dev` where one is given; its device index."""
     if not t.is_cuda:
         raise MoeError(f"{name}: on {t.device}, needs device memory")
-    if like is not None and t.device != like.device:
-        raise MoeError(f"{name}: on {t.device}, x is on {like.device}")
+    d = t.get_device()
+    if dev is not None and d != dev:
+        raise MoeError(f"{name}: on cuda:{d}, x is on cuda:{dev}")
+    return d
 
 
-def _flat(t, name, n, dtype, like):
-    """Checks a contiguous vector of n elements."""
+def _flat(t, name, n, dtype, dev):
+    """Checks a contiguous vector of n elements; its address."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise MoeError(f"{name}: {t.dtype} of shape {tuple(t.shape)}, needs contiguous {dtype} ({n},)")
-    _same_device(t, name, like)
+    _on_device(t, name, dev)
     return t.data_ptr()
 
 
-def _dtype_code(t):
+def _half(x, name="x"):
+    """MOE_BF16 or MOE_FP16 of a 16-bit operand."""
     import torch
-    return MOE_BF16 if t == torch.bfloat16 else MOE_FP16
+    if x.dtype is torch.bfloat16:
+        return MOE_BF16
+    if x.dtype is torch.float16:
+        return MOE_FP16
+    raise MoeError(f"{name}: dtype {x.dtype} is not torch.bfloat16 or torch.float16")
 
 
 def _act_code(act):
@@ -452,175 +465,214 @@ def _act_code(act):
     return ACTIVATIONS[act]
 
 
-class _call:
-    """The device of x current, and `stream` too where one is given: outputs and
-    the workspace of a call are allocated on the stream that uses them."""
-
-    def __init__(self, x, stream):
-        import torch
-        self.ctx = torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.device)
-        if stream is not None and stream.device != x.device:
-            raise MoeError(f"stream: on {stream.device}, x is on {x.device}")
-
-    def __enter__(self):
-        self.ctx.__enter__()
-
-    def __exit__(self, *a):
-        return self.ctx.__exit__(*a)
-
-
-def _ws_for(n, ws, x):
+def _call_ctx(dev, stream):
+    """The context of a call on device `dev`: outputs and the workspace are
+    allocated on the stream that uses them, with the device current. None
+    where the current ones already are."""
     import torch
-    if ws is None and n:
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    if stream is not None:
+        if stream.device.index != dev:
+            raise MoeError(f"stream: on {stream.device}, x is on cuda:{dev}")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _raw_stream(dev, stream):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _workspace(n, ws, dev):
+    """(address, bytes, owner) of the workspace of a call that needs n bytes."""
+    import torch
     if ws is None:
-        return None, 0, None
+        if not n:
+            return None, 0, None
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), n, ws
     if not ws.is_contiguous():
         raise MoeError("ws: needs contiguous memory")
-    _same_device(ws, "ws", x)
-    return C.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+    _on_device(ws, "ws", dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def _glu_args(x, w_gate, w_up, act, s_gate=None, s_up=None, x_scale=None, out_dtype=None):
+    """(argument block, output dtype, device index) of a gated-block call."""
     import torch
-    half = (torch.bfloat16, torch.float16)
     i8 = s_gate is not None
-    ldx = _rows2d(x, "x", (torch.int8,) if x_scale is not None else half)
-    wt = (torch.int8,) if i8 else (x.dtype,)
-    ldg = _rows2d(w_gate, "w_gate", wt, like=x)
+    if x_scale is None:
+        dt = x.dtype
+        code = _half(x)
+        ldx = _rows2d(x, "x", dt)
+        if out_dtype is not None and out_dtype is not dt:
+            raise MoeError(f"out_dtype: {out_dtype} with x of {dt} (it is a choice for int8 x only)")
+    else:
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        if dt not in (torch.bfloat16, torch.float16):
+            raise MoeError(f"out_dtype: {dt} is not torch.bfloat16 or torch.float16")
+        code = MOE_BF16 if dt is torch.bfloat16 else MOE_FP16
+        ldx = _rows2d(x, "x", torch.int8)
+    dev = x.get_device()
+    wt = torch.int8 if i8 else dt
+    ldg = _rows2d(w_gate, "w_gate", wt, None, dev)
+    R, K = x.shape
     I, H = w_gate.shape
-    if x.shape[1] != H:
-        raise MoeError(f"x: rows of {x.shape[1]} elements, w_gate has {H} columns")
-    ldu = _rows2d(w_up, "w_up", wt, shape=(I, H), like=x)
-    dt = out_dtype if x_scale is not None else x.dtype
-    a = GluC(x.shape[0], H, I, _dtype_code(dt), _act_code(act), w_gate.data_ptr(), w_up.data_ptr(), ldg, ldu,
-             None, None, x.data_ptr(), ldx, None)
-    if i8:
-        a.s_gate = _flat(s_gate, "s_gate", I, torch.float32, x)
-        a.s_up = _flat(s_up, "s_up", I, torch.float32, x)
-        a.s_x = _flat(x_scale, "x_scale", x.shape[0], torch.float32, x)
-    return a, dt
+    if K != H:
+        raise MoeError(f"x: rows of {K} elements, w_gate has {H} columns")
+    ldu = _rows2d(w_up, "w_up", wt, (I, H), dev)
+    f32 = torch.float32
+    a = GluC(R, H, I, code, _act_code(act), w_gate.data_ptr(), w_up.data_ptr(), ldg, ldu,
+             _flat(s_gate, "s_gate", I, f32, dev), _flat(s_up, "s_up", I, f32, dev), x.data_ptr(), ldx,
+             _flat(x_scale, "x_scale", R, f32, dev))
+    return a, dt, dev
+
+
+def _glu_need(a, kind):
+    n = C.c_uint64()
+    st = lib().moe_glu_workspace_size(C.byref(a), kind, C.byref(n))
+    if st:
+        _check(st, "moe_glu_workspace_size")
+    return n.value
 
 
 def glu_workspace_size(x, w_gate, w_up, kind=MOE_GLU_FORWARD, s_gate=None, s_up=None, x_scale=None) -> int:
     """moe_glu_workspace_size of a call on these tensors, in bytes."""
-    import torch
-    a, _ = _glu_args(x, w_gate, w_up, "silu", s_gate, s_up, x_scale, torch.bfloat16)
-    n = C.c_uint64()
-    _check(lib().moe_glu_workspace_size(C.byref(a), kind, C.byref(n)), "moe_glu_workspace_size")
-    return n.value
+    return _glu_need(_glu_args(x, w_gate, w_up, "silu", s_gate, s_up, x_scale)[0], kind)
 
 
 def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=None, stream=None):
     """moe_glu_forward: h = act(x w_gate^T) * (x w_up^T), [rows, inter] of x's
     dtype (bf16 or fp16); with save=True (h, gu), gu fp32 [rows, 2, inter] being what
     glu_backward takes."""
+    a, dt, dev = _glu_args(x, w_gate, w_up, act)
+    ctx = _call_ctx(dev, stream)
+    if ctx is None:
+        return _glu_forward(a, dt, dev, save, h, gu, ws, stream)
+    with ctx:
+        return _glu_forward(a, dt, dev, save, h, gu, ws, stream)
+
+
+def _glu_forward(a, dt, dev, save, h, gu, ws, stream):
     import torch
-    a, dt = _glu_args(x, w_gate, w_up, act)
     R, I = a.rows, a.inter
-    with _call(x, stream):
-        if h is None:
-            h = torch.empty((R, I), dtype=dt, device=x.device)
-        ldh = _rows2d(h, "h", (dt,), (R, I), x)
-        if save and gu is None:
-            gu = torch.empty((R, 2, I), dtype=torch.float32, device=x.device)
-        if gu is not None:
-            _gu_ok(gu, R, I, x)
-        n = C.c_uint64()
-        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_FORWARD, C.byref(n)), "moe_glu_workspace_size")
-        wp, wn, ws = _ws_for(n.value, ws, x)
-        _check(lib().moe_glu_forward(C.byref(a), _ptr(h), ldh, _ptr(gu), wp, wn, _stream_ptr(stream)),
-               "moe_glu_forward")
+    n = _glu_need(a, MOE_GLU_FORWARD)
+    if h is None:
+        h, ldh = torch.empty((R, I), dtype=dt, device=dev), I
+    else:
+        ldh = _rows2d(h, "h", dt, (R, I), dev)
+    gp = None
+    if gu is not None:
+        gp = _gu_ok(gu, R, I, dev)
+    elif save:
+        gu = torch.empty((R, 2, I), dtype=torch.float32, device=dev)
+        gp = gu.data_ptr()
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_glu_forward(C.byref(a), h.data_ptr(), ldh, gp, wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_glu_forward")
     return (h, gu) if gu is not None else h
 
 
-def _gu_ok(gu, R, I, x):
+def _gu_ok(gu, R, I, dev):
     import torch
-    if gu.dtype != torch.float32 or tuple(gu.shape) != (R, 2, I) or not gu.is_contiguous():
+    if gu.dtype is not torch.float32 or tuple(gu.shape) != (R, 2, I) or not gu.is_contiguous():
         raise MoeError(f"gu: {gu.dtype} of shape {tuple(gu.shape)}, needs contiguous torch.float32 ({R}, 2, {I})")
-    _same_device(gu, "gu", x)
+    _on_device(gu, "gu", dev)
+    return gu.data_ptr()
 
 
 def glu_backward(dh, x, w_gate, w_up, gu, act="silu", need_dx=True, need_dw=True, dx=None, dw_gate=None,
                  dw_up=None, ws=None, stream=None):
     """moe_glu_backward: (dx, dw_gate, dw_up) of glu_forward(..., save=True) from
     dh and its gu; None in the place of a gradient that is not needed."""
-    import torch
-    a, dt = _glu_args(x, w_gate, w_up, act)
-    R, H, I = a.rows, a.hidden, a.inter
-    _gu_ok(gu, R, I, x)
-    lddh = _rows2d(dh, "dh", (dt,), (R, I), x)
+    a, dt, dev = _glu_args(x, w_gate, w_up, act)
     if not need_dx and not need_dw:
         raise MoeError("glu_backward: neither need_dx nor need_dw")
-    with _call(x, stream):
-        lddx = 0
-        if need_dx:
-            if dx is None:
-                dx = torch.empty((R, H), dtype=dt, device=x.device)
-            lddx = _rows2d(dx, "dx", (dt,), (R, H), x)
-        if need_dw:
-            if dw_gate is None:
-                dw_gate = torch.empty((I, H), dtype=dt, device=x.device)
-            if dw_up is None:
-                dw_up = torch.empty((I, H), dtype=dt, device=x.device)
-            for t, nm in ((dw_gate, "dw_gate"), (dw_up, "dw_up")):
-                if _rows2d(t, nm, (dt,), (I, H), x) != H:
-                    raise MoeError(f"{nm}: needs contiguous memory")
-        dx, dw_gate, dw_up = dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None
-        n = C.c_uint64()
-        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_BACKWARD, C.byref(n)), "moe_glu_workspace_size")
-        wp, wn, ws = _ws_for(n.value, ws, x)
-        _check(lib().moe_glu_backward(C.byref(a), _ptr(gu), _ptr(dh), lddh, _ptr(dx), lddx, _ptr(dw_gate),
-                                      _ptr(dw_up), wp, wn, _stream_ptr(stream)), "moe_glu_backward")
-    return dx, dw_gate, dw_up
+    lddh = _rows2d(dh, "dh", dt, (a.rows, a.inter), dev)
+    gp = _gu_ok(gu, a.rows, a.inter, dev)
+    outs = (dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None)
+    ctx = _call_ctx(dev, stream)
+    if ctx is None:
+        return _glu_backward(a, dt, dev, dh.data_ptr(), lddh, gp, need_dx, need_dw, outs, ws, stream)
+    with ctx:
+        return _glu_backward(a, dt, dev, dh.data_ptr(), lddh, gp, need_dx, need_dw, outs, ws, stream)
+
+
+def _glu_backward(a, dt, dev, dhp, lddh, gp, need_dx, need_dw, outs, ws, stream):
+    import torch
+    R, H, I = a.rows, a.hidden, a.inter
+    n = _glu_need(a, MOE_GLU_BACKWARD)
+    dx, dwg, dwu = outs
+    lddx = H
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((R, H), dtype=dt, device=dev)
+        else:
+            lddx = _rows2d(dx, "dx", dt, (R, H), dev)
+    if need_dw:
+        if dwg is None:
+            dwg = torch.empty((I, H), dtype=dt, device=dev)
+        elif _rows2d(dwg, "dw_gate", dt, (I, H), dev) != H:
+            raise MoeError("dw_gate: needs contiguous memory")
+        if dwu is None:
+            dwu = torch.empty((I, H), dtype=dt, device=dev)
+        elif _rows2d(dwu, "dw_up", dt, (I, H), dev) != H:
+            raise MoeError("dw_up: needs contiguous memory")
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_glu_backward(C.byref(a), gp, dhp, lddh, dx.data_ptr() if need_dx else None, lddx,
+                                dwg.data_ptr() if need_dw else None, dwu.data_ptr() if need_dw else None, wp, wn,
+                                _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_glu_backward")
+    return dx, dwg, dwu
 
 
 def glu_i8(x, w_gate, s_gate, w_up, s_up, act="silu", x_scale=None, out_dtype=None, h=None, ws=None, stream=None):
     """moe_glu_i8: the gated block on int8 weights [inter, hidden] with fp32
     channel scales [inter]; x in bf16/fp16 (quantised a token inside the call),
     or int8 with x_scale [rows] (then out_dtype is h's type, bf16 by default)."""
+    if s_gate is None or s_up is None:
+        raise MoeError("s_gate, s_up: needed with int8 weights")
+    a, dt, dev = _glu_args(x, w_gate, w_up, act, s_gate, s_up, x_scale, out_dtype)
+    ctx = _call_ctx(dev, stream)
+    if ctx is None:
+        return _glu_i8(a, dt, dev, h, ws, stream)
+    with ctx:
+        return _glu_i8(a, dt, dev, h, ws, stream)
+
+
+def _glu_i8(a, dt, dev, h, ws, stream):
     import torch
-    a, dt = _glu_args(x, w_gate, w_up, act, s_gate, s_up, x_scale, _out_dtype(out_dtype, x, x_scale))
-    R, I = a.rows, a.inter
-    with _call(x, stream):
-        if h is None:
-            h = torch.empty((R, I), dtype=dt, device=x.device)
-        ldh = _rows2d(h, "h", (dt,), (R, I), x)
-        n = C.c_uint64()
-        _check(lib().moe_glu_workspace_size(C.byref(a), MOE_GLU_I8, C.byref(n)), "moe_glu_workspace_size")
-        wp, wn, ws = _ws_for(n.value, ws, x)
-        _check(lib().moe_glu_i8(C.byref(a), _ptr(h), ldh, wp, wn, _stream_ptr(stream)), "moe_glu_i8")
+    n = _glu_need(a, MOE_GLU_I8)
+    if h is None:
+        h, ldh = torch.empty((a.rows, a.inter), dtype=dt, device=dev), a.inter
+    else:
+        ldh = _rows2d(h, "h", dt, (a.rows, a.inter), dev)
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_glu_i8(C.byref(a), h.data_ptr(), ldh, wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_glu_i8")
     return h
-
-
-def _out_dtype(out_dtype, x, x_scale):
-    import torch
-    if out_dtype is None:
-        return torch.bfloat16
-    if x_scale is None and out_dtype != x.dtype:
-        raise MoeError(f"out_dtype: {out_dtype} with x of {x.dtype} (it is a choice for int8 x only)")
-    if out_dtype not in (torch.bfloat16, torch.float16):
-        raise MoeError(f"out_dtype: {out_dtype} is not torch.bfloat16 or torch.float16")
-    return out_dtype
 
 
 def quant_rows(x, q=None, scale=None, stream=None):
     """moe_quant_rows: rows of x (bf16, fp16 or fp32) as (int8 [rows, cols],
     fp32 scale [rows]); of a weight matrix [out, in] the rows are its channels."""
     import torch
-    ldx = _rows2d(x, "x", (torch.bfloat16, torch.float16, torch.float32))
-    R, K = x.shape
-    with _call(x, stream):
+    code = MOE_FP32 if x.dtype is torch.float32 else _half(x)
+    ldx = _rows2d(x, "x", x.dtype)
+    dev = x.get_device()
+    ctx = _call_ctx(dev, stream)
+    with ctx if ctx is not None else _nullctx():
+        R, K = x.shape
         if q is None:
-            q = torch.empty((R, K), dtype=torch.int8, device=x.device)
-        if scale is None:
-            scale = torch.empty((R,), dtype=torch.float32, device=x.device)
-        ldq = _rows2d(q, "q", (torch.int8,), (R, K), x)
-        if ldq != K:
+            q = torch.empty((R, K), dtype=torch.int8, device=dev)
+        elif _rows2d(q, "q", torch.int8, (R, K), dev) != K:
             raise MoeError("q: needs contiguous memory")
-        sp = _flat(scale, "scale", R, torch.float32, x)
-        code = MOE_FP32 if x.dtype == torch.float32 else _dtype_code(x.dtype)
-        _check(lib().moe_quant_rows(_ptr(x), code, R, K, ldx, _ptr(q), ldq, C.c_void_p(sp), _stream_ptr(stream)),
+        if scale is None:
+            scale = torch.empty((R,), dtype=torch.float32, device=dev)
+        sp = _flat(scale, "scale", R, torch.float32, dev)
+        _check(lib().moe_quant_rows(x.data_ptr(), code, R, K, ldx, q.data_ptr(), K, sp, _raw_stream(dev, stream)),
                "moe_quant_rows")
     return q, scale
 
@@ -630,23 +682,48 @@ def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=Non
     scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
     int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default)."""
     import torch
-    ldx = _rows2d(x, "x", (torch.int8,) if x_scale is not None else (torch.bfloat16, torch.float16))
-    ldw = _rows2d(w, "w", (torch.int8,), like=x)
+    f32 = torch.float32
+    if x_scale is None:
+        dt = x.dtype
+        code = _half(x)
+        ldx = _rows2d(x, "x", dt)
+        if out_dtype is not None and out_dtype is not dt:
+            raise MoeError(f"out_dtype: {out_dtype} with x of {dt} (it is a choice for int8 x only)")
+    else:
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        if dt not in (torch.bfloat16, torch.float16):
+            raise MoeError(f"out_dtype: {dt} is not torch.bfloat16 or torch.float16")
+        code = MOE_BF16 if dt is torch.bfloat16 else MOE_FP16
+        ldx = _rows2d(x, "x", torch.int8)
+    dev = x.get_device()
+    ldw = _rows2d(w, "w", torch.int8, None, dev)
     N, K = w.shape
-    if x.shape[1] != K:
-        raise MoeError(f"x: rows of {x.shape[1]} elements, w has {K} columns")
-    R = x.shape[0]
-    dt = _out_dtype(out_dtype, x, x_scale)
-    dt = dt if x_scale is not None else x.dtype
-    a = LinearC(R, K, N, _dtype_code(dt), w.data_ptr(), ldw, _flat(s_w, "s_w", N, torch.float32, x),
-                _flat(bias, "bias", N, torch.float32, x), x.data_ptr(), ldx,
-                _flat(x_scale, "x_scale", R, torch.float32, x))
-    with _call(x, stream):
-        if y is None:
-            y = torch.empty((R, N), dtype=dt, device=x.device)
-        ldy = _rows2d(y, "y", (dt,), (R, N), x)
-        n = C.c_uint64()
-        _check(lib().moe_linear_i8_workspace_size(C.byref(a), C.byref(n)), "moe_linear_i8_workspace_size")
-        wp, wn, ws = _ws_for(n.value, ws, x)
-        _check(lib().moe_linear_i8(C.byref(a), _ptr(y), ldy, wp, wn, _stream_ptr(stream)), "moe_linear_i8")
+    R, Kx = x.shape
+    if Kx != K:
+        raise MoeError(f"x: rows of {Kx} elements, w has {K} columns")
+    if s_w is None:
+        raise MoeError("s_w: needed with int8 weights")
+    a = LinearC(R, K, N, code, w.data_ptr(), ldw, _flat(s_w, "s_w", N, f32, dev), _flat(bias, "bias", N, f32, dev),
+                x.data_ptr(), ldx, _flat(x_scale, "x_scale", R, f32, dev))
+    ctx = _call_ctx(dev, stream)
+    if ctx is None:
+        return _linear_i8(a, dt, dev, y, ws, stream)
+    with ctx:
+        return _linear_i8(a, dt, dev, y, ws, stream)
+
+
+def _linear_i8(a, dt, dev, y, ws, stream):
+    import torch
+    n = C.c_uint64()
+    st = lib().moe_linear_i8_workspace_size(C.byref(a), C.byref(n))
+    if st:
+        _check(st, "moe_linear_i8_workspace_size")
+    if y is None:
+        y, ldy = torch.empty((a.rows, a.out), dtype=dt, device=dev), a.out
+    else:
+        ldy = _rows2d(y, "y", dt, (a.rows, a.out), dev)
+    wp, wn, ws = _workspace(n.value, ws, dev)
+    st = lib().moe_linear_i8(C.byref(a), y.data_ptr(), ldy, wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_linear_i8")
     return y
