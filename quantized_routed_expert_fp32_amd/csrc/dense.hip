@@ -109,16 +109,15 @@ __device__ __forceinline__ bool vec_ok(const void* p, int64_t ld, int es) {
 }
 
 // The epilogues on four consecutive columns p.. of row q. `s0` and `s1` are
-// the sums (gate and up for GLU) as fp32 or int32.
+// the sums (gate and up for GLU) as fp32 or int32, `sq` the row's scale.
 template <int T, int EPI, typename V>
-__device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const V* s0, const V* s1) {
+__device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const V* s0, const V* s1, float sq) {
   if (q >= a.nq || p >= a.np) return;
   float v[4], g[4], u[4];
   if constexpr (EPI == EPI_GLU) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (T == DT_I8) {
-        const float sq = a.sq[q];
         const int pi = min(p + i, a.np - 1);
         g[i] = (float)s0[i] * (sq * a.sp0[pi]);
         u[i] = (float)s1[i] * (sq * a.sp1[pi]);
@@ -135,7 +134,6 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
       store4(sv + a.np, p, a.np, DT_F32, vec, u);
     }
   } else if constexpr (EPI == EPI_SCALE) {
-    const float sq = a.sq[q];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pi = min(p + i, a.np - 1);
@@ -180,7 +178,7 @@ __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 // reading one chunk of 16 rows meet 16 different bank groups. k-major
 // operand: rows k of 2 B bytes, 32-byte segment s at s ^ swz_km(k), so the 4
 // rows of a transposed read do.
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB, int KU>
 struct Dense {
   static constexpr int RPM = 1;                    // fragment reads a product
   static constexpr bool PKM = FORM != FORM_NT, QKM = FORM == FORM_TN;
@@ -189,14 +187,14 @@ struct Dense {
   static constexpr int PB = BP * KB, QB = BQ * KB, UNIT = PB > QB ? PB : QB;   // R ring slots of UNIT bytes
   static constexpr int LP = PB / (NW * 1024), LQ = QB / (NW * 1024);
   static constexpr int NK = KB / 64;               // matrix-instruction k blocks of a step
-  static constexpr int QH = FQ > 2 ? FQ / 2 : 1, QG = FQ / QH, NU = NK * QH;   // units: a k block and QG Q fragments
+  static constexpr int QH = KU == 1 && FQ > 2 ? FQ / 2 : 1, QG = FQ / QH, NU = NK / KU * QH;   // units: KU k blocks, QG Q fragments
   static constexpr int CPR = KB / 16, KR = KB / 2;  // chunks of a k-contiguous row; k rows of a step
   typedef typename Elem<T>::acc4 acc_t;
-  static_assert(NK % 2 == 0 && NU % 2 == 0 && QG * QH == FQ, "units");
+  static_assert(NK / KU % 2 == 0 && NK % KU == 0 && QG * QH == FQ, "units");
   static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB && LP == LQ, "whole loads");
   static_assert(R % 2 == 1 && R >= 5, "ring");
 
-  static __device__ __forceinline__ int swz_kc(int r) { return KB == 128 ? r & 7 : (r >> 2) & 3; }
+  static __device__ __forceinline__ int swz_kc(int r) { return KB >= 128 ? r & 7 : (r >> 2) & 3; }
   // the same for k and k + 4
   template <int B> static __device__ __forceinline__ int swz_km(int k) {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
@@ -332,7 +330,8 @@ struct Dense {
     // the step behind segment sg's whole ones into slots 0 and 1, zero past the operands' end
     auto load_rest = [&](int sg) {
       const Src rp = source_p(sg, nws, 0), rq = source_q(sg, nws, 1);
-      const int kr = a.krows - nws * KR, kb = a.kbytes - nws * KB - (sg ? a.segbytes : 0);
+      const int kr = a.krows - nws * KR;
+      const int kb = (NSEG == 1 ? a.kbytes : sg ? a.kbytes - a.segbytes : a.segbytes) - nws * KB;
 #pragma unroll
       for (int n = 0; n < LP; ++n) {
         const int q = (n * NW + w) * 64 + lane;
@@ -349,31 +348,38 @@ struct Dense {
 #pragma unroll
       for (int j = 0; j < FQ; ++j) acc[i][j] = acc_t{};
 
-    // A unit is a k block (64 bytes of k) and QG of the wave's Q fragments.
+    // A unit is KU k blocks (64 bytes of k each) and QG of the wave's Q fragments.
     const int col = lane & 15, quad = lane >> 4;
-    u32x4 fp[2][FP], fq[2][QG];
-    auto frag_p = [&](int sp, int kk, int i) {
+    u32x4 fp[2][KU][FP], fq[2][KU][QG];
+    auto frag_p = [&](int sp, int u, int kb, int i) {
       const uint8_t* pt = smem + sp * UNIT;
-      if constexpr (PKM) fp[kk & 1][i] = frag_km<BP>(pt, wp * TP + i * 16, kk, lane);
-      else fp[kk & 1][i] = frag_kc(pt, wp * TP + i * 16 + col, kk, quad);
+      const int kk = u / QH * KU + kb;
+      if constexpr (PKM) fp[u / QH & 1][kb][i] = frag_km<BP>(pt, wp * TP + i * 16, kk, lane);
+      else fp[u / QH & 1][kb][i] = frag_kc(pt, wp * TP + i * 16 + col, kk, quad);
     };
-    auto frag_q = [&](int sq, int u, int j) {
+    auto frag_q = [&](int sq, int u, int kb, int j) {
       const uint8_t* qt = smem + sq * UNIT;
-      const int kk = u / QH, jj = u % QH * QG + j;
-      if constexpr (QKM) fq[u & 1][j] = frag_km<BQ>(qt, wq * TQ + jj * 16, kk, lane);
-      else fq[u & 1][j] = frag_kc(qt, wq * TQ + jj * 16 + col, kk, quad);
+      const int kk = u / QH * KU + kb, jj = u % QH * QG + j;
+      if constexpr (QKM) fq[u & 1][kb][j] = frag_km<BQ>(qt, wq * TQ + jj * 16, kk, lane);
+      else fq[u & 1][kb][j] = frag_kc(qt, wq * TQ + jj * 16 + col, kk, quad);
     };
-    // read x of unit u, in the order its products need them: P 0, the Qs, the other Ps
+    // read x of unit u, in the order its products need them: a k block's P 0,
+    // its Qs, its other Ps
     auto frag1 = [&](int sp, int sq, int u, int x) {
-      if (u % QH != 0) frag_q(sq, u, x);
-      else if (x == 0 || x > QG) frag_p(sp, u / QH, x == 0 ? 0 : x - QG);
-      else frag_q(sq, u, x - 1);
+      if (u % QH != 0) {
+        frag_q(sq, u, x / QG, x % QG);
+      } else {
+        const int kb = x / (FP + QG), y = x % (FP + QG);
+        if (y == 0 || y > QG) frag_p(sp, u, kb, y == 0 ? 0 : y - QG);
+        else frag_q(sq, u, kb, y - 1);
+      }
     };
-    constexpr int NM = FP * QG;
+    constexpr int NM = KU * FP * QG;
+    auto reads = [](int u) { return KU * (u % QH ? QG : FP + QG); };
     auto mma1 = [&](int u, int n) {
-      const int i = n / QG, j = n % QG;
+      const int kb = n / (FP * QG), i = n / QG % FP, j = n % QG;
       acc_t& c = acc[i][u % QH * QG + j];
-      c = Elem<T>::mma16(fp[u / QH & 1][i], fq[u & 1][j], c);
+      c = Elem<T>::mma16(fp[u / QH & 1][kb][i], fq[u & 1][kb][j], c);
     };
 
     // Ring of R slots, a step's P and Q halves in turn: half 2 t (P) and 2 t + 1
@@ -401,12 +407,15 @@ struct Dense {
       if (halves >= R) step_wait<(R - 2) * LP>();
       else step_wait<0>();
 #pragma unroll
-      for (int x = 0; x < FP + QG; ++x) frag1(0, 1, 0, x);
+      for (int x = 0; x < reads(0); ++x) frag1(0, 1, 0, x);
       // opaque, or the compiler merges these reads with the loop's own
 #pragma unroll
-      for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fp[0][i]));
+      for (int kb = 0; kb < KU; ++kb) {
 #pragma unroll
-      for (int j = 0; j < QG; ++j) asm volatile("" : "+v"(fq[0][j]));
+        for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fp[0][kb][i]));
+#pragma unroll
+        for (int j = 0; j < QG; ++j) asm volatile("" : "+v"(fq[0][kb][j]));
+      }
       int sp = 0, sq = 1;
       Src rp = src(true, t0, 0);
       bool more_p = false;
@@ -415,7 +424,7 @@ struct Dense {
         // unit u's products, between them the reads of unit v of the step in
         // slots fsp, fsq, and some of the loads
         auto unit = [&](int u, int fsp, int fsq, int v, auto loads) {
-          const int nf = v % QH ? QG : FP + QG;
+          const int nf = reads(v);
 #pragma unroll
           for (int n = 0; n < NM; ++n) {
             mma1(u, n);
@@ -462,7 +471,7 @@ struct Dense {
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
 #pragma unroll
-          for (int x = 0; x < (u % QH ? QG : FP + QG); ++x) frag1(0, 1, u, x);
+          for (int x = 0; x < reads(u); ++x) frag1(0, 1, u, x);
 #pragma unroll
           for (int n = 0; n < NM; ++n) mma1(u, n);
         }
@@ -601,15 +610,15 @@ struct Dense {
   }
 };
 
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB, int KU>
 __global__ __launch_bounds__(WP * WQ * 64) void k_dense(DenseArgs a) {
-  Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB>::run(a);
+  Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB, KU>::run(a);
 }
 
 // Joins the K ranges of a split product, range 0 first, and runs its epilogue.
 template <int T, int EPI>
 __global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
-  const int p = (blockIdx.x * 256 + threadIdx.x) * 4, q = blockIdx.y;
+  const int p = (blockIdx.y * 256 + threadIdx.x) * 4, q = blockIdx.x;
   if (p >= a.np) return;
   typedef typename Elem<T>::acc4 acc4;
   const int64_t stride = (int64_t)a.nq * a.pcols;
@@ -626,90 +635,10 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
     s0[e] = v0[e];
     s1[e] = v1[e];
   }
-  finish4<T, EPI>(a, q, p, s0, s1);
+  finish4<T, EPI>(a, q, p, s0, s1, T == DT_I8 ? a.sq[q] : 1.f);
 }
 
-// --------------------------------------------------------------- decode rows
-// nq <= 16: a workgroup of 16 waves computes 16 weight rows (GLU: 8 gate and
-// 8 up) against every activation row on 16x16 matrix instructions; the waves
-// take 64-byte K blocks in turn and their sums join through LDS.
-template <int T>
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int64_t byte, int64_t end) {
-  u32x4 v = {0, 0, 0, 0};
-  if (byte + 16 <= end) {
-    __builtin_memcpy(&v, row + byte, 16);
-  } else {
-    uint8_t* b = reinterpret_cast<uint8_t*>(&v);
-    constexpr int ES = Elem<T>::SIZE;
-#pragma unroll
-    for (int i = 0; i < 16; i += ES)
-      if (byte + i < end) __builtin_memcpy(b + i, row + byte + i, ES);
-  }
-  return v;
-}
-
-template <int T, int EPI>
-__global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
-  const DenseArgs& a = da.d;
-  typedef typename Elem<T>::acc4 acc4;
-  __shared__ __align__(16) uint8_t red[16 * 1024];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int r = lane & 15, c = lane >> 4;
-  constexpr int OP = EPI == EPI_GLU ? 8 : 16;
-  const int p0 = blockIdx.x * OP;
-  const uint8_t* pr;
-  if (EPI == EPI_GLU) {
-    const int p = min(p0 + (r & 7), a.np - 1);
-    pr = r < 8 ? a.p0 + (int64_t)p * a.ldp0 : a.p1 + (int64_t)p * a.ldp1;
-  } else {
-    pr = a.p0 + (int64_t)min(p0 + r, a.np - 1) * a.ldp0;
-  }
-  const uint8_t* qr = a.q0 + (int64_t)min(r, a.nq - 1) * a.ldq;
-  const int64_t kb = (int64_t)da.k * Elem<T>::SIZE;
-  const int nblk = (int)((kb + 63) / 64);
-  acc4 acc = {};
-  constexpr int U = 4;
-  for (int b = w; b < nblk; b += 16 * U) {
-    u32x4 pv[U], qv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t byte = (int64_t)(b + u * 16) * 64 + c * 16;
-      pv[u] = load_chunk<T>(pr, byte, kb);
-      qv[u] = load_chunk<T>(qr, byte, kb);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) acc = Elem<T>::mma16(pv[u], qv[u], acc);
-  }
-  // lane: q = lane % 16, p = 4 (lane / 16) + e; red[w][q][p]
-  acc4* rd = reinterpret_cast<acc4*>(red);
-  rd[w * 64 + r * 4 + c] = acc;
-  __syncthreads();
-  typedef decltype(acc[0] + 0) V;
-  if (threadIdx.x < (EPI == EPI_GLU ? 32 : 64)) {
-    constexpr int PG = OP / 4;
-    const int q = threadIdx.x / PG, g = threadIdx.x % PG;
-    acc4 v0 = {}, v1 = {};
-    for (int i = 0; i < 16; ++i) {
-      v0 += rd[i * 64 + q * 4 + g];
-      if constexpr (EPI == EPI_GLU) v1 += rd[i * 64 + q * 4 + 2 + g];
-    }
-    V s0[4], s1[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s0[e] = v0[e];
-      s1[e] = v1[e];
-    }
-    finish4<T, EPI>(a, q, p0 + g * 4, s0, s1);
-  }
-}
-
-// ----------------------------------------------------------- small kernels
-template <typename E>
-__global__ __launch_bounds__(256) void k_dense_pad(const E* src, int64_t ld, int cols, E* dst, int64_t ldd) {
-  const int64_t r = blockIdx.x;
-  for (int64_t i = threadIdx.x; i < ldd; i += 256) dst[r * ldd + i] = i < cols ? src[r * ld + i] : (E)0;
-}
-
+// ---------------------------------------------------------------- quantising
 template <int T> struct Row;
 template <> struct Row<DT_BF16> {
   typedef uint16_t type;
@@ -748,6 +677,205 @@ template <int T> __device__ __forceinline__ void unpack16(u32x4 v, float* f) {
   }
 }
 
+// Scale, reciprocal (0: every code is 0) of a row whose largest |x| has the
+// bits m, and the code of one value.
+struct RowScale {
+  float s, inv;
+  bool wide;    // the reciprocal does not overflow (it may for a subnormal scale)
+  __device__ __forceinline__ explicit RowScale(uint32_t m) {
+    s = m < 0x7F800000u ? __uint_as_float(m) / 127.f : __builtin_nanf("");
+    inv = s > 0.f ? 1.f / s : 0.f;
+    wide = inv < 3e38f;
+  }
+  __device__ __forceinline__ int code(float x) const {
+    if (!(s > 0.f)) return 0;
+    return wide ? quant1(x, s, inv)
+                : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)x / (double)s), -127.0), 127.0);
+  }
+};
+template <int T, int N> __device__ __forceinline__ uint32_t top_bits(const float* f, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  return m;
+}
+__device__ __forceinline__ uint32_t codes4(const RowScale& rs, const float* f) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o |= (uint32_t)(rs.code(f[e]) & 255) << (8 * e);
+  return o;
+}
+
+// --------------------------------------------------------------- decode rows
+// nq <= 16: a workgroup of 16 waves computes 16 weight rows (GLU: 8 gate and
+// 8 up) against every activation row on 16x16 matrix instructions; the waves
+// take 256-byte K chunks in turn (a chunk's loads in flight while the one
+// before it is multiplied) and their sums join through LDS. Operands come
+// straight from memory at any alignment: bound by the weights' bytes, or by
+// latency when there are few. XT = DT_BF16 / DT_F16 (8-bit weights only): x is
+// quantised by every workgroup into LDS, while its first weights arrive.
+template <int T>
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int64_t byte, int64_t end) {
+  u32x4 v = {0, 0, 0, 0};
+  if (byte + 16 <= end) {
+    __builtin_memcpy(&v, row + byte, 16);
+  } else {
+    uint8_t* b = reinterpret_cast<uint8_t*>(&v);
+    constexpr int ES = Elem<T>::SIZE;
+#pragma unroll
+    for (int i = 0; i < 16; i += ES)
+      if (byte + i < end) __builtin_memcpy(b + i, row + byte + i, ES);
+  }
+  return v;
+}
+
+constexpr int DEC_QUANT = 32;     // elements a thread quantises at most: nq k <= 1024 * 32
+
+template <int T, int EPI, int XT, int NF>
+__global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
+  const DenseArgs& a = da.d;
+  typedef typename Elem<T>::acc4 acc4;
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int RED = NF * 16384;
+  uint8_t* const red = smem;                       // the waves' sums
+  float* const s_sq = reinterpret_cast<float*>(smem + RED);                  // 16 row scales
+  uint32_t* const s_top = reinterpret_cast<uint32_t*>(smem + RED + 64);      // 16 waves' maxima
+  uint8_t* const s_x = smem + RED + 128;         // quantised rows
+  constexpr bool QUANT = XT != DT_I8 && T == DT_I8;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  constexpr int OP = EPI == EPI_GLU ? 8 : 16;
+  const int p0 = blockIdx.x * OP * NF;
+  const uint8_t* pr[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    if (EPI == EPI_GLU) {
+      const int p = min(p0 + f * OP + (r & 7), a.np - 1);
+      pr[f] = r < 8 ? a.p0 + (int64_t)p * a.ldp0 : a.p1 + (int64_t)p * a.ldp1;
+    } else {
+      pr[f] = a.p0 + (int64_t)min(p0 + f * OP + r, a.np - 1) * a.ldp0;
+    }
+  }
+  const uint8_t* const qr = a.q0 + (int64_t)min(r, a.nq - 1) * a.ldq;
+  const int64_t kb = (int64_t)da.k * Elem<T>::SIZE;
+  const int chunks = (int)((kb + 255) / 256);
+  const int xs = QUANT ? chunks * 256 + 16 : 0;    // bytes of a quantised row in LDS (off a bank period)
+  constexpr int U = 4;
+  u32x4 pv[2][NF][U], qv[2][U];
+  auto load_p = [&](int buf, int ch) {
+    const int64_t at = (int64_t)ch * 256 + c * 16;
+    if ((int64_t)(ch + 1) * 256 <= kb) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int u = 0; u < U; ++u) __builtin_memcpy(&pv[buf][f][u], pr[f] + at + u * 64, 16);
+    } else {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int u = 0; u < U; ++u) pv[buf][f][u] = load_chunk<T>(pr[f], at + u * 64, kb);
+    }
+  };
+  auto load_q = [&](int buf, int ch) {
+    const int64_t at = (int64_t)ch * 256 + c * 16;
+    if constexpr (QUANT) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        qv[buf][u] = *reinterpret_cast<const u32x4*>(s_x + min(r, a.nq - 1) * xs + at + u * 64);
+    } else if ((int64_t)(ch + 1) * 256 <= kb) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) __builtin_memcpy(&qv[buf][u], qr + at + u * 64, 16);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) qv[buf][u] = load_chunk<T>(qr, at + u * 64, kb);
+    }
+  };
+  if (w < chunks) load_p(0, w);
+  if constexpr (QUANT) {
+    // threads [t per, (t + 1) per) of the workgroup take row t, per a multiple
+    // of 64; each thread 8 elements at a time, held between maximum and codes
+    const int per = a.nq == 1 ? 1024 : a.nq == 2 ? 512 : a.nq <= 4 ? 256 : a.nq <= 8 ? 128 : 64;
+    const int row = threadIdx.x / per, i0 = threadIdx.x % per;
+    const uint16_t* xr = reinterpret_cast<const uint16_t*>(a.q0 + (int64_t)min(row, a.nq - 1) * a.ldq);
+    float f[DEC_QUANT / 8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < DEC_QUANT / 8; ++h) {
+      const int at = (h * per + i0) * 8;
+      u32x4 v = {0, 0, 0, 0};
+      if (at < da.k) v = load_chunk<XT == DT_I8 ? DT_BF16 : XT>(reinterpret_cast<const uint8_t*>(xr), at * 2, da.k * 2);
+      unpack16<XT>(v, f[h]);
+      m = top_bits<XT, 8>(f[h], m);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    if (lane == 0) s_top[w] = m;
+    __syncthreads();
+    for (int i = 0; i < per / 64; ++i) m = max(m, s_top[row * (per / 64) + i]);
+    const RowScale rs(m);
+    if (row < a.nq) {
+      if (i0 == 0) s_sq[row] = rs.s;
+#pragma unroll
+      for (int h = 0; h < DEC_QUANT / 8; ++h) {
+        const int at = (h * per + i0) * 8;
+        if (at < chunks * 256)
+          *reinterpret_cast<uint2*>(s_x + row * xs + at) = make_uint2(codes4(rs, f[h]), codes4(rs, f[h] + 4));
+      }
+    }
+    __syncthreads();
+  }
+  acc4 acc[NF] = {};
+  if (w < chunks) load_q(0, w);
+  for (int ch = w, i = 0; ch < chunks; ch += 32) {
+    // two chunks a round, so that the buffers' indices are constants
+#pragma unroll
+    for (i = 0; i < 2; ++i) {
+      const int cur = ch + 16 * i;
+      if (cur >= chunks) break;
+      if (cur + 16 < chunks) {
+        load_p(i ^ 1, cur + 16);
+        load_q(i ^ 1, cur + 16);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[f] = Elem<T>::mma16(pv[i][f][u], qv[i][u], acc[f]);
+    }
+  }
+  // lane: q = lane % 16, p = 4 (lane / 16) + e; red[f][w][q][p]
+  acc4* rd = reinterpret_cast<acc4*>(red);
+#pragma unroll
+  for (int f = 0; f < NF; ++f) rd[f * 1024 + w * 64 + r * 4 + c] = acc[f];
+  __syncthreads();
+  typedef decltype(acc[0][0] + 0) V;
+  constexpr int PG = OP / 4, TF = 16 * PG;         // threads of a fragment
+  if (threadIdx.x < NF * TF) {
+    const int f = threadIdx.x / TF, q = threadIdx.x % TF / PG, g = threadIdx.x % PG;
+    acc4 v0 = {}, v1 = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v0 += rd[f * 1024 + i * 64 + q * 4 + g];
+      if constexpr (EPI == EPI_GLU) v1 += rd[f * 1024 + i * 64 + q * 4 + 2 + g];
+    }
+    V s0[4], s1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s0[e] = v0[e];
+      s1[e] = v1[e];
+    }
+    float sq = 1.f;
+    if constexpr (T == DT_I8) sq = QUANT ? s_sq[min(q, a.nq - 1)] : a.sq[min(q, a.nq - 1)];
+    finish4<T, EPI>(a, q, p0 + f * OP + g * 4, s0, s1, sq);
+  }
+}
+
+// ----------------------------------------------------------- small kernels
+template <typename E>
+__global__ __launch_bounds__(256) void k_dense_pad(const E* src, int64_t ld, int cols, E* dst, int64_t ldd) {
+  const int64_t r = blockIdx.x;
+  for (int64_t i = threadIdx.x; i < ldd; i += 256) dst[r * ldd + i] = i < cols ? src[r * ld + i] : (E)0;
+}
+
 // One workgroup a row. Whole 16-byte chunks (VEC: rows at 16 bytes, cols and
 // ldq whole chunks) are read once, the first QUANT_HOLD a thread held in
 // registers between the maximum and the codes; longer rows are read twice
@@ -767,8 +895,7 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   auto top = [&](u32x4 v) {
     float f[N];
     unpack16<T>(v, f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    m = top_bits<T, N>(f, m);
   };
   if constexpr (VEC) {
 #pragma unroll
@@ -787,16 +914,8 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
   m = max(max(red[0], red[1]), max(red[2], red[3]));
-  const bool fin = m < 0x7F800000u;
-  const float s = fin ? __uint_as_float(m) / 127.f : __builtin_nanf("");
-  if (threadIdx.x == 0) scale[r] = s;
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  const bool some = s > 0.f, wide = inv < 3e38f;    // a subnormal scale: its reciprocal may overflow
-  auto code = [&](float xv) {
-    if (!some) return 0;
-    return wide ? quant1(xv, s, inv)
-                : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)xv / (double)s), -127.0), 127.0);
-  };
+  const RowScale rs(m);
+  if (threadIdx.x == 0) scale[r] = rs.s;
   int8_t* qr = q + r * ldq;
   if constexpr (VEC) {
     auto put = [&](int c, u32x4 v) {
@@ -804,11 +923,7 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
       unpack16<T>(v, f);
       uint32_t o[N / 4];
 #pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        o[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i] |= (uint32_t)(code(f[4 * i + e]) & 255) << (8 * e);
-      }
+      for (int i = 0; i < N / 4; ++i) o[i] = codes4(rs, f + 4 * i);
       if constexpr (N == 8) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(o[0], o[1]);
       else *reinterpret_cast<uint32_t*>(qr + c * 4) = o[0];
     };
@@ -820,7 +935,7 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
     for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) put(c, reinterpret_cast<const u32x4*>(xr)[c]);
     for (int64_t i = cols + threadIdx.x; i < ldq; i += 256) qr[i] = 0;
   } else {
-    for (int64_t i = threadIdx.x; i < ldq; i += 256) qr[i] = i < cols ? (int8_t)code(Row<T>::f(xr[i])) : (int8_t)0;
+    for (int64_t i = threadIdx.x; i < ldq; i += 256) qr[i] = i < cols ? (int8_t)rs.code(Row<T>::f(xr[i])) : (int8_t)0;
   }
 }
 
@@ -884,12 +999,12 @@ __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, i
 }
 
 // --------------------------------------------------------------- launchers
-template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB>
+template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB, int KU>
 static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
-  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB> K;
+  typedef Dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB, KU> K;
   constexpr int lds = R * K::UNIT;
   constexpr int OP = EPI == EPI_GLU ? BP / 2 : BP;
-  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB>;
+  auto kern = k_dense<T, EPI, FORM, BP, BQ, WP, WQ, R, KB, KU>;
   const int64_t tiles = (int64_t)((a.np + OP - 1) / OP) * ((a.nq + BQ - 1) / BQ);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lds > 65536) {
@@ -900,7 +1015,7 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3((uint32_t)tiles, a.splits), dim3(WP * WQ * 64), lds, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((k_dense_join<T, EPI>), dim3((a.np + 1023) / 1024, a.nq), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_dense_join<T, EPI>), dim3(a.nq, (a.np + 1023) / 1024), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -908,11 +1023,11 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
 template <int T, int EPI, int FORM>
 static hipError_t launch_form(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 5, 128>(a, s);
-    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 2, 5, 128>(a, s);
+    case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 5, 128, 1>(a, s);
+    case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 4, 5, 128, 1>(a, s);
     case 2:
-      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 2, 9, 128>(a, s);
-      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 9, 128>(a, s);
+      if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 4, 5, 256, 2>(a, s);
+      else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 5, 256, 2>(a, s);
   }
   return hipErrorInvalidValue;
 }
@@ -933,16 +1048,36 @@ hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a,
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_dense_decode(int dt, int epi, const DenseDecodeArgs& a, hipStream_t s) {
-  const int op = epi == EPI_GLU ? 8 : 16;
-  const dim3 grid((a.d.np + op - 1) / op), block(1024);
-  if (epi == EPI_GLU && dt == DT_BF16) hipLaunchKernelGGL((k_dense_decode<DT_BF16, EPI_GLU>), grid, block, 0, s, a);
-  else if (epi == EPI_GLU && dt == DT_F16) hipLaunchKernelGGL((k_dense_decode<DT_F16, EPI_GLU>), grid, block, 0, s, a);
-  else if (epi == EPI_GLU && dt == DT_I8) hipLaunchKernelGGL((k_dense_decode<DT_I8, EPI_GLU>), grid, block, 0, s, a);
-  else if (epi == EPI_SCALE && dt == DT_I8)
-    hipLaunchKernelGGL((k_dense_decode<DT_I8, EPI_SCALE>), grid, block, 0, s, a);
-  else return hipErrorInvalidValue;
+bool dense_decode_quantises(int epi, int rows, int k, int np) {
+  return (int64_t)rows * k <= 1024 * DEC_QUANT / 2 && np <= 512 * (epi == EPI_GLU ? 8 : 16);
+}
+
+template <int T, int EPI, int XT, int NF>
+static hipError_t decode_launch_nf(const DenseDecodeArgs& a, hipStream_t s) {
+  constexpr int OP = (EPI == EPI_GLU ? 8 : 16) * NF;
+  const size_t lds = NF * 16384 + 128 + (XT != DT_I8 && T == DT_I8 ? (size_t)a.d.nq * ((a.k + 255) / 256 * 256 + 16) : 0);
+  hipLaunchKernelGGL((k_dense_decode<T, EPI, XT, NF>), dim3((a.d.np + OP - 1) / OP), dim3(1024), lds, s, a);
   return hipGetLastError();
+}
+template <int T, int EPI, int XT>
+static hipError_t decode_launch(const DenseDecodeArgs& a, hipStream_t s) {
+  constexpr int OP = EPI == EPI_GLU ? 8 : 16;
+  if (XT == DT_I8 && a.d.nq > 4 && a.d.np >= 512 * OP) return decode_launch_nf<T, EPI, XT, XT == DT_I8 ? 2 : 1>(a, s);
+  return decode_launch_nf<T, EPI, XT, 1>(a, s);
+}
+
+hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a, hipStream_t s) {
+  if (dt == DT_BF16 && epi == EPI_GLU) return decode_launch<DT_BF16, EPI_GLU, DT_I8>(a, s);
+  if (dt == DT_F16 && epi == EPI_GLU) return decode_launch<DT_F16, EPI_GLU, DT_I8>(a, s);
+  if (dt != DT_I8) return hipErrorInvalidValue;
+  if (epi == EPI_GLU) {
+    if (xt == DT_BF16) return decode_launch<DT_I8, EPI_GLU, DT_BF16>(a, s);
+    if (xt == DT_F16) return decode_launch<DT_I8, EPI_GLU, DT_F16>(a, s);
+    return decode_launch<DT_I8, EPI_GLU, DT_I8>(a, s);
+  }
+  if (xt == DT_BF16) return decode_launch<DT_I8, EPI_SCALE, DT_BF16>(a, s);
+  if (xt == DT_F16) return decode_launch<DT_I8, EPI_SCALE, DT_F16>(a, s);
+  return decode_launch<DT_I8, EPI_SCALE, DT_I8>(a, s);
 }
 
 hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,

@@ -64,7 +64,8 @@ uint64_t part_bytes(int splits, int64_t nq, int64_t pcols) {
 }
 
 struct GluPlan {
-  bool decode, pad_x, pad_g, pad_u, quant;
+  bool decode, pad_x, pad_g, pad_u;
+  bool quant, inner;      // x quantised into the workspace, or by the decode kernel itself
   int64_t kp;             // padded row length (elements)
   int tile, splits;
   uint64_t x_off, g_off, u_off, sx_off, part_off, total;
@@ -73,8 +74,9 @@ struct GluPlan {
 GluPlan plan_forward(const moe_glu* a, int dt) {
   GluPlan p{};
   const int es = dt == DT_I8 ? 1 : 2;
-  p.quant = dt == DT_I8 && !a->s_x;
   p.decode = a->rows <= kDecodeRows;
+  p.inner = dt == DT_I8 && !a->s_x && p.decode && dense_decode_quantises(EPI_GLU, a->rows, a->hidden, a->inter);
+  p.quant = dt == DT_I8 && !a->s_x && !p.inner;
   p.kp = up(a->hidden, 16 / es);
   Bump b;
   p.pad_x = !p.quant && !p.decode && !plain_rows(a->x, a->ldx, a->hidden, es);
@@ -86,7 +88,7 @@ GluPlan plan_forward(const moe_glu* a, int dt) {
   if (p.pad_u) p.u_off = b.take((uint64_t)a->inter * p.kp * es);
   p.splits = 1;
   if (!p.decode) {
-    p.tile = dense_tile(dt, EPI_GLU, FORM_NT, a->inter, a->rows, steps_of(p.kp * es), &p.splits);
+    p.tile = dense_tile(EPI_GLU, a->inter, a->rows, steps_of(p.kp * es), &p.splits);
     p.part_off = b.take(part_bytes(p.splits, a->rows, 2 * up(a->inter, 4)));
   }
   p.total = b.at;
@@ -115,11 +117,11 @@ GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
   p.splits_x = p.splits_w = 1;
   uint64_t part = 0;
   if (dx) {
-    p.tile_x = dense_tile(a->dtype, EPI_OUT, FORM_NN, a->hidden, a->rows, (int)(2 * p.ip / 64), &p.splits_x);
+    p.tile_x = dense_tile(EPI_OUT, a->hidden, a->rows, (int)(2 * p.ip / 64), &p.splits_x);
     part = std::max(part, part_bytes(p.splits_x, a->rows, up(a->hidden, 4)));
   }
   if (dw) {
-    p.tile_w = dense_tile(a->dtype, EPI_OUT, FORM_TN, a->hidden, (int)(2 * p.ip), (a->rows + 63) / 64, &p.splits_w);
+    p.tile_w = dense_tile(EPI_OUT, a->hidden, (int)(2 * p.ip), (a->rows + 63) / 64, &p.splits_w);
     part = std::max(part, part_bytes(p.splits_w, 2 * p.ip, up(a->hidden, 4)));
   }
   p.part_off = b.take(part);
@@ -189,7 +191,7 @@ int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, floa
                           reinterpret_cast<float*>(w + p.sx_off), s);
     x = {w + p.x_off, p.kp};
   } else {
-    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, es, w + p.x_off, p.kp, s, &x);
+    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, p.inner ? 2 : es, w + p.x_off, p.kp, s, &x);
   }
   if (e == hipSuccess) e = padded(p.pad_g, a->w_gate, a->ldw_gate, a->inter, a->hidden, es, w + p.g_off, p.kp, s, &g);
   if (e == hipSuccess) e = padded(p.pad_u, a->w_up, a->ldw_up, a->inter, a->hidden, es, w + p.u_off, p.kp, s, &u);
@@ -217,13 +219,13 @@ int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, floa
   }
   d.part = reinterpret_cast<float*>(w + p.part_off);
   d.pcols = 2 * up(a->inter, 4);
-  if (p.decode) e = launch_dense_decode(dt, EPI_GLU, DenseDecodeArgs{d, a->hidden}, s);
+  if (p.decode) e = launch_dense_decode(dt, EPI_GLU, p.inner ? a->dtype : DT_I8, DenseDecodeArgs{d, a->hidden}, s);
   else e = launch_dense(dt, EPI_GLU, FORM_NT, p.tile, d, s);
   return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
 }
 
 struct LinPlan {
-  bool decode, pad_x, pad_w, quant;
+  bool decode, pad_x, pad_w, quant, inner;
   int64_t kp;
   int tile, splits;
   uint64_t x_off, sx_off, w_off, part_off, total;
@@ -231,8 +233,9 @@ struct LinPlan {
 
 LinPlan plan_linear(const moe_linear* a) {
   LinPlan p{};
-  p.quant = !a->s_x;
   p.decode = a->rows <= kDecodeRows;
+  p.inner = !a->s_x && p.decode && dense_decode_quantises(EPI_SCALE, a->rows, a->in, a->out);
+  p.quant = !a->s_x && !p.inner;
   p.kp = up(a->in, 16);
   Bump b;
   p.pad_x = !p.quant && !p.decode && !plain_rows(a->x, a->ldx, a->in, 1);
@@ -242,7 +245,7 @@ LinPlan plan_linear(const moe_linear* a) {
   if (p.pad_w) p.w_off = b.take((uint64_t)a->out * p.kp);
   p.splits = 1;
   if (!p.decode) {
-    p.tile = dense_tile(DT_I8, EPI_SCALE, FORM_NT, a->out, a->rows, steps_of(p.kp), &p.splits);
+    p.tile = dense_tile(EPI_SCALE, a->out, a->rows, steps_of(p.kp), &p.splits);
     p.part_off = b.take(part_bytes(p.splits, a->rows, up(a->out, 4)));
   }
   p.total = b.at;
@@ -262,22 +265,38 @@ int check_linear(const char* fn, const moe_linear* a) {
 
 }  // namespace
 
-// Tile (0: 256 x 256, 1: 128 x 128, 2: 64 x 64) and K ranges of a product:
-// the largest tile whose workgroups fill the 256 CUs, else the small one
-// with the contraction cut until they do (at least 8 steps a range).
-int moe::dense_tile(int dt, int epi, int form, int np, int nq, int steps, int* splits) {
-  (void)dt;
-  (void)form;
-  auto count = [&](int bp, int bq) {
-    const int op = epi == EPI_GLU ? bp / 2 : bp;
-    return (int64_t)((np + op - 1) / op) * ((nq + bq - 1) / bq);
-  };
-  *splits = 1;
-  if (count(256, 256) >= 200) return 0;
-  if (count(128, 128) >= 200) return 1;
-  const int64_t n = count(64, 64);
-  if (nq <= 32768) *splits = (int)std::max<int64_t>(1, std::min<int64_t>(512 / n, steps / 8));
-  return 2;
+// Tile (0: 256 x 256, 1: 128 x 128, 2: 64 x 64) and K ranges of a product: the
+// choice of least time under a model fitted to graph replays of 75 products
+// (rows 32..4096, hidden 1000..8192, inter 512..8192; every tile with 1 to 4
+// ranges timed for each): us a 128-byte K step with one workgroup on a CU and
+// with as many as fit (1, 2, 2), us for a tile's start and end; for more than
+// one range the join's launch and its partial sums at 4.3 TB/s. The choice it
+// makes is within 2% of the best timed one on each of them.
+int moe::dense_tile(int epi, int np, int nq, int steps, int* splits) {
+  static const struct {
+    int edge, per_cu;
+    double step1, step2, fixed;
+  } kTile[3] = {{256, 1, 1.08, 1.08, 7.7}, {128, 2, 0.72, 0.90, 5.5}, {64, 2, 0.32, 0.35, 3.4}};
+  const int cus = 256, glu = epi == EPI_GLU ? 2 : 1;
+  double best = 0;
+  int tile = -1;
+  for (int t = 0; t < 3; ++t) {
+    const int op = kTile[t].edge / glu;
+    const int64_t n = (int64_t)((np + op - 1) / op) * ((nq + kTile[t].edge - 1) / kTile[t].edge);
+    for (int s = 1; s <= 8 && (s == 1 || steps >= 4 * s); ++s) {
+      const int64_t wgs = n * s, full = wgs / (cus * kTile[t].per_cu), rest = wgs % (cus * kTile[t].per_cu);
+      const int st = (steps + s - 1) / s;
+      double us = full * (kTile[t].fixed + st * kTile[t].step2);
+      if (rest) us += kTile[t].fixed + st * (rest <= cus ? kTile[t].step1 : kTile[t].step2);
+      if (s > 1) us += 3.8 + 8e-6 / 4.3 * s * nq * np * glu;
+      if (tile < 0 || us < best) {
+        best = us;
+        tile = t;
+        *splits = s;
+      }
+    }
+  }
+  return tile;
 }
 
 extern "C" {
@@ -412,7 +431,7 @@ int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t 
                           reinterpret_cast<float*>(w + p.sx_off), s);
     x = {w + p.x_off, p.kp};
   } else {
-    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->in, 1, w + p.x_off, p.kp, s, &x);
+    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->in, p.inner ? 2 : 1, w + p.x_off, p.kp, s, &x);
   }
   if (e == hipSuccess) e = padded(p.pad_w, a->w, a->ldw, a->out, a->in, 1, w + p.w_off, p.kp, s, &m);
   if (e != hipSuccess) return hip_bad(fn, e);
@@ -433,7 +452,7 @@ int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t 
   d.bias = a->bias;
   d.part = reinterpret_cast<float*>(w + p.part_off);
   d.pcols = up(a->out, 4);
-  if (p.decode) e = launch_dense_decode(DT_I8, EPI_SCALE, DenseDecodeArgs{d, a->in}, s);
+  if (p.decode) e = launch_dense_decode(DT_I8, EPI_SCALE, p.inner ? a->dtype : DT_I8, DenseDecodeArgs{d, a->in}, s);
   else e = launch_dense(DT_I8, EPI_SCALE, FORM_NT, p.tile, d, s);
   return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
 }

@@ -45,15 +45,18 @@ struct DenseArgs {
   int64_t pcols;
 };
 
-// Decode rows (nq <= 16), any alignment: K elements per row.
+// Decode rows (nq <= 16), any alignment: k elements per row. launch_dense_decode's
+// xt: DT_I8 (x has the weights' type), or the 16-bit type of an x that the kernel
+// quantises itself (8-bit weights, where dense_decode_quantises says so).
 struct DenseDecodeArgs {
   DenseArgs d;
   int k;
 };
 
-int dense_tile(int dt, int epi, int form, int np, int nq, int steps, int* splits);
+int dense_tile(int epi, int np, int nq, int steps, int* splits);
 hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a, hipStream_t s);
-hipError_t launch_dense_decode(int dt, int epi, const DenseDecodeArgs& a, hipStream_t s);
+bool dense_decode_quantises(int epi, int rows, int k, int np);
+hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a, hipStream_t s);
 // rows of `cols` elements (esize bytes, row stride ld elements) copied to
 // rows of ldd elements, zero behind cols
 hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,

@@ -19,7 +19,8 @@ hipError_t launch_route_exact(int, int, const RouteArgs&, hipStream_t, hipEvent_
 hipError_t launch_exact_experts(int, int, const DecodeArgs&, hipStream_t, hipEvent_t*) { return hipErrorNoDevice; }
 
 hipError_t launch_dense(int, int, int, int, const DenseArgs&, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_dense_decode(int, int, const DenseDecodeArgs&, hipStream_t) { return hipErrorNoDevice; }
+bool dense_decode_quantises(int, int, int, int) { return true; }
+hipError_t launch_dense_decode(int, int, int, const DenseDecodeArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_dense_pad(const void*, int64_t, int, int, int, void*, int64_t, hipStream_t) {
   return hipErrorNoDevice;
 }
