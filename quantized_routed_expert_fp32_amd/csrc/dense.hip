@@ -638,6 +638,24 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
   finish4<T, EPI>(a, q, p, s0, s1, T == DT_I8 ? a.sq[q] : 1.f);
 }
 
+// -------------------------------------------------- rows at any alignment
+// 16 bytes of a row from byte `byte` on, of elements of ES bytes, zero from
+// byte `end` on. Global loads take any alignment.
+template <int ES>
+__device__ __forceinline__ u32x4 load_chunk(const void* row, int64_t byte, int64_t end) {
+  const uint8_t* at = static_cast<const uint8_t*>(row) + byte;
+  u32x4 v = {0, 0, 0, 0};
+  if (byte + 16 <= end) {
+    __builtin_memcpy(&v, at, 16);
+  } else {
+    uint8_t* b = reinterpret_cast<uint8_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 16; i += ES)
+      if (byte + i < end) __builtin_memcpy(b + i, at + i, ES);
+  }
+  return v;
+}
+
 // ---------------------------------------------------------------- quantising
 template <int T> struct Row;
 template <> struct Row<DT_BF16> {
@@ -713,21 +731,6 @@ __device__ __forceinline__ uint32_t codes4(const RowScale& rs, const float* f) {
 // straight from memory at any alignment: bound by the weights' bytes, or by
 // latency when there are few. XT = DT_BF16 / DT_F16 (8-bit weights only): x is
 // quantised by every workgroup into LDS, while its first weights arrive.
-template <int T>
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int64_t byte, int64_t end) {
-  u32x4 v = {0, 0, 0, 0};
-  if (byte + 16 <= end) {
-    __builtin_memcpy(&v, row + byte, 16);
-  } else {
-    uint8_t* b = reinterpret_cast<uint8_t*>(&v);
-    constexpr int ES = Elem<T>::SIZE;
-#pragma unroll
-    for (int i = 0; i < 16; i += ES)
-      if (byte + i < end) __builtin_memcpy(b + i, row + byte + i, ES);
-  }
-  return v;
-}
-
 constexpr int DEC_QUANT = 32;     // elements a thread quantises at most: nq k <= 1024 * 32
 
 template <int T, int EPI, int XT, int NF>
@@ -773,7 +776,7 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
 #pragma unroll
       for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int u = 0; u < U; ++u) pv[buf][f][u] = load_chunk<T>(pr[f], at + u * 64, kb);
+        for (int u = 0; u < U; ++u) pv[buf][f][u] = load_chunk<Elem<T>::SIZE>(pr[f], at + u * 64, kb);
     }
   };
   auto load_q = [&](int buf, int ch) {
@@ -787,7 +790,7 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
       for (int u = 0; u < U; ++u) __builtin_memcpy(&qv[buf][u], qr + at + u * 64, 16);
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) qv[buf][u] = load_chunk<T>(qr, at + u * 64, kb);
+      for (int u = 0; u < U; ++u) qv[buf][u] = load_chunk<Elem<T>::SIZE>(qr, at + u * 64, kb);
     }
   };
   if (w < chunks) load_p(0, w);
@@ -803,7 +806,7 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
     for (int h = 0; h < DEC_QUANT / 8; ++h) {
       const int at = (h * per + i0) * 8;
       u32x4 v = {0, 0, 0, 0};
-      if (at < da.k) v = load_chunk<XT == DT_I8 ? DT_BF16 : XT>(reinterpret_cast<const uint8_t*>(xr), at * 2, da.k * 2);
+      if (at < da.k) v = load_chunk<2>(xr, at * 2, da.k * 2);
       unpack16<XT>(v, f[h]);
       m = top_bits<XT, 8>(f[h], m);
     }
@@ -870,26 +873,34 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
 }
 
 // ----------------------------------------------------------- small kernels
-template <typename E>
-__global__ __launch_bounds__(256) void k_dense_pad(const E* src, int64_t ld, int cols, E* dst, int64_t ldd) {
-  const int64_t r = blockIdx.x;
-  for (int64_t i = threadIdx.x; i < ldd; i += 256) dst[r * ldd + i] = i < cols ? src[r * ld + i] : (E)0;
+// Up to three operands copied to zero-padded rows of 16-byte chunks in one
+// launch: a wave a row.
+template <int ES>
+__global__ __launch_bounds__(256) void k_dense_pad(DensePad j) {
+  int r = blockIdx.x * 4 + threadIdx.x / 64, o = 0;
+  while (o < 2 && r >= j.rows[o]) r -= j.rows[o++];
+  if (r >= j.rows[o]) return;
+  const uint8_t* src = static_cast<const uint8_t*>(j.src[o]) + (int64_t)r * j.ld[o] * ES;
+  u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(j.dst[o]) + (int64_t)r * j.ldd * ES);
+  const int chunks = (int)(j.ldd * ES / 16);
+  for (int c = threadIdx.x & 63; c < chunks; c += 64) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
 }
 
-// One workgroup a row. Whole 16-byte chunks (VEC: rows at 16 bytes, cols and
-// ldq whole chunks) are read once, the first QUANT_HOLD a thread held in
-// registers between the maximum and the codes; longer rows are read twice
-// (from the L2). Bound by memory: 3 bytes an element for 16-bit rows.
+// One workgroup a row, 16 bytes of x a thread at a time; the first QUANT_HOLD
+// of a thread stay in registers between the maximum and the codes, longer rows
+// are read twice (from the L2). VEC: q's rows are whole 8-byte (fp32: 4-byte)
+// groups at such an address. Bound by memory: 3 bytes an element for 16-bit rows.
 constexpr int QUANT_HOLD = 4;
 template <int T, bool VEC>
 __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type* x, int64_t ldx, int cols, int8_t* q,
                                                     int64_t ldq, float* scale) {
-  constexpr int N = T == DT_F32 ? 4 : 8;
+  constexpr int ES = sizeof(typename Row<T>::type), N = 16 / ES;
   __shared__ uint32_t red[4];
   const int64_t r = blockIdx.x;
   const typename Row<T>::type* xr = x + r * ldx;
-  const int chunks = VEC ? cols / N : 0;
-  u32x4 hold[VEC ? QUANT_HOLD : 1];
+  const int chunks = (int)((ldq + N - 1) / N);     // past cols they are zero
+  auto chunk = [&](int c) { return c * N < cols ? load_chunk<ES>(xr, (int64_t)c * 16, (int64_t)cols * ES) : u32x4{0, 0, 0, 0}; };
+  u32x4 hold[QUANT_HOLD];
   // |x| as bits: ordered as the values, infinity and NaN above them all
   uint32_t m = 0;
   auto top = [&](u32x4 v) {
@@ -897,18 +908,11 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
     unpack16<T>(v, f);
     m = top_bits<T, N>(f, m);
   };
-  if constexpr (VEC) {
 #pragma unroll
-    for (int h = 0; h < QUANT_HOLD; ++h) {
-      const int c = h * 256 + threadIdx.x;
-      hold[h] = c < chunks ? reinterpret_cast<const u32x4*>(xr)[c] : u32x4{0, 0, 0, 0};
-    }
+  for (int h = 0; h < QUANT_HOLD; ++h) hold[h] = chunk(h * 256 + threadIdx.x);
 #pragma unroll
-    for (int h = 0; h < QUANT_HOLD; ++h) top(hold[h]);
-    for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) top(reinterpret_cast<const u32x4*>(xr)[c]);
-  } else {
-    for (int i = threadIdx.x; i < cols; i += 256) m = max(m, __float_as_uint(Row<T>::f(xr[i])) & 0x7FFFFFFFu);
-  }
+  for (int h = 0; h < QUANT_HOLD; ++h) top(hold[h]);
+  for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) top(chunk(c));
 #pragma unroll
   for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -917,85 +921,61 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   const RowScale rs(m);
   if (threadIdx.x == 0) scale[r] = rs.s;
   int8_t* qr = q + r * ldq;
-  if constexpr (VEC) {
-    auto put = [&](int c, u32x4 v) {
-      float f[N];
-      unpack16<T>(v, f);
-      uint32_t o[N / 4];
+  auto put = [&](int c, u32x4 v) {
+    float f[N];
+    unpack16<T>(v, f);
+    uint32_t o[N / 4];
 #pragma unroll
-      for (int i = 0; i < N / 4; ++i) o[i] = codes4(rs, f + 4 * i);
-      if constexpr (N == 8) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint32_t*>(qr + c * 4) = o[0];
-    };
+    for (int i = 0; i < N / 4; ++i) o[i] = codes4(rs, f + 4 * i);
+    if constexpr (VEC && N == 8) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(o[0], o[1]);
+    else if constexpr (VEC) *reinterpret_cast<uint32_t*>(qr + c * 4) = o[0];
+    else
 #pragma unroll
-    for (int h = 0; h < QUANT_HOLD; ++h) {
-      const int c = h * 256 + threadIdx.x;
-      if (c < chunks) put(c, hold[h]);
-    }
-    for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) put(c, reinterpret_cast<const u32x4*>(xr)[c]);
-    for (int64_t i = cols + threadIdx.x; i < ldq; i += 256) qr[i] = 0;
-  } else {
-    for (int64_t i = threadIdx.x; i < ldq; i += 256) qr[i] = i < cols ? (int8_t)rs.code(Row<T>::f(xr[i])) : (int8_t)0;
+      for (int i = 0; i < N; ++i)
+        if ((int64_t)c * N + i < ldq) qr[(int64_t)c * N + i] = (int8_t)(o[i / 4] >> (8 * (i % 4)));
+  };
+#pragma unroll
+  for (int h = 0; h < QUANT_HOLD; ++h) {
+    const int c = h * 256 + threadIdx.x;
+    if (c < chunks) put(c, hold[h]);
   }
+  for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) put(c, chunk(c));
 }
 
-// [dg | du] from dh and the kept g, u: 14 bytes an element through memory,
-// which bounds it. VEC: 8 elements a thread where every row starts at 16 bytes.
-template <int DT, bool VEC>
+// [dg | du] from dh and the kept g, u, 8 elements a thread: 14 bytes an
+// element through memory, which bounds it.
+template <int DT>
 __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int inter,
                                                   int ip, uint16_t* d) {
-  constexpr int N = VEC ? 8 : 1;
   const int64_t r = blockIdx.x;
   const float* g = gu + r * 2 * inter;
-  for (int i = (blockIdx.y * 256 + threadIdx.x) * N; i < ip; i += gridDim.y * 256 * N) {
-    float e[N], gv[N], uv[N];
-    uint16_t dg[N], du[N];
-    if constexpr (VEC) {
-      u32x4 ev = {0, 0, 0, 0};
-      f32x4 g0 = {}, g1 = {}, u0 = {}, u1 = {};
-      if (i < inter) {
-        ev = *reinterpret_cast<const u32x4*>(dh + r * lddh + i);
-        g0 = *reinterpret_cast<const f32x4*>(g + i);
-        g1 = *reinterpret_cast<const f32x4*>(g + i + 4);
-        u0 = *reinterpret_cast<const f32x4*>(g + inter + i);
-        u1 = *reinterpret_cast<const f32x4*>(g + inter + i + 4);
-      }
-      unpack16<DT>(ev, e);
+  const int i = (blockIdx.y * 256 + threadIdx.x) * 8;
+  if (i >= ip) return;
+  float e[8], gv[8], uv[8];
+  unpack16<DT>(i < inter ? load_chunk<2>(dh + r * lddh, i * 2, inter * 2) : u32x4{0, 0, 0, 0}, e);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        gv[k] = g0[k];
-        gv[4 + k] = g1[k];
-        uv[k] = u0[k];
-        uv[4 + k] = u1[k];
-      }
-    } else {
-      const bool in = i < inter;
-      e[0] = in ? Row<DT>::f(dh[r * lddh + i]) : 0.f;
-      gv[0] = in ? g[i] : 0.f;
-      uv[0] = in ? g[inter + i] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      float v, dv;
-      act_grad_f(gv[k], act, &v, &dv);
-      dg[k] = to16<DT>(e[k] * uv[k] * dv);
-      du[k] = to16<DT>(e[k] * v);
-    }
-    uint16_t* o = d + r * 2 * ip + i;
-    if constexpr (VEC) {
-      u32x4 a, b;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a[k] = dg[2 * k] | (uint32_t)dg[2 * k + 1] << 16;
-        b[k] = du[2 * k] | (uint32_t)du[2 * k + 1] << 16;
-      }
-      *reinterpret_cast<u32x4*>(o) = a;
-      *reinterpret_cast<u32x4*>(o + ip) = b;
-    } else {
-      o[0] = dg[0];
-      o[ip] = du[0];
-    }
+  for (int k = 0; k < 2; ++k) {
+    const bool in = i + 4 * k < inter;
+    unpack16<DT_F32>(in ? load_chunk<4>(g, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, gv + 4 * k);
+    unpack16<DT_F32>(in ? load_chunk<4>(g + inter, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, uv + 4 * k);
   }
+  u32x4 a, b;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float v, dv;
+      act_grad_f(gv[2 * k + n], act, &v, &dv);
+      lo[n] = to16<DT>(e[2 * k + n] * uv[2 * k + n] * dv);
+      hi[n] = to16<DT>(e[2 * k + n] * v);
+    }
+    a[k] = lo[0] | lo[1] << 16;
+    b[k] = hi[0] | hi[1] << 16;
+  }
+  u32x4* o = reinterpret_cast<u32x4*>(d + r * 2 * ip + i);
+  o[0] = a;
+  o[ip / 8] = b;
 }
 
 // --------------------------------------------------------------- launchers
@@ -1019,12 +999,14 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// tiles: 0 large (256 x 256), 1 medium (128 x 128), 2 small (64 x 64)
+// tiles: 0 256 x 256; 1 128 x 128, two workgroups a CU; 2 64 x 64, two a CU;
+// 3 128 x 128 in steps of 256 bytes (half the barriers), one a CU
 template <int T, int EPI, int FORM>
 static hipError_t launch_form(int tile, const DenseArgs& a, hipStream_t s) {
   switch (tile) {
     case 0: return launch_tile<T, EPI, FORM, 256, 256, 4, 2, 5, 128, 1>(a, s);
     case 1: return launch_tile<T, EPI, FORM, 128, 128, 2, 4, 5, 128, 1>(a, s);
+    case 3: return launch_tile<T, EPI, FORM, 128, 128, 2, 4, 5, 256, 2>(a, s);
     case 2:
       if constexpr (EPI == EPI_GLU) return launch_tile<T, EPI, FORM, 64, 64, 1, 4, 5, 256, 2>(a, s);
       else return launch_tile<T, EPI, FORM, 64, 64, 2, 2, 5, 256, 2>(a, s);
@@ -1080,14 +1062,12 @@ hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a
   return decode_launch<DT_I8, EPI_SCALE, DT_I8>(a, s);
 }
 
-hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,
-                            hipStream_t s) {
-  if (esize == 1)
-    hipLaunchKernelGGL((k_dense_pad<uint8_t>), dim3(rows), dim3(256), 0, s, static_cast<const uint8_t*>(src), ld, cols,
-                       static_cast<uint8_t*>(dst), ldd);
-  else
-    hipLaunchKernelGGL((k_dense_pad<uint16_t>), dim3(rows), dim3(256), 0, s, static_cast<const uint16_t*>(src), ld,
-                       cols, static_cast<uint16_t*>(dst), ldd);
+hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s) {
+  const int64_t rows = (int64_t)j.rows[0] + j.rows[1] + j.rows[2];
+  if (!rows) return hipSuccess;
+  const dim3 grid((uint32_t)((rows + 3) / 4));
+  if (esize == 1) hipLaunchKernelGGL((k_dense_pad<1>), grid, dim3(256), 0, s, j);
+  else hipLaunchKernelGGL((k_dense_pad<2>), grid, dim3(256), 0, s, j);
   return hipGetLastError();
 }
 
@@ -1096,8 +1076,7 @@ static void quant_launch(const void* x, int64_t ldx, int rows, int cols, int8_t*
                          hipStream_t s) {
   typedef typename Row<T>::type E;
   constexpr int N = T == DT_F32 ? 4 : 8;
-  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % N == 0 && cols % N == 0 &&
-                   reinterpret_cast<uintptr_t>(q) % N == 0 && ldq % N == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(q) % N == 0 && ldq % N == 0;
   if (vec)
     hipLaunchKernelGGL((k_quant_rows<T, true>), dim3(rows), dim3(256), 0, s, static_cast<const E*>(x), ldx, cols, q, ldq,
                        scale);
@@ -1115,24 +1094,13 @@ hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int c
   return hipGetLastError();
 }
 
-template <int DT>
-static void grad_launch(int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip, void* d,
-                        hipStream_t s) {
-  const bool vec = reinterpret_cast<uintptr_t>(dh) % 16 == 0 && lddh % 8 == 0 && inter % 8 == 0 &&
-                   reinterpret_cast<uintptr_t>(gu) % 16 == 0;
-  const int per = vec ? 2048 : 256;
-  const dim3 grid(rows, (ip + per - 1) / per);
-  const uint16_t* e = static_cast<const uint16_t*>(dh);
-  uint16_t* o = static_cast<uint16_t*>(d);
-  if (vec) hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
-  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
-}
-
 hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
                            int ip, void* d, hipStream_t s) {
-  if (dt == DT_BF16) grad_launch<DT_BF16>(act, dh, lddh, gu, rows, inter, ip, d, s);
-  else if (dt == DT_F16) grad_launch<DT_F16>(act, dh, lddh, gu, rows, inter, ip, d, s);
-  else return hipErrorInvalidValue;
+  const dim3 grid(rows, (ip + 2047) / 2048);
+  const uint16_t* e = static_cast<const uint16_t*>(dh);
+  uint16_t* o = static_cast<uint16_t*>(d);
+  if (dt == DT_BF16) hipLaunchKernelGGL((k_glu_grad<DT_BF16>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
+  else hipLaunchKernelGGL((k_glu_grad<DT_F16>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
   return hipGetLastError();
 }
 

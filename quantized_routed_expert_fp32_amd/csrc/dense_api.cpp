@@ -158,21 +158,29 @@ int check_ws(const char* fn, const void* ws, uint64_t have, uint64_t need) {
   return MOE_OK;
 }
 
-// Copies rows to the workspace where the plan says so; the operand as the
-// tile kernels read it.
+// The operands as the tile kernels read them: copied to the workspace where
+// the plan says so, by one launch (run).
 struct Rows {
   const uint8_t* p;
   int64_t ld;   // bytes
 };
-hipError_t padded(bool pad, const void* src, int64_t ld, int rows, int cols, int es, uint8_t* dst, int64_t kp,
-                  hipStream_t s, Rows* out) {
-  if (!pad) {
-    *out = {static_cast<const uint8_t*>(src), ld * es};
-    return hipSuccess;
+struct Padder {
+  DensePad j{};
+  int n = 0, es;
+  Padder(int cols, int64_t kp, int esize) : es(esize) {
+    j.cols = cols;
+    j.ldd = kp;
   }
-  *out = {dst, kp * es};
-  return launch_dense_pad(src, ld, rows, cols, es, dst, kp, s);
-}
+  Rows take(bool pad, const void* src, int64_t ld, int rows, uint8_t* dst) {
+    if (!pad) return {static_cast<const uint8_t*>(src), ld * es};
+    j.src[n] = src;
+    j.dst[n] = dst;
+    j.ld[n] = ld;
+    j.rows[n++] = rows;
+    return {dst, j.ldd * es};
+  }
+  hipError_t run(hipStream_t s) const { return n ? launch_dense_pad(es, j, s) : hipSuccess; }
+};
 
 int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, float* gu, void* ws, uint64_t ws_bytes,
             void* stream) {
@@ -184,17 +192,17 @@ int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, floa
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int es = dt == DT_I8 ? 1 : 2;
-  Rows x, g, u;
-  hipError_t e;
-  if (p.quant) {
+  Padder pad(a->hidden, p.kp, es);
+  Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
+  const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
+  const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
+  hipError_t e = pad.run(s);
+  if (p.inner) x.ld = a->ldx * 2;
+  if (e == hipSuccess && p.quant) {
     e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->hidden, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
                           reinterpret_cast<float*>(w + p.sx_off), s);
     x = {w + p.x_off, p.kp};
-  } else {
-    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, p.inner ? 2 : es, w + p.x_off, p.kp, s, &x);
   }
-  if (e == hipSuccess) e = padded(p.pad_g, a->w_gate, a->ldw_gate, a->inter, a->hidden, es, w + p.g_off, p.kp, s, &g);
-  if (e == hipSuccess) e = padded(p.pad_u, a->w_up, a->ldw_up, a->inter, a->hidden, es, w + p.u_off, p.kp, s, &u);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.p0 = g.p;
@@ -265,22 +273,26 @@ int check_linear(const char* fn, const moe_linear* a) {
 
 }  // namespace
 
-// Tile (0: 256 x 256, 1: 128 x 128, 2: 64 x 64) and K ranges of a product: the
-// choice of least time under a model fitted to graph replays of 75 products
-// (rows 32..4096, hidden 1000..8192, inter 512..8192; every tile with 1 to 4
-// ranges timed for each): us a 128-byte K step with one workgroup on a CU and
-// with as many as fit (1, 2, 2), us for a tile's start and end; for more than
-// one range the join's launch and its partial sums at 4.3 TB/s. The choice it
-// makes is within 2% of the best timed one on each of them.
+// Tile (see launch_dense) and K ranges of a product: the choice of least cost
+// under a model of a tile's start and end, of a 128-byte K step with one
+// workgroup on a CU and with two, of the join of several ranges and of their
+// partial sums (bytes through memory). The weights are fitted so that the
+// choice agrees with graph replays of 95 products (rows 24..4096, hidden
+// 512..8192, inter 512..8192, every tile with 1 to 4 ranges timed for each):
+// its time is 0.3% above the best timed one on average, 8% at most (1024 x
+// 4096 -> 2048 in 38.2 us against 35.3). One tile for all would cost more: 700 x
+// 4096 -> 2 x 2000 takes 79 us on 256 x 256, 40 on 128 x 128, 33 on it in
+// 256-byte steps, 45 on 64 x 64; 512 x 2048 -> 2 x 512 takes 43, 18, 18 and 12.
 int moe::dense_tile(int epi, int np, int nq, int steps, int* splits) {
   static const struct {
     int edge, per_cu;
     double step1, step2, fixed;
-  } kTile[3] = {{256, 1, 1.08, 1.08, 7.7}, {128, 2, 0.72, 0.90, 5.5}, {64, 2, 0.32, 0.35, 3.4}};
+  } kTile[4] = {{256, 1, 1.60, 1.60, 11.4}, {128, 2, 0.73, 1.12, 7.0}, {64, 2, 0.27, 0.48, 5.1}, {128, 1, 0.56, 0.56, 10.2}};
+  constexpr double kJoin = 3.1, kJoinByte = 1e-6 / 6.4;
   const int cus = 256, glu = epi == EPI_GLU ? 2 : 1;
   double best = 0;
   int tile = -1;
-  for (int t = 0; t < 3; ++t) {
+  for (int t = 0; t < 4; ++t) {
     const int op = kTile[t].edge / glu;
     const int64_t n = (int64_t)((np + op - 1) / op) * ((nq + kTile[t].edge - 1) / kTile[t].edge);
     for (int s = 1; s <= 8 && (s == 1 || steps >= 4 * s); ++s) {
@@ -288,7 +300,7 @@ int moe::dense_tile(int epi, int np, int nq, int steps, int* splits) {
       const int st = (steps + s - 1) / s;
       double us = full * (kTile[t].fixed + st * kTile[t].step2);
       if (rest) us += kTile[t].fixed + st * (rest <= cus ? kTile[t].step1 : kTile[t].step2);
-      if (s > 1) us += 3.8 + 8e-6 / 4.3 * s * nq * np * glu;
+      if (s > 1) us += kJoin + kJoinByte * 8 * s * nq * np * glu;
       if (tile < 0 || us < best) {
         best = us;
         tile = t;
@@ -338,6 +350,11 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch_glu_grad(a->dtype, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off, s);
+  Padder pad(a->hidden, p.kp, 2);
+  const Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
+  const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
+  const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
+  if (e == hipSuccess) e = pad.run(s);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.q0 = w + p.d_off;
@@ -348,10 +365,6 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   d.pcols = up(a->hidden, 4);
   if (dx) {
     // dx[r] = sum_i dg[r, i] Wg[i] + du[r, i] Wu[i]: both sums one contraction
-    Rows g, u;
-    e = padded(p.pad_g, a->w_gate, a->ldw_gate, a->inter, a->hidden, 2, w + p.g_off, p.kp, s, &g);
-    if (e == hipSuccess) e = padded(p.pad_u, a->w_up, a->ldw_up, a->inter, a->hidden, 2, w + p.u_off, p.kp, s, &u);
-    if (e != hipSuccess) return hip_bad(fn, e);
     DenseArgs dd = d;
     dd.p0 = g.p;
     dd.p1 = u.p;
@@ -369,9 +382,6 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   }
   if (dw_gate) {
     // [dWg; dWu] = D^T x
-    Rows x;
-    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->hidden, 2, w + p.x_off, p.kp, s, &x);
-    if (e != hipSuccess) return hip_bad(fn, e);
     DenseArgs dd = d;
     dd.p0 = x.p;
     dd.ldp0 = x.ld;
@@ -424,16 +434,16 @@ int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t 
   if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  Rows x, m;
-  hipError_t e;
-  if (p.quant) {
+  Padder pad(a->in, p.kp, 1);
+  Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
+  const Rows m = pad.take(p.pad_w, a->w, a->ldw, a->out, w + p.w_off);
+  hipError_t e = pad.run(s);
+  if (p.inner) x.ld = a->ldx * 2;
+  if (e == hipSuccess && p.quant) {
     e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->in, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
                           reinterpret_cast<float*>(w + p.sx_off), s);
     x = {w + p.x_off, p.kp};
-  } else {
-    e = padded(p.pad_x, a->x, a->ldx, a->rows, a->in, p.inner ? 2 : 1, w + p.x_off, p.kp, s, &x);
   }
-  if (e == hipSuccess) e = padded(p.pad_w, a->w, a->ldw, a->out, a->in, 1, w + p.w_off, p.kp, s, &m);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.p0 = m.p;

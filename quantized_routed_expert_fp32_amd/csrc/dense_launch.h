@@ -55,12 +55,20 @@ struct DenseDecodeArgs {
 
 int dense_tile(int epi, int np, int nq, int steps, int* splits);
 hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a, hipStream_t s);
+// Copies of up to three operands (rows of `cols` elements, any start and row
+// stride ld) to rows of ldd elements, zero behind cols; rows[o] = 0: none.
+struct DensePad {
+  const void* src[3];
+  void* dst[3];
+  int64_t ld[3];
+  int rows[3];
+  int cols;
+  int64_t ldd;   // a multiple of 16 bytes
+};
+
 bool dense_decode_quantises(int epi, int rows, int k, int np);
 hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a, hipStream_t s);
-// rows of `cols` elements (esize bytes, row stride ld elements) copied to
-// rows of ldd elements, zero behind cols
-hipError_t launch_dense_pad(const void* src, int64_t ld, int rows, int cols, int esize, void* dst, int64_t ldd,
-                            hipStream_t s);
+hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
 // q[r, 0..ldq) (zero behind cols), scale[r]
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, hipStream_t s);

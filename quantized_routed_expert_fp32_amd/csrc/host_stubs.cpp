@@ -21,9 +21,7 @@ hipError_t launch_exact_experts(int, int, const DecodeArgs&, hipStream_t, hipEve
 hipError_t launch_dense(int, int, int, int, const DenseArgs&, hipStream_t) { return hipErrorNoDevice; }
 bool dense_decode_quantises(int, int, int, int) { return true; }
 hipError_t launch_dense_decode(int, int, int, const DenseDecodeArgs&, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_dense_pad(const void*, int64_t, int, int, int, void*, int64_t, hipStream_t) {
-  return hipErrorNoDevice;
-}
+hipError_t launch_dense_pad(int, const DensePad&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64_t, float*, hipStream_t) {
   return hipErrorNoDevice;
 }

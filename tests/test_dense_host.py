@@ -108,7 +108,7 @@ def test_linear_refusals(kw, msg, st):
 def test_linear_output_and_quant_refusals():
     L = _lib()
     err = lambda: L.moe_last_error().decode()
-    a, n = linear(), C.c_uint64()
+    a, n = linear(rows=40), C.c_uint64()
     assert L.moe_linear_i8(C.byref(a), None, 32, P, 1 << 30, None) == -1 and "NULL y" in err()
     assert L.moe_linear_i8(C.byref(a), P, 8, P, 1 << 30, None) == -3 and "ldy=8" in err()
     assert L.moe_linear_i8_workspace_size(C.byref(a), C.byref(n)) == 0 and n.value
