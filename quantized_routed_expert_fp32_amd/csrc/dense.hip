@@ -4,7 +4,7 @@
 #include "dense_launch.h"
 
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 namespace moe {
 
@@ -988,9 +988,17 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
   const int64_t tiles = (int64_t)((a.np + OP - 1) / OP) * ((a.nq + BQ - 1) / BQ);
   if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lds > 65536) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                       lds);
+    // once a kernel and device (a runtime call of about a microsecond)
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+      allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   hipLaunchKernelGGL(kern, dim3((uint32_t)tiles, a.splits), dim3(WP * WQ * 64), lds, s, a);
   hipError_t e = hipGetLastError();

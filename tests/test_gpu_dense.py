@@ -91,7 +91,8 @@ def test_linear_i8(M, K, N, dt, bias):
 
 
 def check_linear(y, q, s, w, sw, b, dt):
-    acc = (q.double().cuda() @ w.double().t()).cpu()
+    q, s = q.cuda(), s.cpu()
+    acc = (q.double() @ w.double().t()).cpu()
     v = acc * s.double().unsqueeze(1) * sw.double().cpu()
     bb = b.double().cpu() if b is not None else torch.zeros(1, dtype=torch.float64)
     # the sum to fp32, two products, the bias added: one rounding each
@@ -117,6 +118,53 @@ def test_glu_i8(M, H, I, dt, act):
     D.close(h, want, bound, "h")
     gq, gs = B.quant_rows(x)
     assert torch.equal(B.glu_i8(gq, wg, sg, wu, su, act=act, x_scale=gs, out_dtype=dt), h)
+
+
+# sizes that take each tile of the products with one K range and with several:
+# 256 x 256, 128 x 128 (both step widths) and 64 x 64, in the forward products
+# and in each gradient, ragged in every dimension
+TILES = [(4000, 1300, 2000), (700, 2056, 2000), (2000, 4100, 300), (520, 4104, 2060), (40, 8200, 520), (2048, 512, 4100),
+         (700, 4100, 1000), (100, 200, 9000), (2500, 3000, 40), (9000, 520, 520)]
+
+
+@pytest.mark.parametrize("M,H,I", TILES)
+def test_every_tile(M, H, I):
+    log(f"case tiles {M} {H} {I}")
+    B = binding()
+    dt, act = BF, "silu"
+    x, wg, wu, dh = block(M + H + I, M, H, I, dt)
+    h, gu = B.glu_forward(x, wg, wu, act=act, save=True)
+    check_forward(x, wg, wu, h, act)
+    got = B.glu_backward(dh, x, wg, wu, gu, act=act)
+    for name, t, (want, bound) in zip(("dx", "dw_gate", "dw_up"), got, D.grads(x, wg, wu, gu, dh, act, dt)):
+        D.close(t, want, bound, name)
+    again = B.glu_backward(dh, x, wg, wu, gu, act=act)
+    assert torch.equal(B.glu_forward(x, wg, wu, act=act), h)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+    (q, s), (w, sw), (v, sv) = B.quant_rows(x), B.quant_rows(wg), B.quant_rows(wu)
+    check_linear(B.linear_i8(x, w, sw), q, s, w, sw, None, dt)
+    qc, sc = q.double(), s.double().unsqueeze(1)
+    gg, uu = (qc @ m.double().t() * sc * sm.double() for m, sm in ((w, sw), (v, sv)))
+    want, bound = D.h_bound(gg, uu, 4 * D.U * gg.abs(), 4 * D.U * uu.abs(), act, dt)
+    D.close(B.glu_i8(x, w, sw, v, sv, act=act), want, bound, "h")
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 15, 16])
+def test_decode_rows_of_8_bit_weights(M):
+    """Every row count of the decode form, on both sides of the size up to which
+    it quantises x itself; a row's result does not depend on the others'."""
+    B = binding()
+    g = gen(M)
+    for K in (16, 250, 16384 // M, 16384 // M + 1, 5000):
+        log(f"case decode {M} {K}")
+        x = rnd(g, M, K, dt=BF)
+        w, sw = B.quant_rows(rnd(g, 70, K, std=K ** -0.5))
+        y = B.linear_i8(x, w, sw)
+        q, s = D.quant(x)
+        check_linear(y, q, s, w, sw, None, BF)
+        for r in (0, M - 1):
+            assert torch.equal(B.linear_i8(x[r:r + 1], w, sw)[0], y[r])
 
 
 def test_quant_rows_borders_and_extremes():
