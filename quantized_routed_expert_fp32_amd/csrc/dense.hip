@@ -75,14 +75,12 @@ template <int T> __device__ __forceinline__ uint16_t to16(float v) {
 __device__ __forceinline__ uint16_t to16_rt(float v, int dt) {
   return dt == DT_BF16 ? to16<DT_BF16>(v) : to16<DT_F16>(v);
 }
-__device__ __forceinline__ float from16_rt(uint16_t b, int dt) {
-  return dt == DT_BF16 ? __uint_as_float((uint32_t)b << 16) : (float)__builtin_bit_cast(f16, b);
-}
-// four consecutive outputs of a row, the first at column p of np
-__device__ __forceinline__ void store4(void* row, int p, int np, int dt, bool vec, const float* v) {
+// four consecutive outputs of a row, the first at column p of np (global
+// stores take any alignment)
+__device__ __forceinline__ void store4(void* row, int p, int np, int dt, const float* v) {
   if (dt == DT_F32) {
     float* o = static_cast<float*>(row) + p;
-    if (vec && p + 4 <= np) *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    if (p + 4 <= np) __builtin_memcpy(o, v, 16);
     else
       for (int i = 0; i < 4; ++i)
         if (p + i < np) o[i] = v[i];
@@ -92,8 +90,7 @@ __device__ __forceinline__ void store4(void* row, int p, int np, int dt, bool ve
   uint16_t b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) b[i] = to16_rt(v[i], dt);
-  if (vec && p + 4 <= np)
-    *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+  if (p + 4 <= np) __builtin_memcpy(o, b, 8);
   else
     for (int i = 0; i < 4; ++i)
       if (p + i < np) o[i] = b[i];
@@ -104,10 +101,6 @@ __device__ __forceinline__ char* out_row(const DenseArgs& a, int q) {
   if (q >= a.qpad && q < a.qpad + a.qseg) return static_cast<char*>(a.out1) + (q - a.qpad) * a.ldo * 2;
   return nullptr;
 }
-__device__ __forceinline__ bool vec_ok(const void* p, int64_t ld, int es) {
-  return ((uintptr_t)p % (4 * es) == 0) && (ld % 4 == 0);
-}
-
 // The epilogues on four consecutive columns p.. of row q. `s0` and `s1` are
 // the sums (gate and up for GLU) as fp32 or int32, `sq` the row's scale.
 template <int T, int EPI, typename V>
@@ -129,9 +122,8 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
     }
     if (a.save) {
       float* sv = static_cast<float*>(a.save) + (int64_t)q * 2 * a.np;
-      const bool vec = vec_ok(a.save, a.np, 4);
-      store4(sv, p, a.np, DT_F32, vec, g);
-      store4(sv + a.np, p, a.np, DT_F32, vec, u);
+      store4(sv, p, a.np, DT_F32, g);
+      store4(sv + a.np, p, a.np, DT_F32, u);
     }
   } else if constexpr (EPI == EPI_SCALE) {
 #pragma unroll
@@ -144,7 +136,7 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
     for (int i = 0; i < 4; ++i) v[i] = s0[i];
   }
   char* row = out_row(a, q);
-  if (row) store4(row, p, a.np, a.out_dt, vec_ok(a.out0, a.ldo, 2) && (!a.qpad || vec_ok(a.out1, a.ldo, 2)), v);
+  if (row) store4(row, p, a.np, a.out_dt, v);
 }
 
 // ------------------------------------------------------- loads into the ring
@@ -489,7 +481,7 @@ struct Dense {
   // would be 32 bytes of 16 rows)
   template <int ES, int COLS> static constexpr int row_bytes() { return COLS * ES + 16; }
   template <int ES, int COLS, typename RowOf>
-  static __device__ __forceinline__ void flush(const uint8_t* buf, int lane, int q0, int nq, int p0, int np, bool vec,
+  static __device__ __forceinline__ void flush(const uint8_t* buf, int lane, int q0, int nq, int p0, int np,
                                                RowOf row) {
     constexpr int CH = COLS * ES / 16, N = 16 / ES;
     asm volatile("" ::: "memory");     // other lanes' writes: LDS runs in order
@@ -503,7 +495,7 @@ struct Dense {
       char* o = row(q);
       if (!o) continue;
       o += (int64_t)p * ES;
-      if (vec && p + N <= np) *reinterpret_cast<u32x4*>(o) = v;
+      if (p + N <= np) __builtin_memcpy(o, &v, 16);      // at any alignment
       else
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -519,9 +511,6 @@ struct Dense {
     else
       *reinterpret_cast<uint2*>(at) = make_uint2(to16<DT>(v[0]) | (uint32_t)to16<DT>(v[1]) << 16,
                                                  to16<DT>(v[2]) | (uint32_t)to16<DT>(v[3]) << 16);
-  }
-  static __device__ __forceinline__ bool whole16(const void* p, int64_t ld, int es) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
   }
 
   // The wave's TP x TQ part of the tile: in acc[i][j] a lane holds column
@@ -545,7 +534,7 @@ struct Dense {
           for (int g = 0; g < OG; ++g)
             *reinterpret_cast<acc_t*>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4) = acc[gate(g) + 2 * k][j];
           float* base = part + (k ? a.pcols / 2 : 0);
-          flush<4, OC>(buf, lane, q0 + 16 * j, a.nq, p0, lim, true,
+          flush<4, OC>(buf, lane, q0 + 16 * j, a.nq, p0, lim,
                        [&](int q) { return reinterpret_cast<char*>(base + (int64_t)q * a.pcols); });
         }
       return;
@@ -563,8 +552,6 @@ struct Dense {
           sp1[g][e] = second ? second[p] : 0.f;
         }
     }
-    const bool vec = whole16(a.out0, a.ldo, 2) && (!a.qpad || whole16(a.out1, a.ldo, 2));
-    const bool vecs = GLU && whole16(a.save, a.np, 4);
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
       const int q = q0 + 16 * j;
@@ -591,7 +578,7 @@ struct Dense {
             for (int g = 0; g < OG; ++g)
               put4<DT_F32>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4, k ? s1[g] : s0[g]);
             float* base = static_cast<float*>(a.save) + k * a.np;
-            flush<4, OC>(buf, lane, q, a.nq, p0, a.np, vecs,
+            flush<4, OC>(buf, lane, q, a.nq, p0, a.np,
                          [&](int qq) { return reinterpret_cast<char*>(base + (int64_t)qq * 2 * a.np); });
           }
         }
@@ -605,7 +592,7 @@ struct Dense {
         if (a.out_dt == DT_BF16) put4<DT_BF16>(at, s0[g]);
         else put4<DT_F16>(at, s0[g]);
       }
-      flush<2, OC>(buf, lane, q, a.nq, p0, a.np, vec, [&](int qq) { return out_row(a, qq); });
+      flush<2, OC>(buf, lane, q, a.nq, p0, a.np, [&](int qq) { return out_row(a, qq); });
     }
   }
 };
