@@ -8,4 +8,5 @@ from .binding import (  # noqa: F401
     MoeError, layer_desc, pack_layer, pack_layer_host, pack_size, route, experts,
     experts_decode, experts_grouped, workspace_size,
     glu_forward, glu_backward, glu_i8, quant_rows, linear_i8, glu_workspace_size,
+    linear_i8_workspace_size,
 )

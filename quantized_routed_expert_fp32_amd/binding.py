@@ -677,10 +677,8 @@ def quant_rows(x, q=None, scale=None, stream=None):
     return q, scale
 
 
-def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=None, stream=None):
-    """moe_linear_i8: y = x w^T (+ bias) for int8 w [out, in] with fp32 channel
-    scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
-    int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default)."""
+def _linear_args(x, w, s_w, bias, x_scale, out_dtype):
+    """(argument block, output dtype, device index) of a linear_i8 call."""
     import torch
     f32 = torch.float32
     if x_scale is None:
@@ -705,6 +703,27 @@ def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=Non
         raise MoeError("s_w: needed with int8 weights")
     a = LinearC(R, K, N, code, w.data_ptr(), ldw, _flat(s_w, "s_w", N, f32, dev), _flat(bias, "bias", N, f32, dev),
                 x.data_ptr(), ldx, _flat(x_scale, "x_scale", R, f32, dev))
+    return a, dt, dev
+
+
+def _linear_need(a):
+    n = C.c_uint64()
+    st = lib().moe_linear_i8_workspace_size(C.byref(a), C.byref(n))
+    if st:
+        _check(st, "moe_linear_i8_workspace_size")
+    return n.value
+
+
+def linear_i8_workspace_size(x, w, s_w, x_scale=None) -> int:
+    """moe_linear_i8_workspace_size of a call on these tensors, in bytes."""
+    return _linear_need(_linear_args(x, w, s_w, None, x_scale, None)[0])
+
+
+def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=None, stream=None):
+    """moe_linear_i8: y = x w^T (+ bias) for int8 w [out, in] with fp32 channel
+    scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
+    int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default)."""
+    a, dt, dev = _linear_args(x, w, s_w, bias, x_scale, out_dtype)
     ctx = _call_ctx(dev, stream)
     if ctx is None:
         return _linear_i8(a, dt, dev, y, ws, stream)
@@ -714,15 +733,12 @@ def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=Non
 
 def _linear_i8(a, dt, dev, y, ws, stream):
     import torch
-    n = C.c_uint64()
-    st = lib().moe_linear_i8_workspace_size(C.byref(a), C.byref(n))
-    if st:
-        _check(st, "moe_linear_i8_workspace_size")
+    n = _linear_need(a)
     if y is None:
         y, ldy = torch.empty((a.rows, a.out), dtype=dt, device=dev), a.out
     else:
         ldy = _rows2d(y, "y", dt, (a.rows, a.out), dev)
-    wp, wn, ws = _workspace(n.value, ws, dev)
+    wp, wn, ws = _workspace(n, ws, dev)
     st = lib().moe_linear_i8(C.byref(a), y.data_ptr(), ldy, wp, wn, _raw_stream(dev, stream))
     if st:
         _check(st, "moe_linear_i8")

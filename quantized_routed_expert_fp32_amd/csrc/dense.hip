@@ -861,16 +861,17 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
 
 // ----------------------------------------------------------- small kernels
 // Up to three operands copied to zero-padded rows of 16-byte chunks in one
-// launch: a wave a row.
+// launch, a workgroup a row (a wave a row took 6.9 us for 2315 rows of 1283,
+// bound by its own round trips).
 template <int ES>
 __global__ __launch_bounds__(256) void k_dense_pad(DensePad j) {
-  int r = blockIdx.x * 4 + threadIdx.x / 64, o = 0;
+  int r = blockIdx.x, o = 0;
   while (o < 2 && r >= j.rows[o]) r -= j.rows[o++];
   if (r >= j.rows[o]) return;
   const uint8_t* src = static_cast<const uint8_t*>(j.src[o]) + (int64_t)r * j.ld[o] * ES;
   u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(j.dst[o]) + (int64_t)r * j.ldd * ES);
   const int chunks = (int)(j.ldd * ES / 16);
-  for (int c = threadIdx.x & 63; c < chunks; c += 64) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
+  for (int c = threadIdx.x; c < chunks; c += 256) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
 }
 
 // One workgroup a row, 16 bytes of x a thread at a time; the first QUANT_HOLD
@@ -1060,7 +1061,7 @@ hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a
 hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s) {
   const int64_t rows = (int64_t)j.rows[0] + j.rows[1] + j.rows[2];
   if (!rows) return hipSuccess;
-  const dim3 grid((uint32_t)((rows + 3) / 4));
+  const dim3 grid((uint32_t)rows);
   if (esize == 1) hipLaunchKernelGGL((k_dense_pad<1>), grid, dim3(256), 0, s, j);
   else hipLaunchKernelGGL((k_dense_pad<2>), grid, dim3(256), 0, s, j);
   return hipGetLastError();

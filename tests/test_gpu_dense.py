@@ -167,6 +167,77 @@ def test_decode_rows_of_8_bit_weights(M):
             assert torch.equal(B.linear_i8(x[r:r + 1], w, sw)[0], y[r])
 
 
+def test_longest_contraction():
+    """in = 65536, the most that int32 sums of 127^2 hold, decode and chunk form."""
+    B = binding()
+    K = 65536
+    w = torch.full((5, K), 127, dtype=torch.int8, device="cuda")
+    w[1] = -127
+    w[2, ::2] = -127
+    sw = torch.ones(5, device="cuda")
+    for M in (2, 40):
+        x = torch.full((M, K), 127, dtype=torch.int8, device="cuda")
+        y = B.linear_i8(x, w, sw, x_scale=torch.full((M,), 2.0 ** -30, device="cuda"))
+        top = torch.tensor(127.0 * 127 * K * 2.0 ** -30).bfloat16()       # 127^2 K has 14 significant bits: exact in fp32
+        want = torch.stack([top, -top, 0 * top, top, top]).cuda()
+        assert torch.equal(y, want.expand(M, 5))
+        h = B.glu_i8(x, w[:1], sw[:1] * 0 + 1e-9, w[2:3], sw[:1], x_scale=torch.ones(M, device="cuda"))
+        assert (h == 0).all()
+
+
+def test_most_rows():
+    """2^20 rows through every kernel with a workgroup a row."""
+    B = binding()
+    M, H, I = 1 << 20, 8, 8
+    x, wg, wu, dh = block(3, M, H, I, BF)
+    h, gu = B.glu_forward(x, wg, wu, save=True)
+    check_forward(x, wg, wu, h, "silu")
+    got = B.glu_backward(dh, x, wg, wu, gu)
+    for name, t, (want, bound) in zip(("dx", "dw_gate", "dw_up"), got, D.grads(x, wg, wu, gu, dh, "silu", BF)):
+        D.close(t, want, bound, name)
+    w, sw = B.quant_rows(wg)
+    y = B.linear_i8(x, w, sw)
+    check_linear(y, *D.quant(x), w, sw, None, BF)
+    assert torch.equal(y[-7:], B.linear_i8(x[-7:], w, sw))
+
+
+def test_calls_at_once():
+    """Calls on two streams at once, each with its own workspace, and two graphs replayed at once."""
+    B = binding()
+    sets = [block(60 + i, 300 + 50 * i, 520, 264, BF) for i in range(2)]
+
+    def step(s):
+        x, wg, wu, dh = s
+        h, gu = B.glu_forward(x, wg, wu, save=True)
+        w, sw = B.quant_rows(wu)
+        return (h, *B.glu_backward(dh, x, wg, wu, gu), B.linear_i8(x, w, sw))
+
+    want = [step(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    for st, s in zip(streams, sets):
+        with torch.cuda.stream(st):
+            step(s)
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(s))
+        graphs.append(g)
+    for _ in range(3):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(step(s))
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, a, b in zip(want, got, outs):
+            for t, u, v in zip(w, a, b):
+                assert torch.equal(t, u) and torch.equal(t, v)
+
+
 def test_quant_rows_borders_and_extremes():
     """Ties, rows of zeros, the smallest and largest values, infinities and NaN."""
     B = binding()
