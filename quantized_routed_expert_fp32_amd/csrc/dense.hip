@@ -1,6 +1,34 @@
 // Dense feed-forward products beside the routed experts: the gated block
-// h = act(x Wg^T) * (x Wu^T) in 16 bits with its gradients, and products of
-// 8-bit integers with a scale per token and per channel.
+//   g = x Wg^T, u = x Wu^T, h = act(g) u
+// in 16 bits, its gradients
+//   dg = dh u act'(g), du = dh act(g),
+//   dx = dg Wg + du Wu (one contraction over [dg | du]), dWg = dg^T x, dWu = du^T x,
+// and products of 8-bit integers with a scale per token and per channel, which
+// the gated block takes too.
+//
+//  * k_dense: all of the products for more than 16 rows, on four workgroup
+//    tiles (dense_tile picks one and, for few tiles, a number of K ranges).
+//  * k_dense_decode: up to 16 rows, the weights straight from memory into
+//    16x16 matrix instructions, one launch.
+//  * k_quant_rows (rows to 8 bits), k_glu_grad (dg and du), k_dense_pad (rows
+//    the tiles cannot read in place), k_dense_join (K ranges): one pass over
+//    memory each.
+// Sums are fp32 (int32 for 8-bit operands, exact), in a fixed order. Rounded
+// to 16 bits: the outputs, and dg and du, because the matrix instructions of
+// their two products take 16-bit operands; g and u are kept in fp32 for the
+// gradients (kept in 16 bits they cost dx and dW as much error again as dg,
+// du and the outputs together: 3.1e-3 of their norm in bf16 against 2.4e-3,
+// where rounding the outputs alone is 1.7e-3).
+//
+// What bounds the large products is the card's power: on normal data 16x16
+// matrix instructions alone run 2.02 PFLOP/s bf16 and 4.26 POP/s 8-bit, the
+// 32x32 ones 1.75 and 3.55 (zeros: 2.44 and 4.87 both), which is why every
+// product here is 16x16. With the loads into LDS the 8192 x 4096 x 8192
+// training step's three products run at 1.31 to 1.42 PFLOP/s (kernel times
+// 842, 794 and 818 us), 8192 x 4096 -> 8192 8-bit at 2.4 POP/s (229 us);
+// leaving the loads out of the loop would take 17% off, leaving zeros in the
+// operands 30%, at the same cycle count. A library's products of the same
+// shapes take 832, 916 and 1030 us, its 8-bit one runs at 2.1 POP/s.
 #include "dense_launch.h"
 
 #include <algorithm>
@@ -19,7 +47,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------------ element types
 template <int T> struct Elem;
 template <> struct Elem<DT_BF16> {
-  typedef __bf16 type;
   typedef f32x4 acc4;
   static constexpr int SIZE = 2;
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
@@ -28,7 +55,6 @@ template <> struct Elem<DT_BF16> {
   }
 };
 template <> struct Elem<DT_F16> {
-  typedef f16 type;
   typedef f32x4 acc4;
   static constexpr int SIZE = 2;
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
@@ -37,7 +63,6 @@ template <> struct Elem<DT_F16> {
   }
 };
 template <> struct Elem<DT_I8> {
-  typedef int8_t type;
   typedef i32x4 acc4;
   static constexpr int SIZE = 1;
   static __device__ __forceinline__ acc4 mma16(u32x4 p, u32x4 q, acc4 c) {
@@ -140,13 +165,16 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
 }
 
 // ------------------------------------------------------- loads into the ring
-// 64 x 16 bytes from base + off (a lane's own) to LDS [lds, lds + 1024). The
-// compiler does not see it, so a read of the ring is ordered by step_wait.
+// A wave-uniform address, in scalar registers.
 __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
 }
+// 64 x 16 bytes from base + off (a lane's own) to LDS [lds, lds + 1024). In
+// asm, because the compiler would guard every LDS read against the loads in
+// flight by waiting for all of them; it has no register outputs, and reads of
+// what it writes are ordered by step_wait.
 __device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const uint8_t* base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
 }
@@ -164,12 +192,24 @@ template <int N> __device__ __forceinline__ void step_wait() {
 __device__ const u32x4 g_zero16 = {0, 0, 0, 0};
 
 // ---------------------------------------------------------------- the product
-// Workgroup tile BP x BQ; a K step is KB bytes of a k-contiguous row (KB / 2
-// k of 16 bits), KB = 128 or 64. k-contiguous operand in LDS: rows of KB
-// bytes, 16-byte chunk c of row r at position c ^ swz_kc(r), so 16 lanes
-// reading one chunk of 16 rows meet 16 different bank groups. k-major
-// operand: rows k of 2 B bytes, 32-byte segment s at s ^ swz_km(k), so the 4
-// rows of a transposed read do.
+// Workgroup tile BP x BQ of WP x WQ waves; a K step is KB bytes of a
+// k-contiguous row (KB / 2 k of 16 bits). Both operands go from memory straight
+// into an LDS ring. k-contiguous operand: rows of KB bytes, 16-byte chunk c of
+// row r at position c ^ (r & 7), so the rows that are read together meet
+// different banks. k-major operand (the gradients' weights and activations,
+// never transposed in memory): rows k of 2 B bytes, 32-byte segment s at s ^
+// swz_km(k), so the 4 rows of a transposed read do. Counted at 8192 x 4096 x
+// 8192: 1 to 4% of the LDS cycles are conflicts, LDS is busy 27% of the time,
+// the matrix units 64 to 67%, the L2 serves 77 to 81% of the loads (a band of 4
+// x 8 tiles an XCD: 12 operand tiles for 32 workgroups' 64).
+//
+// 256 x 256, 8 waves of 64 x 128: 128 accumulators, 2 waves a SIMD to cover
+// each other's waits (4 waves of 128 x 128 read a third less LDS but spill: 1398
+// us against 940 for the 8192 x 4096 -> 2 x 8192 forward); its epilogue is
+// alone on the CU (160 KiB of LDS), 5 us a tile. The smaller tiles fill the CUs
+// when there are few rows and are bound by a step's latency (barrier, LDS
+// reads); 8 waves on 128 x 128 take 15% off 4, and two k blocks a unit in
+// 256-byte steps 20 to 30% off one in 128-byte steps on 64 x 64.
 template <int T, int EPI, int FORM, int BP, int BQ, int WP, int WQ, int R, int KB, int KU>
 struct Dense {
   static constexpr int RPM = 1;                    // fragment reads a product
@@ -186,7 +226,7 @@ struct Dense {
   static_assert(LP * NW * 1024 == PB && LQ * NW * 1024 == QB && LP == LQ, "whole loads");
   static_assert(R % 2 == 1 && R >= 5, "ring");
 
-  static __device__ __forceinline__ int swz_kc(int r) { return KB >= 128 ? r & 7 : (r >> 2) & 3; }
+  static __device__ __forceinline__ int swz_kc(int r) { return r & 7; }
   // the same for k and k + 4
   template <int B> static __device__ __forceinline__ int swz_km(int k) {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
@@ -718,7 +758,7 @@ __device__ __forceinline__ uint32_t codes4(const RowScale& rs, const float* f) {
 // straight from memory at any alignment: bound by the weights' bytes, or by
 // latency when there are few. XT = DT_BF16 / DT_F16 (8-bit weights only): x is
 // quantised by every workgroup into LDS, while its first weights arrive.
-constexpr int DEC_QUANT = 32;     // elements a thread quantises at most: nq k <= 1024 * 32
+constexpr int DEC_QUANT = 32;     // elements a thread holds while it quantises
 
 template <int T, int EPI, int XT, int NF>
 __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
@@ -1026,6 +1066,11 @@ hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a,
   return hipErrorInvalidValue;
 }
 
+// Whether a decode call quantises x in its own launch: where that costs each
+// workgroup little (half of what its threads can hold) and the workgroups run
+// in one round. 1 x 2048 -> 2048: 5.2 us against 3.5 + 2.5 and a launch between;
+// 16 x 2048 -> 2 x 512 (twice the bound): 9.6 us against 7.4 in two launches; 1 x
+// 4096 -> 2 x 8192 (two rounds): 20.9 against 17.3.
 bool dense_decode_quantises(int epi, int rows, int k, int np) {
   return (int64_t)rows * k <= 1024 * DEC_QUANT / 2 && np <= 512 * (epi == EPI_GLU ? 8 : 16);
 }
@@ -1040,6 +1085,9 @@ static hipError_t decode_launch_nf(const DenseDecodeArgs& a, hipStream_t s) {
 template <int T, int EPI, int XT>
 static hipError_t decode_launch(const DenseDecodeArgs& a, hipStream_t s) {
   constexpr int OP = EPI == EPI_GLU ? 8 : 16;
+  // Two fragments a workgroup halve the reads of x (from the L2), where enough
+  // workgroups are left and x is not small: 16 x 4096 -> 2 x 8192 bf16 30.8 us
+  // against 34.8; 2 x 2048 outputs would take 13.9 against 11.0.
   if (XT == DT_I8 && a.d.nq > 4 && a.d.np >= 512 * OP) return decode_launch_nf<T, EPI, XT, XT == DT_I8 ? 2 : 1>(a, s);
   return decode_launch_nf<T, EPI, XT, 1>(a, s);
 }
