@@ -698,17 +698,6 @@ template <> struct Row<DT_F32> {
   static __device__ __forceinline__ float f(float b) { return b; }
 };
 
-// q = round-half-even(x / s) of the exact quotient, |q| <= 127. The fp32
-// quotient decides unless it lies next to a half-integer; there the 53-bit
-// quotient of the two 24-bit numbers does (x - s (n + 1/2) is either zero or
-// at least 2^-32 of x, so 53 bits tell the two apart).
-__device__ __forceinline__ int quant1(float x, float s, float inv) {
-  float t = x * inv;
-  float n = __builtin_rintf(t);
-  if (__builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) < 1e-3f) n = (float)__builtin_rint((double)x / (double)s);
-  return (int)__builtin_fminf(__builtin_fmaxf(n, -127.f), 127.f);
-}
-
 template <int T> __device__ __forceinline__ void unpack16(u32x4 v, float* f) {
   if constexpr (T == DT_F32) {
 #pragma unroll
@@ -722,20 +711,44 @@ template <int T> __device__ __forceinline__ void unpack16(u32x4 v, float* f) {
   }
 }
 
-// Scale, reciprocal (0: every code is 0) of a row whose largest |x| has the
-// bits m, and the code of one value.
+// Scale of a row whose largest |x| has the bits m, and its codes: q =
+// round-half-even of the exact x / s, |q| <= 127, 0 where s is not positive.
+// The fp32 product with the reciprocal (two roundings: off by at most 127 2^-24
+// = 7.6e-6) decides, four values at a time, unless one of them lies within 2e-5
+// of a half-integer or the reciprocal overflows (a subnormal scale); then
+// 53-bit quotients do: x - s (n + 1/2) is zero or at least 2^-32 of x, so 53
+// bits tell the two apart. (A wider margin sends whole waves there: with 1e-3 the
+// 8-bit block of 1 x 2048 -> 2 x 512 takes 5.5 us instead of 5.2.)
 struct RowScale {
   float s, inv;
-  bool wide;    // the reciprocal does not overflow (it may for a subnormal scale)
+  bool fast;
   __device__ __forceinline__ explicit RowScale(uint32_t m) {
     s = m < 0x7F800000u ? __uint_as_float(m) / 127.f : __builtin_nanf("");
     inv = s > 0.f ? 1.f / s : 0.f;
-    wide = inv < 3e38f;
+    fast = s > 0.f && inv < 3e38f;
   }
-  __device__ __forceinline__ int code(float x) const {
-    if (!(s > 0.f)) return 0;
-    return wide ? quant1(x, s, inv)
-                : (int)__builtin_fmin(__builtin_fmax(__builtin_rint((double)x / (double)s), -127.0), 127.0);
+  __device__ __forceinline__ uint32_t exact(float x) const {
+    const double q = __builtin_rint((double)x / (double)s);
+    return s > 0.f ? (uint32_t)(int)__builtin_fmin(__builtin_fmax(q, -127.0), 127.0) & 255u : 0u;
+  }
+  // four codes, the first in the low byte
+  __device__ __forceinline__ uint32_t codes4(const float* f) const {
+    float n[4], far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = f[e] * inv;
+      n[e] = __builtin_rintf(t);
+      far = __builtin_fmaxf(far, __builtin_fabsf(t - n[e]));
+    }
+    uint32_t o = 0;
+    if (fast && far < 0.49998f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o |= ((uint32_t)(int)n[e] & 255u) << (8 * e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o |= exact(f[e]) << (8 * e);
+    }
+    return o;
   }
 };
 template <int T, int N> __device__ __forceinline__ uint32_t top_bits(const float* f, uint32_t m) {
@@ -743,13 +756,6 @@ template <int T, int N> __device__ __forceinline__ uint32_t top_bits(const float
   for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
   return m;
 }
-__device__ __forceinline__ uint32_t codes4(const RowScale& rs, const float* f) {
-  uint32_t o = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o |= (uint32_t)(rs.code(f[e]) & 255) << (8 * e);
-  return o;
-}
-
 // --------------------------------------------------------------- decode rows
 // nq <= 16: a workgroup of 16 waves computes 16 weight rows (GLU: 8 gate and
 // 8 up) against every activation row on 16x16 matrix instructions; the waves
@@ -849,7 +855,7 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
       for (int h = 0; h < DEC_QUANT / 8; ++h) {
         const int at = (h * per + i0) * 8;
         if (at < chunks * 256)
-          *reinterpret_cast<uint2*>(s_x + row * xs + at) = make_uint2(codes4(rs, f[h]), codes4(rs, f[h] + 4));
+          *reinterpret_cast<uint2*>(s_x + row * xs + at) = make_uint2(rs.codes4(f[h]), rs.codes4(f[h] + 4));
       }
     }
     __syncthreads();
@@ -954,7 +960,7 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
     unpack16<T>(v, f);
     uint32_t o[N / 4];
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) o[i] = codes4(rs, f + 4 * i);
+    for (int i = 0; i < N / 4; ++i) o[i] = rs.codes4(f + 4 * i);
     if constexpr (VEC && N == 8) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(o[0], o[1]);
     else if constexpr (VEC) *reinterpret_cast<uint32_t*>(qr + c * 4) = o[0];
     else
