@@ -424,7 +424,8 @@ int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, float* gu, void* ws,
 
 /* Gradients of the block from dh [rows, inter] (row stride lddh) and the gu of
  * the forward call:
- *   dg = dh * u * act'(g), du = dh * act(g)       (rounded to dtype once)
+ *   dg = dh * u * act'(g), du = dh * act(g)       (rounded to dtype once; up to 32
+ *                                                 rows to a high and a low part)
  *   dx = dg Wg + du Wu   [rows, hidden], row stride lddx
  *   dw_gate = dg^T x, dw_up = du^T x   [inter, hidden] contiguous
  * dx may be NULL, or dw_gate and dw_up both (not wanted, not computed).

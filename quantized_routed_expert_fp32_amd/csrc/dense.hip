@@ -15,7 +15,8 @@
 //    memory each.
 // Sums are fp32 (int32 for 8-bit operands, exact), in a fixed order. Rounded
 // to 16 bits: the outputs, and dg and du, because the matrix instructions of
-// their two products take 16-bit operands; g and u are kept in fp32 for the
+// their two products take 16-bit operands (up to 32 rows they go as a high and
+// a low part, in tile rows that would be idle); g and u are kept in fp32 for the
 // gradients (kept in 16 bits they cost dx and dW as much error again as dg,
 // du and the outputs together: 3.1e-3 of their norm in bf16 against 2.4e-3,
 // where rounding the outputs alone is 1.7e-3).
@@ -231,13 +232,16 @@ struct Dense {
   template <int B> static __device__ __forceinline__ int swz_km(int k) {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
   }
+  // the x row of k row k, where D's rows are high and low parts in groups of 16 (see DenseArgs::fold)
+  static __device__ __forceinline__ int pair_row(int k) { return (k >> 5) * 16 + (k & 15); }
   // whether load i of wave w holds up rows (GLU: rows interleaved 32 gate, 32 up)
   static __device__ __forceinline__ bool is_up(int i, int w) {
     return EPI == EPI_GLU && (((i * NW + w) * (64 / CPR)) >> 5 & 1);
   }
   // source offset of load i of a lane, k-contiguous rows clamped below n
   template <bool KM, int B, int L, bool GLU>
-  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld0, int64_t ld1) {
+  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld0, int64_t ld1,
+                                                 int fold = 0) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int q = (i * NW + w) * 64 + lane;
@@ -252,7 +256,7 @@ struct Dense {
         const int k = q / RC, pos = q % RC;
         const int s = (pos >> 1) ^ swz_km<B>(k);
         const int col = c0 + (s * 2 + (pos & 1)) * 8;
-        off[i] = (uint32_t)k * ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
+        off[i] = (uint32_t)(fold ? pair_row(k) : k) * ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
       }
     }
   }
@@ -301,14 +305,15 @@ struct Dense {
     // them, and the masked rest (up to one step a segment), which the last
     // range takes. NN: two segments of P rows, gate then up.
     const int z = blockIdx.y;
-    const int nws = PKM ? a.krows / KR : a.kbytes / KB;
-    const bool rest = PKM ? a.krows % KR != 0 : a.kbytes % KB != 0;
+    const bool pairs = FORM == FORM_TN && a.fold;      // (at most 64 k rows: one masked step)
+    const int nws = pairs ? 0 : PKM ? a.krows / KR : a.kbytes / KB;
+    const bool rest = pairs || (PKM ? a.krows % KR != 0 : a.kbytes % KB != 0);
     constexpr int NSEG = FORM == FORM_NN ? 2 : 1;
     const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * z / a.splits));
     const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * (z + 1) / a.splits));
 
     uint32_t offp[LP], offq[LQ];
-    offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1);
+    offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1, FORM == FORM_TN ? a.fold : 0);
     offsets<QKM, BQ, LQ, false>(offq, w, lane, c0q, a.nq, a.ldq, a.ldq);
     // NN's second segment counts its offsets in its own stride
     uint32_t offp1[FORM == FORM_NN ? LP : 1];
@@ -367,7 +372,8 @@ struct Dense {
 #pragma unroll
       for (int n = 0; n < LP; ++n) {
         const int q = (n * NW + w) * 64 + lane;
-        const bool inp = PKM ? q / (BP * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
+        bool inp = PKM ? q / (BP * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
+        if (pairs) inp = inp && pair_row(q / (BP * 2 / 16)) < a.fold;
         const bool inq = QKM ? q / (BQ * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
         dma16_at(rp.lds + n * NW * 1024, inp ? base_p(rp, n) + off_p(rp, n) : zero);
         dma16_at(rq.lds + n * NW * 1024, inq ? rq.b + offq[n] : zero);
@@ -563,18 +569,29 @@ struct Dense {
     constexpr int OG = OC / 16;                        // groups of 16
     const int col = lane & 15, quad = lane >> 4;
     auto gate = [](int g) { return GLU ? g / 2 * 4 + g % 2 : g; };
+    // pairs of Q rows (high and low parts): one output row each
+    const int fold = EPI == EPI_OUT && FORM == FORM_NN ? a.fold : 0, nq = fold ? fold : a.nq;
+    const int js = fold ? FQ / 2 : FQ;
+    if (fold) {
+      q0 /= 2;
+#pragma unroll
+      for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ / 2; ++j) acc[i][j] = acc[i][2 * j] + acc[i][2 * j + 1];
+    }
     if (a.splits > 1) {
-      float* part = a.part + (int64_t)z * a.nq * a.pcols;
+      float* part = a.part + (int64_t)z * nq * a.pcols;
       const int lim = (int)(GLU ? a.pcols / 2 : a.pcols);
 #pragma unroll
       for (int j = 0; j < FQ; ++j)
 #pragma unroll
         for (int k = 0; k < (GLU ? 2 : 1); ++k) {
+          if (j >= js) continue;
 #pragma unroll
           for (int g = 0; g < OG; ++g)
             *reinterpret_cast<acc_t*>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4) = acc[gate(g) + 2 * k][j];
           float* base = part + (k ? a.pcols / 2 : 0);
-          flush<4, OC>(buf, lane, q0 + 16 * j, a.nq, p0, lim,
+          flush<4, OC>(buf, lane, q0 + 16 * j, nq, p0, lim,
                        [&](int q) { return reinterpret_cast<char*>(base + (int64_t)q * a.pcols); });
         }
       return;
@@ -594,9 +611,10 @@ struct Dense {
     }
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
+      if (j >= js) continue;
       const int q = q0 + 16 * j;
       float sq = 1.f;
-      if constexpr (T == DT_I8) sq = a.sq[min(q + col, a.nq - 1)];
+      if constexpr (T == DT_I8) sq = a.sq[min(q + col, nq - 1)];
       float s0[OG][4], s1[OG][4];
 #pragma unroll
       for (int g = 0; g < OG; ++g)
@@ -618,7 +636,7 @@ struct Dense {
             for (int g = 0; g < OG; ++g)
               put4<DT_F32>(buf + col * row_bytes<4, OC>() + (g * 16 + quad * 4) * 4, k ? s1[g] : s0[g]);
             float* base = static_cast<float*>(a.save) + k * a.np;
-            flush<4, OC>(buf, lane, q, a.nq, p0, a.np,
+            flush<4, OC>(buf, lane, q, nq, p0, a.np,
                          [&](int qq) { return reinterpret_cast<char*>(base + (int64_t)qq * 2 * a.np); });
           }
         }
@@ -632,7 +650,7 @@ struct Dense {
         if (a.out_dt == DT_BF16) put4<DT_BF16>(at, s0[g]);
         else put4<DT_F16>(at, s0[g]);
       }
-      flush<2, OC>(buf, lane, q, a.nq, p0, a.np, [&](int qq) { return out_row(a, qq); });
+      flush<2, OC>(buf, lane, q, nq, p0, a.np, [&](int qq) { return out_row(a, qq); });
     }
   }
 };
@@ -648,7 +666,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
   const int p = (blockIdx.y * 256 + threadIdx.x) * 4, q = blockIdx.x;
   if (p >= a.np) return;
   typedef typename Elem<T>::acc4 acc4;
-  const int64_t stride = (int64_t)a.nq * a.pcols;
+  const int64_t stride = (int64_t)gridDim.x * a.pcols;
   const float* r0 = a.part + q * a.pcols + p;
   const float* r1 = r0 + (EPI == EPI_GLU ? a.pcols / 2 : 0);
   acc4 v0 = *reinterpret_cast<const acc4*>(r0), v1 = *reinterpret_cast<const acc4*>(r1);
@@ -711,6 +729,17 @@ template <int T> __device__ __forceinline__ void unpack16(u32x4 v, float* f) {
   }
 }
 
+template <int DT> __device__ __forceinline__ u32x4 pack16(const float* f) {
+  u32x4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = to16<DT>(f[2 * k]) | (uint32_t)to16<DT>(f[2 * k + 1]) << 16;
+  return v;
+}
+// what rounding v to 16 bits leaves (nothing where that is not finite)
+template <int DT> __device__ __forceinline__ float low_part(float v) {
+  const float hi = Row<DT>::f(to16<DT>(v));
+  return __builtin_fabsf(hi) < __builtin_inff() ? v - hi : 0.f;
+}
 // Scale of a row whose largest |x| has the bits m, and its codes: q =
 // round-half-even of the exact x / s, |q| <= 127, 0 where s is not positive.
 // The fp32 product with the reciprocal (two roundings: off by at most 127 2^-24
@@ -977,39 +1006,47 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
 }
 
 // [dg | du] from dh and the kept g, u, 8 elements a thread: 14 bytes an
-// element through memory, which bounds it.
-template <int DT>
-__global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int inter,
-                                                  int ip, uint16_t* d) {
+// element through memory, which bounds it (196 us for 8192 x 8192, 4.8 TB/s).
+// PAIRS: each row as a high and a low part, in groups of 16 rows of each (see
+// DenseArgs::fold), the last group filled up with zero rows.
+template <int DT, bool PAIRS>
+__global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
+                                                  int inter, int ip, uint16_t* d) {
   const int64_t r = blockIdx.x;
   const float* g = gu + r * 2 * inter;
   const int i = (blockIdx.y * 256 + threadIdx.x) * 8;
   if (i >= ip) return;
+  const bool row = !PAIRS || r < rows;
   float e[8], gv[8], uv[8];
-  unpack16<DT>(i < inter ? load_chunk<2>(dh + r * lddh, i * 2, inter * 2) : u32x4{0, 0, 0, 0}, e);
+  unpack16<DT>(row && i < inter ? load_chunk<2>(dh + r * lddh, i * 2, inter * 2) : u32x4{0, 0, 0, 0}, e);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const bool in = i + 4 * k < inter;
+    const bool in = row && i + 4 * k < inter;
     unpack16<DT_F32>(in ? load_chunk<4>(g, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, gv + 4 * k);
     unpack16<DT_F32>(in ? load_chunk<4>(g + inter, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, uv + 4 * k);
   }
-  u32x4 a, b;
+  float dg[8], du[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t lo[2], hi[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float v, dv;
-      act_grad_f(gv[2 * k + n], act, &v, &dv);
-      lo[n] = to16<DT>(e[2 * k + n] * uv[2 * k + n] * dv);
-      hi[n] = to16<DT>(e[2 * k + n] * v);
-    }
-    a[k] = lo[0] | lo[1] << 16;
-    b[k] = hi[0] | hi[1] << 16;
+  for (int k = 0; k < 8; ++k) {
+    float v, dv;
+    act_grad_f(gv[k], act, &v, &dv);
+    dg[k] = e[k] * uv[k] * dv;
+    du[k] = e[k] * v;
   }
-  u32x4* o = reinterpret_cast<u32x4*>(d + r * 2 * ip + i);
-  o[0] = a;
-  o[ip / 8] = b;
+  const int64_t at = PAIRS ? (r / 16) * 32 + r % 16 : r;
+  u32x4* o = reinterpret_cast<u32x4*>(d + at * 2 * ip + i);
+  o[0] = pack16<DT>(dg);
+  o[ip / 8] = pack16<DT>(du);
+  if constexpr (PAIRS) {
+    o += 16 * (2 * ip / 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      dg[k] = low_part<DT>(dg[k]);
+      du[k] = low_part<DT>(du[k]);
+    }
+    o[0] = pack16<DT>(dg);
+    o[ip / 8] = pack16<DT>(du);
+  }
 }
 
 // --------------------------------------------------------------- launchers
@@ -1037,7 +1074,8 @@ static hipError_t launch_tile(const DenseArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3((uint32_t)tiles, a.splits), dim3(WP * WQ * 64), lds, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((k_dense_join<T, EPI>), dim3(a.nq, (a.np + 1023) / 1024), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_dense_join<T, EPI>), dim3(FORM == FORM_NN && a.fold ? a.fold : a.nq, (a.np + 1023) / 1024), dim3(256), 0,
+                     s, a);
   return hipGetLastError();
 }
 
@@ -1144,13 +1182,20 @@ hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int c
   return hipGetLastError();
 }
 
-hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
-                           int ip, void* d, hipStream_t s) {
-  const dim3 grid(rows, (ip + 2047) / 2048);
+template <int DT>
+static void grad_launch(bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip,
+                        void* d, hipStream_t s) {
+  const dim3 grid(pairs ? (rows + 15) / 16 * 16 : rows, (ip + 2047) / 2048);
   const uint16_t* e = static_cast<const uint16_t*>(dh);
   uint16_t* o = static_cast<uint16_t*>(d);
-  if (dt == DT_BF16) hipLaunchKernelGGL((k_glu_grad<DT_BF16>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
-  else hipLaunchKernelGGL((k_glu_grad<DT_F16>), grid, dim3(256), 0, s, act, e, lddh, gu, inter, ip, o);
+  if (pairs) hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o);
+  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o);
+}
+
+hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
+                           int inter, int ip, void* d, hipStream_t s) {
+  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, s);
+  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, s);
   return hipGetLastError();
 }
 

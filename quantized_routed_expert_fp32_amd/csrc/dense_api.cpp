@@ -13,6 +13,7 @@ using namespace moe;
 namespace {
 
 constexpr int kDecodeRows = 16;          // rows the decode form takes
+constexpr int kPairRows = 32;            // rows whose dg and du go as high and low parts
 constexpr int kMaxDim = 65536;           // hidden, inter, out: int32 sums of 127^2 stay below 2^31
 constexpr int kMaxRows = 1 << 20;
 constexpr int64_t kMaxLd = 1 << 22;      // 255 rows of 16-bit elements stay below 2^32 bytes
@@ -96,8 +97,9 @@ GluPlan plan_forward(const moe_glu* a, int dt) {
 }
 
 struct GradPlan {
-  bool pad_x, pad_g, pad_u;
+  bool pad_x, pad_g, pad_u, pairs;
   int64_t kp, ip;
+  int parts;              // rows of D
   int tile_x, splits_x, tile_w, splits_w;
   uint64_t d_off, x_off, g_off, u_off, part_off, total;
 };
@@ -107,7 +109,9 @@ GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
   p.kp = up(a->hidden, 8);
   p.ip = up(a->inter, 64);
   Bump b;
-  p.d_off = b.take((uint64_t)a->rows * 2 * p.ip * 2);
+  p.pairs = a->rows <= kPairRows;
+  p.parts = p.pairs ? (int)up(a->rows, 16) * 2 : a->rows;
+  p.d_off = b.take((uint64_t)p.parts * 2 * p.ip * 2);
   p.pad_x = dw && !plain_rows(a->x, a->ldx, a->hidden, 2);
   p.pad_g = dx && !plain_rows(a->w_gate, a->ldw_gate, a->hidden, 2);
   p.pad_u = dx && !plain_rows(a->w_up, a->ldw_up, a->hidden, 2);
@@ -117,11 +121,11 @@ GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
   p.splits_x = p.splits_w = 1;
   uint64_t part = 0;
   if (dx) {
-    p.tile_x = dense_tile(EPI_OUT, a->hidden, a->rows, (int)(2 * p.ip / 64), &p.splits_x);
+    p.tile_x = dense_tile(EPI_OUT, a->hidden, p.parts, (int)(2 * p.ip / 64), &p.splits_x);
     part = std::max(part, part_bytes(p.splits_x, a->rows, up(a->hidden, 4)));
   }
   if (dw) {
-    p.tile_w = dense_tile(EPI_OUT, a->hidden, (int)(2 * p.ip), (a->rows + 63) / 64, &p.splits_w);
+    p.tile_w = dense_tile(EPI_OUT, a->hidden, (int)(2 * p.ip), (p.parts + 63) / 64, &p.splits_w);
     part = std::max(part, part_bytes(p.splits_w, 2 * p.ip, up(a->hidden, 4)));
   }
   p.part_off = b.take(part);
@@ -349,7 +353,7 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = launch_glu_grad(a->dtype, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off, s);
+  hipError_t e = launch_glu_grad(a->dtype, p.pairs, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off, s);
   Padder pad(a->hidden, p.kp, 2);
   const Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
   const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
@@ -360,6 +364,7 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   d.q0 = w + p.d_off;
   d.ldq = 2 * p.ip * 2;
   d.np = a->hidden;
+  d.fold = p.pairs ? a->rows : 0;
   d.out_dt = a->dtype;
   d.part = reinterpret_cast<float*>(w + p.part_off);
   d.pcols = up(a->hidden, 4);
@@ -370,7 +375,7 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
     dd.p1 = u.p;
     dd.ldp0 = g.ld;
     dd.ldp1 = u.ld;
-    dd.nq = a->rows;
+    dd.nq = p.parts;
     dd.kbytes = (int)(2 * p.ip * 2);
     dd.krows = a->inter;
     dd.segbytes = (int)(p.ip * 2);
@@ -386,7 +391,7 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
     dd.p0 = x.p;
     dd.ldp0 = x.ld;
     dd.nq = (int)(2 * p.ip);
-    dd.krows = a->rows;
+    dd.krows = p.parts;
     dd.splits = p.splits_w;
     dd.out0 = dw_gate;
     dd.out1 = dw_up;

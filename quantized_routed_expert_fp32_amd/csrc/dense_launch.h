@@ -30,6 +30,11 @@ struct DenseArgs {
   int segbytes;           // NN: Q bytes of the first segment
   int splits;             // K ranges (1: the epilogue runs in the product)
   int act;
+  // Gradients of few rows: D's rows are pairs of a high and a low 16-bit part, 16
+  // high rows, then their 16 low ones, and so on (the last group zero behind the
+  // rows). fold = rows (0: no pairs). NN: nq counts the parts, the output has
+  // fold rows. TN: krows counts the parts (at most 64), P has fold rows.
+  int fold;
   // outputs
   void* out0;             // [nq, np] (weight gradients: rows below qseg)
   void* out1;             // weight gradients: rows from qpad on
@@ -72,8 +77,8 @@ hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
 // q[r, 0..ldq) (zero behind cols), scale[r]
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, hipStream_t s);
-// D[r] = [dg | du], each ip wide (zero behind inter)
-hipError_t launch_glu_grad(int dt, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter,
-                           int ip, void* d, hipStream_t s);
+// D[r] = [dg | du], each ip wide (zero behind inter); pairs: see DenseArgs::fold
+hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
+                           int inter, int ip, void* d, hipStream_t s);
 
 }  // namespace moe

@@ -25,7 +25,7 @@ hipError_t launch_dense_pad(int, const DensePad&, hipStream_t) { return hipError
 hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64_t, float*, hipStream_t) {
   return hipErrorNoDevice;
 }
-hipError_t launch_glu_grad(int, int, const void*, int64_t, const float*, int, int, int, void*, hipStream_t) {
+hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, int, int, int, void*, hipStream_t) {
   return hipErrorNoDevice;
 }
 

@@ -87,13 +87,16 @@ def grads(x, wg, wu, gu, dh, name, dt):
     # act' = p + g p (1 - p) w': |p (1 - p) g w'| <= 1.2, both terms to act_u
     eg = (e * u).abs() * (1.0 + 1.2) * (act_u(g, name) + 8) * U
     eu = du.abs() * (act_u(g, name) + 2) * U
-    eg = eg + E16[dt] * (dg.abs() + eg) + SUB[dt]
-    eu = eu + E16[dt] * (du.abs() + eu) + SUB[dt]
     I, M = g.shape[1], g.shape[0]
+    # rounded to 16 bits, or (up to 32 rows) to a high and a low part: half a
+    # step of what half a step leaves
+    e16 = E16[dt] if M > 32 else E16[dt] ** 2
+    eg = eg + e16 * (dg.abs() + eg) + SUB[dt]
+    eu = eu + e16 * (du.abs() + eu) + SUB[dt]
     dx = dg @ wg + du @ wu
-    # 2 inter terms, and up to 16 partial sums more
-    bx = eg @ wg.abs() + eu @ wu.abs() + (2 * I + 16) * U * ((dg.abs() + eg) @ wg.abs() + (du.abs() + eu) @ wu.abs())
+    # 2 inter terms (twice: parts), and up to 16 partial sums more
+    bx = eg @ wg.abs() + eu @ wu.abs() + (4 * I + 16) * U * ((dg.abs() + eg) @ wg.abs() + (du.abs() + eu) @ wu.abs())
     out = [(dx, bx)]
     for d, b in ((dg, eg), (du, eu)):
-        out.append((d.t() @ x, b.t() @ x.abs() + (M + 16) * U * ((d.abs() + b).t() @ x.abs())))
+        out.append((d.t() @ x, b.t() @ x.abs() + (2 * M + 16) * U * ((d.abs() + b).t() @ x.abs())))
     return [(v, b + E16[dt] * (v.abs() + b) + SUB[dt]) for v, b in out]

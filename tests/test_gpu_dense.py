@@ -150,6 +150,28 @@ def test_every_tile(M, H, I):
     D.close(B.glu_i8(x, w, sw, v, sv, act=act), want, bound, "h")
 
 
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("dt", [BF, FP], ids=IDS.get)
+def test_gradients_of_few_rows(M, dt):
+    """On both sides of the 32 rows up to which dg and du go as high and low
+    parts (the bounds of the gradients count them), with one K range and several."""
+    B = binding()
+    for H, I in ((72, 40), (264, 4096), (1001, 129)):
+        log(f"case few rows {M} {H} {I} {dt}")
+        x, wg, wu, dh = block(M * H, M, H, I, dt)
+        _, gu = B.glu_forward(x, wg, wu, save=True)
+        got = B.glu_backward(dh, x, wg, wu, gu)
+        for name, t, (want, bound) in zip(("dx", "dw_gate", "dw_up"), got, D.grads(x, wg, wu, gu, dh, "silu", dt)):
+            D.close(t, want, bound, name)
+    # a gradient beyond the type's range: infinite, not NaN, and in its own row
+    if dt == FP:
+        x, wg, wu, dh = block(1, M, 64, 32, dt)
+        gu = B.glu_forward(x, wg, wu, save=True)[1]
+        gu[0] = 1e6          # act' = 1, so dg = 1e6: infinite in fp16, and so is act(g)
+        dx = B.glu_backward(torch.ones_like(dh), x, torch.ones_like(wg), torch.ones_like(wu), gu, need_dw=False)[0]
+        assert (dx[0] == float("inf")).all() and torch.isfinite(dx[1:]).all()
+
+
 @pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 15, 16])
 def test_decode_rows_of_8_bit_weights(M):
     """Every row count of the decode form, on both sides of the size up to which
