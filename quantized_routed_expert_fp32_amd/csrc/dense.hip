@@ -701,6 +701,25 @@ __device__ __forceinline__ u32x4 load_chunk(const void* row, int64_t byte, int64
   return v;
 }
 
+// Row r of the operands that are copied to zero-padded rows of 16-byte chunks,
+// by a workgroup of 256 (a wave a row took 6.9 us for 2315 rows of 1283, bound by
+// its own round trips). The copies ride in the grid of the kernel that has to run
+// before the product anyway, where there is one: dx at 777 x 1283 x 769 fp16
+// 26.4 us, 29.3 with a launch of their own.
+template <int ES> __device__ __forceinline__ void pad_row(const DensePad& j, int r) {
+  // Selects, not j.src[o]: an index known at run time moves j into scratch
+  // (the copies of 777, 769 and 769 rows of 1283: 5 us, and 13 from scratch).
+  const int r1 = r - j.rows[0], r2 = r1 - j.rows[1];
+  const int64_t i = r2 >= 0 ? r2 : r1 >= 0 ? r1 : r;
+  if (r2 >= j.rows[2]) return;
+  const int64_t ld = r2 >= 0 ? j.ld[2] : r1 >= 0 ? j.ld[1] : j.ld[0];
+  const uint8_t* src = static_cast<const uint8_t*>(r2 >= 0 ? j.src[2] : r1 >= 0 ? j.src[1] : j.src[0]) + i * ld * ES;
+  u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(r2 >= 0 ? j.dst[2] : r1 >= 0 ? j.dst[1] : j.dst[0]) +
+                                        i * j.ldd * ES);
+  const int chunks = (int)(j.ldd * ES / 16);
+  for (int c = threadIdx.x; c < chunks; c += 256) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
+}
+
 // ---------------------------------------------------------------- quantising
 template <int T> struct Row;
 template <> struct Row<DT_BF16> {
@@ -935,19 +954,7 @@ __global__ __launch_bounds__(1024) void k_dense_decode(DenseDecodeArgs da) {
 }
 
 // ----------------------------------------------------------- small kernels
-// Up to three operands copied to zero-padded rows of 16-byte chunks in one
-// launch, a workgroup a row (a wave a row took 6.9 us for 2315 rows of 1283,
-// bound by its own round trips).
-template <int ES>
-__global__ __launch_bounds__(256) void k_dense_pad(DensePad j) {
-  int r = blockIdx.x, o = 0;
-  while (o < 2 && r >= j.rows[o]) r -= j.rows[o++];
-  if (r >= j.rows[o]) return;
-  const uint8_t* src = static_cast<const uint8_t*>(j.src[o]) + (int64_t)r * j.ld[o] * ES;
-  u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(j.dst[o]) + (int64_t)r * j.ldd * ES);
-  const int chunks = (int)(j.ldd * ES / 16);
-  for (int c = threadIdx.x; c < chunks; c += 256) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
-}
+template <int ES> __global__ __launch_bounds__(256) void k_dense_pad(DensePad j) { pad_row<ES>(j, blockIdx.x); }
 
 // One workgroup a row, 16 bytes of x a thread at a time; the first QUANT_HOLD
 // of a thread stay in registers between the maximum and the codes, longer rows
@@ -955,8 +962,12 @@ __global__ __launch_bounds__(256) void k_dense_pad(DensePad j) {
 // groups at such an address. Bound by memory: 3 bytes an element for 16-bit rows.
 constexpr int QUANT_HOLD = 4;
 template <int T, bool VEC>
-__global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type* x, int64_t ldx, int cols, int8_t* q,
-                                                    int64_t ldq, float* scale) {
+__global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type* x, int64_t ldx, int rows, int cols,
+                                                    int8_t* q, int64_t ldq, float* scale, DensePad pad) {
+  if (blockIdx.x >= (uint32_t)rows) {
+    pad_row<1>(pad, blockIdx.x - rows);
+    return;
+  }
   constexpr int ES = sizeof(typename Row<T>::type), N = 16 / ES;
   __shared__ uint32_t red[4];
   const int64_t r = blockIdx.x;
@@ -1011,7 +1022,12 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
 // DenseArgs::fold), the last group filled up with zero rows.
 template <int DT, bool PAIRS>
 __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
-                                                  int inter, int ip, uint16_t* d) {
+                                                  int inter, int ip, uint16_t* d, DensePad pad) {
+  const int drows = PAIRS ? (rows + 15) / 16 * 16 : rows;
+  if (blockIdx.x >= (uint32_t)drows) {
+    if (blockIdx.y == 0) pad_row<2>(pad, blockIdx.x - drows);
+    return;
+  }
   const int64_t r = blockIdx.x;
   const float* g = gu + r * 2 * inter;
   const int i = (blockIdx.y * 256 + threadIdx.x) * 8;
@@ -1150,52 +1166,52 @@ hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a
   return decode_launch<DT_I8, EPI_SCALE, DT_I8>(a, s);
 }
 
+static uint32_t pad_rows(const DensePad* j) { return j ? (uint32_t)(j->rows[0] + j->rows[1] + j->rows[2]) : 0; }
+
 hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s) {
-  const int64_t rows = (int64_t)j.rows[0] + j.rows[1] + j.rows[2];
-  if (!rows) return hipSuccess;
-  const dim3 grid((uint32_t)rows);
-  if (esize == 1) hipLaunchKernelGGL((k_dense_pad<1>), grid, dim3(256), 0, s, j);
-  else hipLaunchKernelGGL((k_dense_pad<2>), grid, dim3(256), 0, s, j);
+  if (!pad_rows(&j)) return hipSuccess;
+  if (esize == 1) hipLaunchKernelGGL((k_dense_pad<1>), dim3(pad_rows(&j)), dim3(256), 0, s, j);
+  else hipLaunchKernelGGL((k_dense_pad<2>), dim3(pad_rows(&j)), dim3(256), 0, s, j);
   return hipGetLastError();
 }
 
 template <int T>
 static void quant_launch(const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq, float* scale,
-                         hipStream_t s) {
+                         const DensePad* pad, hipStream_t s) {
   typedef typename Row<T>::type E;
   constexpr int N = T == DT_F32 ? 4 : 8;
   const bool vec = reinterpret_cast<uintptr_t>(q) % N == 0 && ldq % N == 0;
-  if (vec)
-    hipLaunchKernelGGL((k_quant_rows<T, true>), dim3(rows), dim3(256), 0, s, static_cast<const E*>(x), ldx, cols, q, ldq,
-                       scale);
-  else
-    hipLaunchKernelGGL((k_quant_rows<T, false>), dim3(rows), dim3(256), 0, s, static_cast<const E*>(x), ldx, cols, q,
-                       ldq, scale);
+  const dim3 grid((uint32_t)rows + pad_rows(pad));
+  const E* e = static_cast<const E*>(x);
+  const DensePad j = pad ? *pad : DensePad{};
+  if (vec) hipLaunchKernelGGL((k_quant_rows<T, true>), grid, dim3(256), 0, s, e, ldx, rows, cols, q, ldq, scale, j);
+  else hipLaunchKernelGGL((k_quant_rows<T, false>), grid, dim3(256), 0, s, e, ldx, rows, cols, q, ldq, scale, j);
 }
 
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
-                             float* scale, hipStream_t s) {
-  if (dt == DT_BF16) quant_launch<DT_BF16>(x, ldx, rows, cols, q, ldq, scale, s);
-  else if (dt == DT_F16) quant_launch<DT_F16>(x, ldx, rows, cols, q, ldq, scale, s);
-  else if (dt == DT_F32) quant_launch<DT_F32>(x, ldx, rows, cols, q, ldq, scale, s);
+                             float* scale, const DensePad* pad, hipStream_t s) {
+  if (dt == DT_BF16) quant_launch<DT_BF16>(x, ldx, rows, cols, q, ldq, scale, pad, s);
+  else if (dt == DT_F16) quant_launch<DT_F16>(x, ldx, rows, cols, q, ldq, scale, pad, s);
+  else if (dt == DT_F32) quant_launch<DT_F32>(x, ldx, rows, cols, q, ldq, scale, pad, s);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
 template <int DT>
 static void grad_launch(bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip,
-                        void* d, hipStream_t s) {
-  const dim3 grid(pairs ? (rows + 15) / 16 * 16 : rows, (ip + 2047) / 2048);
+                        void* d, const DensePad& pad, hipStream_t s) {
+  const dim3 grid((pairs ? (rows + 15) / 16 * 16 : rows) + pad_rows(&pad), (ip + 2047) / 2048);
   const uint16_t* e = static_cast<const uint16_t*>(dh);
   uint16_t* o = static_cast<uint16_t*>(d);
-  if (pairs) hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o);
-  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o);
+  if (pairs)
+    hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad);
+  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad);
 }
 
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, hipStream_t s) {
-  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, s);
-  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, s);
+                           int inter, int ip, void* d, const DensePad& pad, hipStream_t s) {
+  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, s);
+  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, s);
   return hipGetLastError();
 }
 

@@ -183,7 +183,7 @@ struct Padder {
     j.rows[n++] = rows;
     return {dst, j.ldd * es};
   }
-  hipError_t run(hipStream_t s) const { return n ? launch_dense_pad(es, j, s) : hipSuccess; }
+  hipError_t run(hipStream_t s) const { return n ? launch_dense_pad(es, j, s) : hipSuccess; }   // a launch of its own
 };
 
 int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, float* gu, void* ws, uint64_t ws_bytes,
@@ -200,12 +200,14 @@ int glu_run(const char* fn, const moe_glu* a, int dt, void* h, int64_t ldh, floa
   Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
   const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
   const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
-  hipError_t e = pad.run(s);
+  hipError_t e;
   if (p.inner) x.ld = a->ldx * 2;
-  if (e == hipSuccess && p.quant) {
+  if (p.quant) {
     e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->hidden, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
-                          reinterpret_cast<float*>(w + p.sx_off), s);
+                          reinterpret_cast<float*>(w + p.sx_off), &pad.j, s);
     x = {w + p.x_off, p.kp};
+  } else {
+    e = pad.run(s);
   }
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
@@ -353,12 +355,12 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = launch_glu_grad(a->dtype, p.pairs, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off, s);
   Padder pad(a->hidden, p.kp, 2);
   const Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
   const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
   const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
-  if (e == hipSuccess) e = pad.run(s);
+  hipError_t e = launch_glu_grad(a->dtype, p.pairs, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off,
+                                 pad.j, s);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.q0 = w + p.d_off;
@@ -415,7 +417,7 @@ int moe_quant_rows(const void* x, int dtype, int rows, int cols, int64_t ldx, in
   if ((st = check_dim(fn, "rows", rows, kMaxRows)) || (st = check_dim(fn, "cols", cols, kMaxDim)) ||
       (st = check_ld(fn, "ldx", ldx, cols)) || (st = check_ld(fn, "ldq", ldq, cols)))
     return st;
-  hipError_t e = launch_quant_rows(dtype == MOE_FP32 ? DT_F32 : dtype, x, ldx, rows, cols, q, ldq, scale,
+  hipError_t e = launch_quant_rows(dtype == MOE_FP32 ? DT_F32 : dtype, x, ldx, rows, cols, q, ldq, scale, nullptr,
                                    static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_bad(fn, e);
 }
@@ -442,12 +444,14 @@ int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t 
   Padder pad(a->in, p.kp, 1);
   Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
   const Rows m = pad.take(p.pad_w, a->w, a->ldw, a->out, w + p.w_off);
-  hipError_t e = pad.run(s);
+  hipError_t e;
   if (p.inner) x.ld = a->ldx * 2;
-  if (e == hipSuccess && p.quant) {
+  if (p.quant) {
     e = launch_quant_rows(a->dtype, a->x, a->ldx, a->rows, a->in, reinterpret_cast<int8_t*>(w + p.x_off), p.kp,
-                          reinterpret_cast<float*>(w + p.sx_off), s);
+                          reinterpret_cast<float*>(w + p.sx_off), &pad.j, s);
     x = {w + p.x_off, p.kp};
+  } else {
+    e = pad.run(s);
   }
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};

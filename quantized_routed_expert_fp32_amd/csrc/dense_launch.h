@@ -74,11 +74,13 @@ struct DensePad {
 bool dense_decode_quantises(int epi, int rows, int k, int np);
 hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a, hipStream_t s);
 hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
-// q[r, 0..ldq) (zero behind cols), scale[r]
+// q[r, 0..ldq) (zero behind cols), scale[r]; and the copies of pad (8-bit
+// operands), or null
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
-                             float* scale, hipStream_t s);
-// D[r] = [dg | du], each ip wide (zero behind inter); pairs: see DenseArgs::fold
+                             float* scale, const DensePad* pad, hipStream_t s);
+// D[r] = [dg | du], each ip wide (zero behind inter); pairs: see
+// DenseArgs::fold; and the copies of pad (16-bit operands)
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, hipStream_t s);
+                           int inter, int ip, void* d, const DensePad& pad, hipStream_t s);
 
 }  // namespace moe

@@ -22,10 +22,12 @@ hipError_t launch_dense(int, int, int, int, const DenseArgs&, hipStream_t) { ret
 bool dense_decode_quantises(int, int, int, int) { return true; }
 hipError_t launch_dense_decode(int, int, int, const DenseDecodeArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_dense_pad(int, const DensePad&, hipStream_t) { return hipErrorNoDevice; }
-hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64_t, float*, hipStream_t) {
+hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64_t, float*, const DensePad*,
+                             hipStream_t) {
   return hipErrorNoDevice;
 }
-hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, int, int, int, void*, hipStream_t) {
+hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, int, int, int, void*, const DensePad&,
+                           hipStream_t) {
   return hipErrorNoDevice;
 }
 
