@@ -685,13 +685,23 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseArgs a) {
 
 // -------------------------------------------------- rows at any alignment
 // 16 bytes of a row from byte `byte` on, of elements of ES bytes, zero from
-// byte `end` on. Global loads take any alignment.
-template <int ES>
+// byte `end` on. Global loads take any alignment. SHIFT: a chunk that passes the
+// end is the row's last 16 bytes, shifted, instead of up to 15 loads (8-bit
+// 333 x 1288 -> 776, both operands copied: 10.9 us for 11.6); the decode kernel
+// has no registers left for it.
+template <int ES, bool SHIFT = false>
 __device__ __forceinline__ u32x4 load_chunk(const void* row, int64_t byte, int64_t end) {
   const uint8_t* at = static_cast<const uint8_t*>(row) + byte;
   u32x4 v = {0, 0, 0, 0};
   if (byte + 16 <= end) {
     __builtin_memcpy(&v, at, 16);
+  } else if (SHIFT && end >= 16) {
+    __builtin_memcpy(&v, static_cast<const uint8_t*>(row) + (end - 16), 16);
+    const int n = (int)min(byte + 16 - end, (int64_t)16) * 8;
+    uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    lo = n < 64 ? lo >> n | hi << 1 << (63 - n) : n < 128 ? hi >> (n - 64) : 0;
+    hi = n < 64 ? hi >> n : 0;
+    v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   } else {
     uint8_t* b = reinterpret_cast<uint8_t*>(&v);
 #pragma unroll
@@ -717,7 +727,8 @@ template <int ES> __device__ __forceinline__ void pad_row(const DensePad& j, int
   u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(r2 >= 0 ? j.dst[2] : r1 >= 0 ? j.dst[1] : j.dst[0]) +
                                         i * j.ldd * ES);
   const int chunks = (int)(j.ldd * ES / 16);
-  for (int c = threadIdx.x; c < chunks; c += 256) dst[c] = load_chunk<ES>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
+  for (int c = threadIdx.x; c < chunks; c += 256)
+    dst[c] = load_chunk<ES, true>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
 }
 
 // ---------------------------------------------------------------- quantising

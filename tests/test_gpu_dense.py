@@ -120,6 +120,37 @@ def test_glu_i8(M, H, I, dt, act):
     assert torch.equal(B.glu_i8(gq, wg, sg, wu, su, act=act, x_scale=gs, out_dtype=dt), h)
 
 
+@pytest.mark.parametrize("K", [*range(15, 34), 4095, 4097, 4113])
+def test_copied_rows_of_every_length(K):
+    """Rows off 16 bytes, of each length modulo 16, among other values: the
+    copies hold the row and zeros behind it, whatever stands there."""
+    log(f"case copied rows {K}")
+    B = binding()
+    g = gen(K)
+    M, N, pad = 37, 29, -K % 16
+    wide = [torch.randint(-127, 128, (r, K + 5), generator=g, device="cuda", dtype=torch.int8) for r in (M, N)]
+    s, sw = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    x, w = (t[:, 3:3 + K] for t in wide)
+    # the same codes with zeros behind them on 16 bytes: the same exact sums
+    xz, wz = (torch.nn.functional.pad(t, (0, pad)) for t in (x, w))
+    y = B.linear_i8(x, w, sw, x_scale=s, out_dtype=BF)
+    assert torch.equal(y, B.linear_i8(xz, wz, sw, x_scale=s, out_dtype=BF))
+    v = rnd(g, M, K + 5, dt=BF)[:, 1:1 + K]              # x quantised in the launch that copies w
+    q, qs = B.quant_rows(v)
+    assert torch.equal(B.linear_i8(v, w, sw), B.linear_i8(q, w, sw, x_scale=qs, out_dtype=BF))
+    for dt in (BF, FP):
+        f = [torch.full((r, K + 3), float("nan"), device="cuda", dtype=dt) for r in (M, N, N)]
+        x, wg, wu = (t[:, 1:1 + K] for t in f)
+        for t, a in zip((x, wg, wu), block(K, M, K, N, dt)):
+            t.copy_(a)
+        h, gu = B.glu_forward(x, wg, wu, save=True)
+        check_forward(x, wg, wu, h, "silu")
+        dh = rnd(g, M, N, dt=dt)
+        got = B.glu_backward(dh, x, wg, wu, gu)
+        for name, t, (want, bound) in zip(("dx", "dw_gate", "dw_up"), got, D.grads(x, wg, wu, gu, dh, "silu", dt)):
+            D.close(t, want, bound, name)
+
+
 # sizes that take each tile of the products with one K range and with several:
 # 256 x 256, 128 x 128 (both step widths) and 64 x 64, in the forward products
 # and in each gradient, ragged in every dimension
