@@ -232,16 +232,13 @@ struct Dense {
   template <int B> static __device__ __forceinline__ int swz_km(int k) {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (B / 16 - 1);
   }
-  // the x row of k row k, where D's rows are high and low parts in groups of 16 (see DenseArgs::fold)
-  static __device__ __forceinline__ int pair_row(int k) { return (k >> 5) * 16 + (k & 15); }
   // whether load i of wave w holds up rows (GLU: rows interleaved 32 gate, 32 up)
   static __device__ __forceinline__ bool is_up(int i, int w) {
     return EPI == EPI_GLU && (((i * NW + w) * (64 / CPR)) >> 5 & 1);
   }
   // source offset of load i of a lane, k-contiguous rows clamped below n
   template <bool KM, int B, int L, bool GLU>
-  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld0, int64_t ld1,
-                                                 int fold = 0) {
+  static __device__ __forceinline__ void offsets(uint32_t* off, int w, int lane, int c0, int n, int64_t ld0, int64_t ld1) {
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int q = (i * NW + w) * 64 + lane;
@@ -256,7 +253,7 @@ struct Dense {
         const int k = q / RC, pos = q % RC;
         const int s = (pos >> 1) ^ swz_km<B>(k);
         const int col = c0 + (s * 2 + (pos & 1)) * 8;
-        off[i] = (uint32_t)(fold ? pair_row(k) : k) * ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
+        off[i] = (uint32_t)k * ld + (uint32_t)(min(col, (n - 1) & ~7) - c0) * 2;
       }
     }
   }
@@ -305,15 +302,14 @@ struct Dense {
     // them, and the masked rest (up to one step a segment), which the last
     // range takes. NN: two segments of P rows, gate then up.
     const int z = blockIdx.y;
-    const bool pairs = FORM == FORM_TN && a.fold;      // (at most 64 k rows: one masked step)
-    const int nws = pairs ? 0 : PKM ? a.krows / KR : a.kbytes / KB;
-    const bool rest = pairs || (PKM ? a.krows % KR != 0 : a.kbytes % KB != 0);
+    const int nws = PKM ? a.krows / KR : a.kbytes / KB;
+    const bool rest = PKM ? a.krows % KR != 0 : a.kbytes % KB != 0;
     constexpr int NSEG = FORM == FORM_NN ? 2 : 1;
     const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * z / a.splits));
     const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)NSEG * nws * (z + 1) / a.splits));
 
     uint32_t offp[LP], offq[LQ];
-    offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1, FORM == FORM_TN ? a.fold : 0);
+    offsets<PKM, BP, LP, EPI == EPI_GLU>(offp, w, lane, c0p, a.np, a.ldp0, a.ldp1);
     offsets<QKM, BQ, LQ, false>(offq, w, lane, c0q, a.nq, a.ldq, a.ldq);
     // NN's second segment counts its offsets in its own stride
     uint32_t offp1[FORM == FORM_NN ? LP : 1];
@@ -372,8 +368,7 @@ struct Dense {
 #pragma unroll
       for (int n = 0; n < LP; ++n) {
         const int q = (n * NW + w) * 64 + lane;
-        bool inp = PKM ? q / (BP * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
-        if (pairs) inp = inp && pair_row(q / (BP * 2 / 16)) < a.fold;
+        const bool inp = PKM ? q / (BP * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
         const bool inq = QKM ? q / (BQ * 2 / 16) < kr : ((q % CPR) ^ swz_kc(q / CPR)) * 16 < kb;
         dma16_at(rp.lds + n * NW * 1024, inp ? base_p(rp, n) + off_p(rp, n) : zero);
         dma16_at(rq.lds + n * NW * 1024, inq ? rq.b + offq[n] : zero);
@@ -569,7 +564,9 @@ struct Dense {
     constexpr int OG = OC / 16;                        // groups of 16
     const int col = lane & 15, quad = lane >> 4;
     auto gate = [](int g) { return GLU ? g / 2 * 4 + g % 2 : g; };
-    // pairs of Q rows (high and low parts): one output row each
+    // Pairs of Q rows (high and low parts): one output row each. Where the high
+    // part's sum is not finite the low part's stays out: an infinite weight times
+    // a low part of zero, or of the other sign, would turn infinity into NaN.
     const int fold = EPI == EPI_OUT && FORM == FORM_NN ? a.fold : 0, nq = fold ? fold : a.nq;
     const int js = fold ? FQ / 2 : FQ;
     if (fold) {
@@ -577,7 +574,12 @@ struct Dense {
 #pragma unroll
       for (int i = 0; i < FP; ++i)
 #pragma unroll
-        for (int j = 0; j < FQ / 2; ++j) acc[i][j] = acc[i][2 * j] + acc[i][2 * j + 1];
+        for (int j = 0; j < FQ / 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float hi = (float)acc[i][2 * j][e];
+            acc[i][j][e] = __builtin_fabsf(hi) < __builtin_inff() ? hi + acc[i][2 * j + 1][e] : hi;
+          }
     }
     if (a.splits > 1) {
       float* part = a.part + (int64_t)z * nq * a.pcols;
@@ -729,6 +731,30 @@ template <int ES> __device__ __forceinline__ void pad_row(const DensePad& j, int
   const int chunks = (int)(j.ldd * ES / 16);
   for (int c = threadIdx.x; c < chunks; c += 256)
     dst[c] = load_chunk<ES, true>(src, (int64_t)c * 16, (int64_t)j.cols * ES);
+}
+
+// The rows of x as the product with high and low parts of few rows takes them
+// (see DensePairs), a workgroup a row: zero where the low parts meet an element
+// that is not finite, whose product with the high part stands alone then
+// (infinity times a low part of zero, or of the other sign, is NaN).
+template <int DT> __device__ __forceinline__ void pair_row(const DensePairs& x, int r) {
+  const int i = (r >> 5) * 16 + (r & 15);
+  const bool low = r & 16;
+  constexpr uint32_t EXP = DT == DT_BF16 ? 0x7F80 : 0x7C00;
+  const uint8_t* src = static_cast<const uint8_t*>(x.src) + i * x.ld * 2;
+  u32x4* dst = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(x.dst) + r * x.ldd * 2);
+  const int chunks = (int)(x.ldd * 2 / 16);
+  for (int c = threadIdx.x; c < chunks; c += 256) {
+    u32x4 v = {0, 0, 0, 0};
+    if (i < x.rows) v = load_chunk<2, true>(src, (int64_t)c * 16, (int64_t)x.cols * 2);
+    if (low)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((v[k] & EXP) == EXP) v[k] &= 0xFFFF0000u;
+        if ((v[k] >> 16 & EXP) == EXP) v[k] &= 0xFFFFu;
+      }
+    dst[c] = v;
+  }
 }
 
 // ---------------------------------------------------------------- quantising
@@ -1033,10 +1059,14 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
 // DenseArgs::fold), the last group filled up with zero rows.
 template <int DT, bool PAIRS>
 __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
-                                                  int inter, int ip, uint16_t* d, DensePad pad) {
+                                                  int inter, int ip, uint16_t* d, DensePad pad, DensePairs px) {
   const int drows = PAIRS ? (rows + 15) / 16 * 16 : rows;
   if (blockIdx.x >= (uint32_t)drows) {
-    if (blockIdx.y == 0) pad_row<2>(pad, blockIdx.x - drows);
+    const int r = blockIdx.x - drows, pr = PAIRS && px.src ? 2 * drows : 0;
+    if (blockIdx.y == 0) {
+      if (r < pr) pair_row<DT>(px, r);
+      else pad_row<2>(pad, r - pr);
+    }
     return;
   }
   const int64_t r = blockIdx.x;
@@ -1210,19 +1240,20 @@ hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int c
 
 template <int DT>
 static void grad_launch(bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip,
-                        void* d, const DensePad& pad, hipStream_t s) {
-  const dim3 grid((pairs ? (rows + 15) / 16 * 16 : rows) + pad_rows(&pad), (ip + 2047) / 2048);
+                        void* d, const DensePad& pad, const DensePairs& px, hipStream_t s) {
+  const int drows = pairs ? (rows + 15) / 16 * 16 : rows;
+  const dim3 grid(drows + (pairs && px.src ? 2 * drows : 0) + pad_rows(&pad), (ip + 2047) / 2048);
   const uint16_t* e = static_cast<const uint16_t*>(dh);
   uint16_t* o = static_cast<uint16_t*>(d);
   if (pairs)
-    hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad);
-  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad);
+    hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px);
+  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px);
 }
 
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, const DensePad& pad, hipStream_t s) {
-  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, s);
-  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, s);
+                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, hipStream_t s) {
+  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, s);
+  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, s);
   return hipGetLastError();
 }
 

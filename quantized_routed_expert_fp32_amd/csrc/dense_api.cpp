@@ -112,10 +112,10 @@ GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
   p.pairs = a->rows <= kPairRows;
   p.parts = p.pairs ? (int)up(a->rows, 16) * 2 : a->rows;
   p.d_off = b.take((uint64_t)p.parts * 2 * p.ip * 2);
-  p.pad_x = dw && !plain_rows(a->x, a->ldx, a->hidden, 2);
+  p.pad_x = dw && !p.pairs && !plain_rows(a->x, a->ldx, a->hidden, 2);
   p.pad_g = dx && !plain_rows(a->w_gate, a->ldw_gate, a->hidden, 2);
   p.pad_u = dx && !plain_rows(a->w_up, a->ldw_up, a->hidden, 2);
-  if (p.pad_x) p.x_off = b.take((uint64_t)a->rows * p.kp * 2);
+  if (p.pad_x || (dw && p.pairs)) p.x_off = b.take((uint64_t)p.parts * p.kp * 2);   // pairs: a DensePairs copy
   if (p.pad_g) p.g_off = b.take((uint64_t)a->inter * p.kp * 2);
   if (p.pad_u) p.u_off = b.take((uint64_t)a->inter * p.kp * 2);
   p.splits_x = p.splits_w = 1;
@@ -356,11 +356,16 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   Padder pad(a->hidden, p.kp, 2);
-  const Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
+  Rows x = pad.take(p.pad_x, a->x, a->ldx, a->rows, w + p.x_off);
+  DensePairs px{};
+  if (p.pairs && dw_gate) {
+    px = {a->x, w + p.x_off, a->ldx, p.kp, a->rows, a->hidden};
+    x = {w + p.x_off, p.kp * 2};
+  }
   const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
   const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
   hipError_t e = launch_glu_grad(a->dtype, p.pairs, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off,
-                                 pad.j, s);
+                                 pad.j, px, s);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.q0 = w + p.d_off;

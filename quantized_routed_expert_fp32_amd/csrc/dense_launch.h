@@ -33,7 +33,7 @@ struct DenseArgs {
   // Gradients of few rows: D's rows are pairs of a high and a low 16-bit part, 16
   // high rows, then their 16 low ones, and so on (the last group zero behind the
   // rows). fold = rows (0: no pairs). NN: nq counts the parts, the output has
-  // fold rows. TN: krows counts the parts (at most 64), P has fold rows.
+  // fold rows. (TN: krows counts the parts, P is a DensePairs copy.)
   int fold;
   // outputs
   void* out0;             // [nq, np] (weight gradients: rows below qseg)
@@ -71,6 +71,17 @@ struct DensePad {
   int64_t ldd;   // a multiple of 16 bytes
 };
 
+// The copy of rows [rows, cols] of 16 bits (row stride ld) that meets D's high
+// and low parts in the product over rows: dst rows of ldd elements, for each
+// group of 16 rows the rows, then the same rows with zeros where they are not
+// finite; zero behind rows and behind cols. src = null: none.
+struct DensePairs {
+  const void* src;
+  void* dst;
+  int64_t ld, ldd;
+  int rows, cols;
+};
+
 bool dense_decode_quantises(int epi, int rows, int k, int np);
 hipError_t launch_dense_decode(int dt, int epi, int xt, const DenseDecodeArgs& a, hipStream_t s);
 hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
@@ -79,8 +90,8 @@ hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, const DensePad* pad, hipStream_t s);
 // D[r] = [dg | du], each ip wide (zero behind inter); pairs: see
-// DenseArgs::fold; and the copies of pad (16-bit operands)
+// DenseArgs::fold; and the copies of pad (16-bit operands) and px (with pairs)
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, const DensePad& pad, hipStream_t s);
+                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, hipStream_t s);
 
 }  // namespace moe
