@@ -429,7 +429,10 @@ int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, float* gu, void* ws,
  *   dx = dg Wg + du Wu   [rows, hidden], row stride lddx
  *   dw_gate = dg^T x, dw_up = du^T x   [inter, hidden] contiguous
  * dx may be NULL, or dw_gate and dw_up both (not wanted, not computed).
- * fp16: dg and du beyond 65504 become infinite, as h does. */
+ * fp16: dg and du beyond 65504 become infinite, as h does; all of them go into
+ * the products times one power of two a call, divided out of the sums again, so
+ * that small ones lose no more than 2^-39 of the largest (and half a step each):
+ * dh below the type's normal range costs no precision but its own. */
 int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                      void* dw_gate, void* dw_up, void* ws, uint64_t ws_bytes, void* stream);
 

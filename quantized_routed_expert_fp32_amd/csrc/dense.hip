@@ -10,9 +10,9 @@
 //    tiles (dense_tile picks one and, for few tiles, a number of K ranges).
 //  * k_dense_decode: up to 16 rows, the weights straight from memory into
 //    16x16 matrix instructions, one launch.
-//  * k_quant_rows (rows to 8 bits), k_glu_grad (dg and du), k_dense_pad (rows
-//    the tiles cannot read in place), k_dense_join (K ranges): one pass over
-//    memory each.
+//  * k_quant_rows (rows to 8 bits), k_glu_grad (dg and du; k_glu_top before it
+//    in fp16), k_dense_pad (rows the tiles cannot read in place), k_dense_join
+//    (K ranges): one pass over memory each.
 // Sums are fp32 (int32 for 8-bit operands, exact), in a fixed order. Rounded
 // to 16 bits: the outputs, and dg and du, because the matrix instructions of
 // their two products take 16-bit operands (up to 32 rows they go as a high and
@@ -127,6 +127,11 @@ __device__ __forceinline__ char* out_row(const DenseArgs& a, int q) {
   if (q >= a.qpad && q < a.qpad + a.qseg) return static_cast<char*>(a.out1) + (q - a.qpad) * a.ldo * 2;
   return nullptr;
 }
+// What a gradient's sums are multiplied by: fp16 operands carry a power of two (see k_glu_top)
+template <int T> __device__ __forceinline__ float grad_down(const DenseArgs& a) {
+  if constexpr (T == DT_F16) return *a.down;
+  else return 1.f;
+}
 // The epilogues on four consecutive columns p.. of row q. `s0` and `s1` are
 // the sums (gate and up for GLU) as fp32 or int32, `sq` the row's scale.
 template <int T, int EPI, typename V>
@@ -158,8 +163,9 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
       v[i] = (float)s0[i] * (sq * a.sp0[pi]) + (a.bias ? a.bias[pi] : 0.f);
     }
   } else {
+    const float down = grad_down<T>(a);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = s0[i];
+    for (int i = 0; i < 4; ++i) v[i] = s0[i] * down;
   }
   char* row = out_row(a, q);
   if (row) store4(row, p, a.np, a.out_dt, v);
@@ -611,6 +617,7 @@ struct Dense {
           sp1[g][e] = second ? second[p] : 0.f;
         }
     }
+    const float down = EPI == EPI_OUT ? grad_down<T>(a) : 1.f;
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
       if (j >= js) continue;
@@ -624,6 +631,7 @@ struct Dense {
         for (int e = 0; e < 4; ++e) {
           s0[g][e] = (float)acc[gate(g)][j][e];
           if constexpr (GLU) s1[g][e] = (float)acc[gate(g) + 2][j][e];
+          if constexpr (EPI == EPI_OUT) s0[g][e] *= down;
           if constexpr (T == DT_I8) {
             s0[g][e] *= sq * sp0[g][e];
             if constexpr (GLU) s1[g][e] *= sq * sp1[g][e];
@@ -1053,13 +1061,89 @@ __global__ __launch_bounds__(256) void k_quant_rows(const typename Row<T>::type*
   for (int c = QUANT_HOLD * 256 + threadIdx.x; c < chunks; c += 256) put(c, chunk(c));
 }
 
+// dg = dh u act'(g) and du = dh act(g) of 8 elements from column i on, from one
+// row's dh, g and u (g + inter); zero behind inter and where the row is not `in`.
+template <int DT>
+__device__ __forceinline__ void grad8(int act, const uint16_t* dh, const float* g, int i, int inter, bool in, float* dg,
+                                      float* du) {
+  float e[8], gv[8], uv[8];
+  unpack16<DT>(in && i < inter ? load_chunk<2>(dh, i * 2, inter * 2) : u32x4{0, 0, 0, 0}, e);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bool here = in && i + 4 * k < inter;
+    unpack16<DT_F32>(here ? load_chunk<4>(g, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, gv + 4 * k);
+    unpack16<DT_F32>(here ? load_chunk<4>(g + inter, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, uv + 4 * k);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float v, dv;
+    act_grad_f(gv[k], act, &v, &dv);
+    dg[k] = e[k] * uv[k] * dv;
+    du[k] = e[k] * v;
+  }
+}
+
+// fp16 has 11 bits from 2^-14 on only, and gradients are often smaller: dg and
+// du go into their products times 2^k, one k a call, and the epilogues multiply
+// by 2^-k. k (0 to 100) is the largest that leaves every |dg|, |du| that fp16
+// holds below 2^15, so they lose what fp16 does relative to the largest of
+// them (2^-39 of it at least: half a subnormal step). Values that are not finite
+// or too large for fp16 do not count, and become infinite as they are. This
+// kernel finds the largest: each workgroup of four groups of 256 threads, a group
+// a stretch of 2048 columns at a time, leaves its maximum in top[block]. It reads
+what k_glu_grad reads again: a backward call of 512 x 2048 x 512 takes 25.7 us
+with it and 21.8 without, 8192 x 4096 x 8192 2,010 and 1,870; without it dWg of
+512 rows with dh of deviation 1e-6 is 2.7e-2 off in norm, where rounding the
+outputs alone is 1.2e-3. bf16 has the range of fp32 and needs none of this.
+__global__ __launch_bounds__(1024) void k_glu_top(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
+                                                  int inter, uint32_t* top) {
+  __shared__ uint32_t red[16];
+  const int ny = (inter + 2047) / 2048, t = threadIdx.x & 255;
+  uint32_t m = 0;
+  for (int it = blockIdx.x * 4 + (threadIdx.x >> 8); it < rows * ny; it += gridDim.x * 4) {
+    const int64_t r = it / ny;
+    const int i = (it % ny * 256 + t) * 8;
+    if (i >= inter) continue;
+    float dg[8], du[8];
+    grad8<DT_F16>(act, dh + r * lddh, gu + r * 2 * inter, i, inter, true, dg, du);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = __builtin_fabsf(dg[k]), b = __builtin_fabsf(du[k]);
+      if (a < 65520.f) m = max(m, __float_as_uint(a));
+      if (b < 65520.f) m = max(m, __float_as_uint(b));
+    }
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) m = max(m, red[w]);
+    top[blockIdx.x] = m;
+  }
+}
+// the k of a call, for every thread of a workgroup of 256
+__device__ __forceinline__ int grad_shift(const uint32_t* top, int tops) {
+  __shared__ uint32_t red[4];
+  uint32_t m = 0;
+  for (int c = threadIdx.x; c < tops; c += 256) m = max(m, top[c]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = max(max(red[0], red[1]), max(red[2], red[3]));
+  return m ? min(max(14 + 127 - (int)(m >> 23), 0), 100) : 0;
+}
+
 // [dg | du] from dh and the kept g, u, 8 elements a thread: 14 bytes an
 // element through memory, which bounds it (196 us for 8192 x 8192, 4.8 TB/s).
 // PAIRS: each row as a high and a low part, in groups of 16 rows of each (see
-// DenseArgs::fold), the last group filled up with zero rows.
+// DenseArgs::fold), the last group filled up with zero rows. fp16: times 2^k
+// (k_glu_top's maxima in top), 2^-k left in `down`.
 template <int DT, bool PAIRS>
 __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
-                                                  int inter, int ip, uint16_t* d, DensePad pad, DensePairs px) {
+                                                  int inter, int ip, uint16_t* d, DensePad pad, DensePairs px,
+                                                  const uint32_t* top, int tops, float* down) {
   const int drows = PAIRS ? (rows + 15) / 16 * 16 : rows;
   if (blockIdx.x >= (uint32_t)drows) {
     const int r = blockIdx.x - drows, pr = PAIRS && px.src ? 2 * drows : 0;
@@ -1070,26 +1154,20 @@ __global__ __launch_bounds__(256) void k_glu_grad(int act, const uint16_t* dh, i
     return;
   }
   const int64_t r = blockIdx.x;
-  const float* g = gu + r * 2 * inter;
   const int i = (blockIdx.y * 256 + threadIdx.x) * 8;
-  if (i >= ip) return;
-  const bool row = !PAIRS || r < rows;
-  float e[8], gv[8], uv[8];
-  unpack16<DT>(row && i < inter ? load_chunk<2>(dh + r * lddh, i * 2, inter * 2) : u32x4{0, 0, 0, 0}, e);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const bool in = row && i + 4 * k < inter;
-    unpack16<DT_F32>(in ? load_chunk<4>(g, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, gv + 4 * k);
-    unpack16<DT_F32>(in ? load_chunk<4>(g + inter, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, uv + 4 * k);
-  }
   float dg[8], du[8];
+  grad8<DT>(act, dh + r * lddh, gu + r * 2 * inter, i, inter, !PAIRS || r < rows, dg, du);
+  if constexpr (DT == DT_F16) {
+    const int k = grad_shift(top, tops);
+    if (r == 0 && i == 0) *down = __builtin_ldexpf(1.f, -k);
+    const float up = __builtin_ldexpf(1.f, k);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float v, dv;
-    act_grad_f(gv[k], act, &v, &dv);
-    dg[k] = e[k] * uv[k] * dv;
-    du[k] = e[k] * v;
+    for (int n = 0; n < 8; ++n) {
+      dg[n] *= up;
+      du[n] *= up;
+    }
   }
+  if (i >= ip) return;
   const int64_t at = PAIRS ? (r / 16) * 32 + r % 16 : r;
   u32x4* o = reinterpret_cast<u32x4*>(d + at * 2 * ip + i);
   o[0] = pack16<DT>(dg);
@@ -1240,20 +1318,30 @@ hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int c
 
 template <int DT>
 static void grad_launch(bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows, int inter, int ip,
-                        void* d, const DensePad& pad, const DensePairs& px, hipStream_t s) {
+                        void* d, const DensePad& pad, const DensePairs& px, float* down, hipStream_t s) {
   const int drows = pairs ? (rows + 15) / 16 * 16 : rows;
   const dim3 grid(drows + (pairs && px.src ? 2 * drows : 0) + pad_rows(&pad), (ip + 2047) / 2048);
   const uint16_t* e = static_cast<const uint16_t*>(dh);
   uint16_t* o = static_cast<uint16_t*>(d);
+  uint32_t* top = reinterpret_cast<uint32_t*>(down) + 1;
+  int tops = 0;
+  if (DT == DT_F16) {
+    tops = (int)std::min<int64_t>(((int64_t)rows * ((inter + 2047) / 2048) + 3) / 4, GRAD_TOPS);
+    hipLaunchKernelGGL(k_glu_top, dim3(tops), dim3(1024), 0, s, act, e, lddh, gu, rows, inter, top);
+  }
   if (pairs)
-    hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px);
-  else hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px);
+    hipLaunchKernelGGL((k_glu_grad<DT, true>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px,
+                       top, tops, down);
+  else
+    hipLaunchKernelGGL((k_glu_grad<DT, false>), grid, dim3(256), 0, s, act, e, lddh, gu, rows, inter, ip, o, pad, px,
+                       top, tops, down);
 }
 
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, hipStream_t s) {
-  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, s);
-  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, s);
+                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, float* down,
+                           hipStream_t s) {
+  if (dt == DT_BF16) grad_launch<DT_BF16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, down, s);
+  else grad_launch<DT_F16>(pairs, act, dh, lddh, gu, rows, inter, ip, d, pad, px, down, s);
   return hipGetLastError();
 }
 

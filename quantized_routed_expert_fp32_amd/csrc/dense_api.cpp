@@ -101,7 +101,7 @@ struct GradPlan {
   int64_t kp, ip;
   int parts;              // rows of D
   int tile_x, splits_x, tile_w, splits_w;
-  uint64_t d_off, x_off, g_off, u_off, part_off, total;
+  uint64_t d_off, x_off, g_off, u_off, down_off, part_off, total;
 };
 
 GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
@@ -118,6 +118,7 @@ GradPlan plan_backward(const moe_glu* a, bool dx, bool dw) {
   if (p.pad_x || (dw && p.pairs)) p.x_off = b.take((uint64_t)p.parts * p.kp * 2);   // pairs: a DensePairs copy
   if (p.pad_g) p.g_off = b.take((uint64_t)a->inter * p.kp * 2);
   if (p.pad_u) p.u_off = b.take((uint64_t)a->inter * p.kp * 2);
+  if (a->dtype == MOE_FP16) p.down_off = b.take((1 + GRAD_TOPS) * 4);
   p.splits_x = p.splits_w = 1;
   uint64_t part = 0;
   if (dx) {
@@ -365,13 +366,14 @@ int moe_glu_backward(const moe_glu* a, const float* gu, const void* dh, int64_t 
   const Rows g = pad.take(p.pad_g, a->w_gate, a->ldw_gate, a->inter, w + p.g_off);
   const Rows u = pad.take(p.pad_u, a->w_up, a->ldw_up, a->inter, w + p.u_off);
   hipError_t e = launch_glu_grad(a->dtype, p.pairs, a->act, dh, lddh, gu, a->rows, a->inter, (int)p.ip, w + p.d_off,
-                                 pad.j, px, s);
+                                 pad.j, px, reinterpret_cast<float*>(w + p.down_off), s);
   if (e != hipSuccess) return hip_bad(fn, e);
   DenseArgs d{};
   d.q0 = w + p.d_off;
   d.ldq = 2 * p.ip * 2;
   d.np = a->hidden;
   d.fold = p.pairs ? a->rows : 0;
+  d.down = reinterpret_cast<const float*>(w + p.down_off);
   d.out_dt = a->dtype;
   d.part = reinterpret_cast<float*>(w + p.part_off);
   d.pcols = up(a->hidden, 4);

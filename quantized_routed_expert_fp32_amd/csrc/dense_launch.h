@@ -48,6 +48,7 @@ struct DenseArgs {
   const float* bias;      // SCALE: [np] or null
   float* part;            // splits > 1: [splits, nq, pcols] sums (int32 for 8-bit)
   int64_t pcols;
+  const float* down;      // gradients in fp16: the power of two that divides D's out again
 };
 
 // Decode rows (nq <= 16), any alignment: k elements per row. launch_dense_decode's
@@ -90,8 +91,12 @@ hipError_t launch_dense_pad(int esize, const DensePad& j, hipStream_t s);
 hipError_t launch_quant_rows(int dt, const void* x, int64_t ldx, int rows, int cols, int8_t* q, int64_t ldq,
                              float* scale, const DensePad* pad, hipStream_t s);
 // D[r] = [dg | du], each ip wide (zero behind inter); pairs: see
-// DenseArgs::fold; and the copies of pad (16-bit operands) and px (with pairs)
+// DenseArgs::fold; and the copies of pad (16-bit operands) and px (with pairs).
+// fp16: D times a power of two, its inverse in *down, in front of GRAD_TOPS
+// words of scratch (bf16: down is not used).
+constexpr int GRAD_TOPS = 512;
 hipError_t launch_glu_grad(int dt, bool pairs, int act, const void* dh, int64_t lddh, const float* gu, int rows,
-                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, hipStream_t s);
+                           int inter, int ip, void* d, const DensePad& pad, const DensePairs& px, float* down,
+                           hipStream_t s);
 
 }  // namespace moe

@@ -27,7 +27,7 @@ hipError_t launch_quant_rows(int, const void*, int64_t, int, int, int8_t*, int64
   return hipErrorNoDevice;
 }
 hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, int, int, int, void*, const DensePad&,
-                           const DensePairs&, hipStream_t) {
+                           const DensePairs&, float*, hipStream_t) {
   return hipErrorNoDevice;
 }
 
