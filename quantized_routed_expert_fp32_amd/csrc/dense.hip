@@ -1091,10 +1091,10 @@ __device__ __forceinline__ void grad8(int act, const uint16_t* dh, const float* 
 // or too large for fp16 do not count, and become infinite as they are. This
 // kernel finds the largest: each workgroup of four groups of 256 threads, a group
 // a stretch of 2048 columns at a time, leaves its maximum in top[block]. It reads
-what k_glu_grad reads again: a backward call of 512 x 2048 x 512 takes 25.7 us
-with it and 21.8 without, 8192 x 4096 x 8192 2,010 and 1,870; without it dWg of
-512 rows with dh of deviation 1e-6 is 2.7e-2 off in norm, where rounding the
-outputs alone is 1.2e-3. bf16 has the range of fp32 and needs none of this.
+// what k_glu_grad reads again: a backward call of 512 x 2048 x 512 takes 25.7 us
+// with it and 21.8 without, 8192 x 4096 x 8192 2,010 and 1,870; without it dWg of
+// 512 rows with dh of deviation 1e-6 is 2.7e-2 off in norm, where rounding the
+// outputs alone is 1.2e-3. bf16 has the range of fp32 and needs none of this.
 __global__ __launch_bounds__(1024) void k_glu_top(int act, const uint16_t* dh, int64_t lddh, const float* gu, int rows,
                                                   int inter, uint32_t* top) {
   __shared__ uint32_t red[16];
