@@ -420,6 +420,8 @@ def _rows2d(t, name, dtype, shape=None, dev=None):
     if t.dtype is not dtype:
         raise MoeError(f"{name}: dtype {t.dtype} is not {dtype}")
     rows, cols = t.shape
+    if (rows | cols) >> 31:      # the argument blocks would cut it to 32 bits
+        raise MoeError(f"{name}: shape {(rows, cols)}, needs sizes below 2^31")
     if shape is not None and (rows != shape[0] or cols != shape[1]):
         raise MoeError(f"{name}: shape {(rows, cols)}, needs {tuple(shape)}")
     _on_device(t, name, dev)
