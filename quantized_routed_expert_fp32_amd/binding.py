@@ -461,6 +461,21 @@ def _half(x, name="x"):
     raise MoeError(f"{name}: dtype {x.dtype} is not torch.bfloat16 or torch.float16")
 
 
+def _no_history(fn, instead, names, *operands):
+    """Refuses operands that require a gradient where one would be recorded: the
+    result has no history, and a backward pass would leave them out without a word."""
+    for t in operands:
+        if t is not None and t.requires_grad:
+            break
+    else:
+        return
+    import torch
+    if torch.is_grad_enabled():
+        name = names.split()[[t is not None and t.requires_grad for t in operands].index(True)]
+        raise MoeError(f"{fn}: {name} requires a gradient, which this call does not record: {instead}"
+                       "call it under torch.no_grad()")
+
+
 def _act_code(act):
     if act not in ACTIVATIONS:
         raise MoeError(f"act: {act!r} is not one of {', '.join(ACTIVATIONS)}")
@@ -545,7 +560,10 @@ def glu_workspace_size(x, w_gate, w_up, kind=MOE_GLU_FORWARD, s_gate=None, s_up=
 def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=None, stream=None):
     """moe_glu_forward: h = act(x w_gate^T) * (x w_up^T), [rows, inter] of x's
     dtype (bf16 or fp16); with save=True (h, gu), gu fp32 [rows, 2, inter] being what
-    glu_backward takes."""
+    glu_backward takes. h has no autograd history: without save (or gu), operands
+    that require a gradient are refused where grad mode is on."""
+    if not save and gu is None:
+        _no_history("glu_forward", "take save=True and glu_backward, or ", "x w_gate w_up", x, w_gate, w_up)
     a, dt, dev = _glu_args(x, w_gate, w_up, act)
     ctx = _call_ctx(dev, stream)
     if ctx is None:
@@ -586,7 +604,9 @@ def _gu_ok(gu, R, I, dev):
 def glu_backward(dh, x, w_gate, w_up, gu, act="silu", need_dx=True, need_dw=True, dx=None, dw_gate=None,
                  dw_up=None, ws=None, stream=None):
     """moe_glu_backward: (dx, dw_gate, dw_up) of glu_forward(..., save=True) from
-    dh and its gu; None in the place of a gradient that is not needed."""
+    dh and its gu; None in the place of a gradient that is not needed. Gradients
+    of these gradients are not computed: a dh that requires one is refused."""
+    _no_history("glu_backward", "", "dh", dh)
     a, dt, dev = _glu_args(x, w_gate, w_up, act)
     if not need_dx and not need_dw:
         raise MoeError("glu_backward: neither need_dx nor need_dw")
@@ -632,7 +652,9 @@ def _glu_backward(a, dt, dev, dhp, lddh, gp, need_dx, need_dw, outs, ws, stream)
 def glu_i8(x, w_gate, s_gate, w_up, s_up, act="silu", x_scale=None, out_dtype=None, h=None, ws=None, stream=None):
     """moe_glu_i8: the gated block on int8 weights [inter, hidden] with fp32
     channel scales [inter]; x in bf16/fp16 (quantised a token inside the call),
-    or int8 with x_scale [rows] (then out_dtype is h's type, bf16 by default)."""
+    or int8 with x_scale [rows] (then out_dtype is h's type, bf16 by default). No
+    gradients: operands that require one are refused where grad mode is on."""
+    _no_history("glu_i8", "", "x s_gate s_up x_scale", x, s_gate, s_up, x_scale)
     if s_gate is None or s_up is None:
         raise MoeError("s_gate, s_up: needed with int8 weights")
     a, dt, dev = _glu_args(x, w_gate, w_up, act, s_gate, s_up, x_scale, out_dtype)
@@ -659,7 +681,8 @@ def _glu_i8(a, dt, dev, h, ws, stream):
 
 def quant_rows(x, q=None, scale=None, stream=None):
     """moe_quant_rows: rows of x (bf16, fp16 or fp32) as (int8 [rows, cols],
-    fp32 scale [rows]); of a weight matrix [out, in] the rows are its channels."""
+    fp32 scale [rows]); of a weight matrix [out, in] the rows are its channels.
+    Neither has a gradient (rounding has none)."""
     import torch
     code = MOE_FP32 if x.dtype is torch.float32 else _half(x)
     ldx = _rows2d(x, "x", x.dtype)
@@ -724,7 +747,9 @@ def linear_i8_workspace_size(x, w, s_w, x_scale=None) -> int:
 def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=None, stream=None):
     """moe_linear_i8: y = x w^T (+ bias) for int8 w [out, in] with fp32 channel
     scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
-    int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default)."""
+    int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default). No
+    gradients: operands that require one are refused where grad mode is on."""
+    _no_history("linear_i8", "", "x s_w bias x_scale", x, s_w, bias, x_scale)
     a, dt, dev = _linear_args(x, w, s_w, bias, x_scale, out_dtype)
     ctx = _call_ctx(dev, stream)
     if ctx is None:
