@@ -196,11 +196,12 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // flight by waiting for all of them; it has no register outputs, and reads of
 // what it writes are ordered by step_wait.
 __device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const uint8_t* base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "m0");
 }
 // the same with a whole address per lane (the last step's masked loads)
 __device__ __forceinline__ void dma16_at(uint32_t lds, const uint8_t* src) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "m0");
 }
 // the wave's own loads but the newest N have landed, its LDS reads are done;
 // then every wave's
