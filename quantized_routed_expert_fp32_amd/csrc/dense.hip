@@ -194,7 +194,11 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // 64 x 16 bytes from base + off (a lane's own) to LDS [lds, lds + 1024). In
 // asm, because the compiler would guard every LDS read against the loads in
 // flight by waiting for all of them; it has no register outputs, and reads of
-// what it writes are ordered by step_wait.
+// what it writes are ordered by step_wait. Nor does the compiler look for hazards
+// in here: m0 needs its one wait state, and a base that a vector instruction
+// wrote (a readlane) would need five. The kernels as built compute every base in
+// scalar registers, which a test checks (s_nop 3 in place of s_nop 0 would cover
+// it too, and costs the 512 x 2048 -> 2 x 512 forward 5%, the large ones 1%).
 __device__ __forceinline__ void dma16(uint32_t lds, uint32_t off, const uint8_t* base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "m0");
