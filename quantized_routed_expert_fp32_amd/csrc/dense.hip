@@ -76,21 +76,54 @@ template <> struct Elem<DT_I8> {
 // silu(g) = g s(g); gelu_tanh(g) = g s(w(g)) with w = 2 sqrt(2/pi) (g +
 // 0.044715 g^3), since (1 + tanh(w/2)) / 2 = s(w): one sigmoid for both.
 constexpr float GELU_C = 1.5957691216057308f;
-// v_rcp_f32 is good to one ulp; 1 + e^-w = inf gives 0
-__device__ __forceinline__ float sigmoid_f(float w) { return __builtin_amdgcn_rcpf(1.f + __expf(-w)); }
-__device__ __forceinline__ float act_f(float g, int act) {
-  const float w = act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
-  return g * sigmoid_f(w);
+// v_rcp_f32 and v_exp_f32 are good to one ulp. Below w = FAR the sigmoid is e^w to
+// fp32 and soon subnormal, or its inverse infinite, where g e^w still counts: there
+// t = e^(w / 2) goes in twice, on either side of the rounding. act_n and act_grad_n
+// look once at all of a wave's gates (a minimum a gate; in place of the plain form
+// everywhere it would cost 2048 x 2048 -> 2 x 8192 2%, 8-bit 4%; so, 0 to 2%).
+constexpr float FAR = -80.f;
+__device__ __forceinline__ float act_arg(float g, int act) {
+  return act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
 }
-// value and derivative: p + g p (1 - p) w'; where p (1 - p) is zero the
+__device__ __forceinline__ float act_slope(float g, int act) {
+  return act == ACT_SILU ? 1.f : GELU_C * (1.f + 0.134145f * g * g);
+}
+__device__ __forceinline__ float sigmoid_f(float w) { return __builtin_amdgcn_rcpf(1.f + __expf(-w)); }
+template <int N> __device__ __forceinline__ void act_n(const float* g, int act, float* v) {
+  float low = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float w = act_arg(g[i], act);
+    v[i] = g[i] * sigmoid_f(w);
+    low = __builtin_fminf(low, w);
+  }
+  if (__any(low < FAR))
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = act_arg(g[i], act), t = __expf(0.5f * w);
+      if (w < FAR) v[i] = (g[i] * t) * t;
+    }
+}
+// Values and derivatives: p + g p (1 - p) w'; where p (1 - p) is zero the
 // second term is (w' may overflow there)
-__device__ __forceinline__ void act_grad_f(float g, int act, float* v, float* d) {
-  const float w = act == ACT_SILU ? g : GELU_C * g * (1.f + 0.044715f * g * g);
-  const float dw = act == ACT_SILU ? 1.f : GELU_C * (1.f + 0.134145f * g * g);
-  const float p = sigmoid_f(w);
-  const float pp = p * sigmoid_f(-w);
-  *v = g * p;
-  *d = p + (pp > 0.f ? g * pp * dw : 0.f * pp);
+template <int N> __device__ __forceinline__ void act_grad_n(const float* g, int act, float* v, float* d) {
+  float low = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float w = act_arg(g[i], act), p = sigmoid_f(w), pp = p * sigmoid_f(-w);
+    v[i] = g[i] * p;
+    d[i] = p + (pp > 0.f ? g[i] * pp * act_slope(g[i], act) : 0.f * pp);
+    low = __builtin_fminf(low, w);
+  }
+  if (__any(low < FAR))
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = act_arg(g[i], act), t = __expf(0.5f * w);
+      if (w < FAR) {
+        v[i] = (g[i] * t) * t;
+        d[i] = t > 0.f ? ((1.f + g[i] * act_slope(g[i], act)) * t) * t : 0.f;
+      }
+    }
 }
 
 // ------------------------------------------------------------------ stores
@@ -162,8 +195,10 @@ __device__ __forceinline__ void finish4(const DenseArgs& a, int q, int p, const 
         g[i] = s0[i];
         u[i] = s1[i];
       }
-      v[i] = act_f(g[i], a.act) * u[i];
     }
+    act_n<4>(g, a.act, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= u[i];
     if (a.save) {
       float* sv = static_cast<float*>(a.save) + (int64_t)q * 2 * a.np;
       store4(sv, p, a.np, DT_F32, g);
@@ -694,11 +729,16 @@ struct Dense {
           }
         }
       }
+      if constexpr (GLU) {
+        float v[OG][4];
+        act_n<OG * 4>(&s0[0][0], a.act, &v[0][0]);
+#pragma unroll
+        for (int g = 0; g < OG; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s0[g][e] = v[g][e] * s1[g][e];
+      }
 #pragma unroll
       for (int g = 0; g < OG; ++g) {
-        if constexpr (GLU)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s0[g][e] = act_f(s0[g][e], a.act) * s1[g][e];
         uint8_t* at = buf + col * row_bytes<2, OC>() + (g * 16 + quad * 4) * 2;
         if (a.out_dt == DT_BF16) put4<DT_BF16>(at, s0[g]);
         else put4<DT_F16>(at, s0[g]);
@@ -1117,12 +1157,12 @@ __device__ __forceinline__ void grad8(int act, const uint16_t* dh, const float* 
     unpack16<DT_F32>(here ? load_chunk<4>(g, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, gv + 4 * k);
     unpack16<DT_F32>(here ? load_chunk<4>(g + inter, (i + 4 * k) * 4, inter * 4) : u32x4{0, 0, 0, 0}, uv + 4 * k);
   }
+  float v[8], dv[8];
+  act_grad_n<8>(gv, act, v, dv);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    float v, dv;
-    act_grad_f(gv[k], act, &v, &dv);
-    dg[k] = e[k] * uv[k] * dv;
-    du[k] = e[k] * v;
+    dg[k] = e[k] * uv[k] * dv[k];
+    du[k] = e[k] * v[k];
   }
 }
 
