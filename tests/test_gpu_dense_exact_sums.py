@@ -1,0 +1,119 @@
+"""The dense products on whole numbers, where every sum is exact in fp32 (below
+2^24) in any order, so that the results are compared bit for bit: through every
+tile, with one K range and with several, in every type (tests/dense_tile_sizes.py).
+
+For the gradients g = 32, where the sigmoid is 1 in fp32 (e^-32 < 2^-25) and so
+silu(g) = 32 and silu'(g) = 1 (g p (1 - p) = 4e-13): dg = dh u, du = 32 dh.
+"""
+import pytest
+import torch
+
+import dense_common as D
+import dense_tile_sizes as S
+from gpu_common import binding, log
+from test_gpu_dense import BF, FP, IDS, gen
+
+pytestmark = pytest.mark.gpu
+
+TYPES = pytest.mark.parametrize("dt", [BF, FP], ids=IDS.get)
+
+
+def whole(g, *shape, dt=BF, top=2):
+    return torch.randint(-top, top + 1, shape, generator=g, device="cuda").to(dt)
+
+
+def same(got, want, what):
+    assert torch.isfinite(got).all() and got.any(), what
+    assert torch.equal(got, want), f"{what}: {int((got != want).sum())} of {want.numel()} differ"
+
+
+@TYPES
+@pytest.mark.parametrize("product,tile,several,M,H,I", S.cases("forward"))
+def test_forward(product, tile, several, M, H, I, dt):
+    log(f"case exact forward {M} {H} {I} {dt}")
+    B = binding()
+    g = gen(M + H)
+    x, wg, wu = (whole(g, *s, dt=dt) for s in ((M, H), (I, H), (I, H)))
+    h, gu = B.glu_forward(x, wg, wu, save=True)
+    gg, uu, ag, au = D.products(x, wg, wu)
+    assert max(ag.max().item(), au.max().item()) < 2 ** 24
+    same(gu[:, 0], gg.float(), "g")
+    same(gu[:, 1], uu.float(), "u")
+    want, bound = D.h_bound(gg, uu, torch.zeros_like(gg), torch.zeros_like(uu), "silu", dt)
+    # what rounds to 65504 or beyond in fp16 (infinity from 65520 on; 32 is a step
+    # there) is that or infinite
+    top = want.abs() + bound >= 65504 if dt == FP else torch.zeros_like(want, dtype=torch.bool)
+    assert (~top | (h.abs() >= 65504 - 32 - 2 * bound)).all() and (h[top].sign() == want[top].sign()).all()
+    D.close(torch.where(top, 0, h), torch.where(top, 0.0, want), bound, "h")
+    assert torch.equal(B.glu_forward(x, wg, wu), h)
+
+
+def step(g, M, I, dt):
+    """dh and gu of the gradients' cases, and dg and du in 64 bits."""
+    dh = whole(g, M, I, dt=dt)
+    u = whole(g, M, I).float()
+    gu = torch.stack([torch.full_like(u, 32.0), u], dim=1).contiguous()
+    e = dh.double()
+    return dh, gu, e * u.double(), e * 32
+
+
+@TYPES
+@pytest.mark.parametrize("product,tile,several,M,H,I",
+                         S.cases("dx") + [("dx", None, None, M, H, I) for M in (1, 15, 16, 17, 32, 33)
+                                          for H, I in ((40, 72), (264, 4100))])
+def test_dx(product, tile, several, M, H, I, dt):
+    log(f"case exact dx {M} {H} {I} {dt}")
+    B = binding()
+    g = gen(M + I)
+    x, wg, wu = (whole(g, *s, dt=dt) for s in ((M, H), (I, H), (I, H)))
+    dh, gu, dg, du = step(g, M, I, dt)
+    want = dg @ wg.double() + du @ wu.double()
+    assert (dg.abs() @ wg.double().abs() + du.abs() @ wu.double().abs()).max().item() < 2 ** 24
+    same(B.glu_backward(dh, x, wg, wu, gu, need_dw=False)[0], want.float().to(dt), "dx")
+
+
+@TYPES
+@pytest.mark.parametrize("product,tile,several,M,H,I",
+                         S.cases("dw") + [("dw", None, None, M, H, I) for M in (1, 15, 16, 17, 32, 33, 64, 65)
+                                          for H, I in ((40, 72), (520, 300))])
+def test_dw(product, tile, several, M, H, I, dt):
+    log(f"case exact dw {M} {H} {I} {dt}")
+    B = binding()
+    g = gen(M + I)
+    x, wg, wu = (whole(g, *s, dt=dt) for s in ((M, H), (I, H), (I, H)))
+    dh, gu, dg, du = step(g, M, I, dt)
+    got = B.glu_backward(dh, x, wg, wu, gu, need_dx=False)[1:]
+    for t, d, name in zip(got, (dg, du), ("dw_gate", "dw_up")):
+        assert (d.abs().t() @ x.double().abs()).max().item() < 2 ** 24
+        same(t, (d.t() @ x.double()).float().to(dt), name)
+
+
+@TYPES
+@pytest.mark.parametrize("product,tile,several,M,K,N", S.cases("linear"))
+def test_linear_i8(product, tile, several, M, K, N, dt):
+    log(f"case exact linear_i8 {M} {K} {N} {dt}")
+    B = binding()
+    g = gen(M + K)
+    q, w = (torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8) for s in ((M, K), (N, K)))
+    acc = q.double() @ w.double().t()                # exact
+    a = 1.0 if dt == BF else 2.0 ** -10              # in fp16's range, and a power of two
+    y = B.linear_i8(q, w, torch.ones(N, device="cuda"), x_scale=torch.full((M,), a, device="cuda"), out_dtype=dt)
+    same(y, (acc.float() * a).to(dt), "y")
+
+
+@TYPES
+@pytest.mark.parametrize("product,tile,several,M,H,I", S.cases("glu_i8"))
+def test_glu_i8(product, tile, several, M, H, I, dt):
+    """Gate sums near 127^2, where silu is the identity in fp32."""
+    log(f"case exact glu_i8 {M} {H} {I} {dt}")
+    B = binding()
+    g = gen(M + H)
+    q, wg, wu = (whole(g, *s, dt=torch.int8) for s in ((M, H), (I, H), (I, H)))
+    q[:, H // 2] = 127
+    wg[:, H // 2] = 127
+    gg, uu = q.double() @ wg.double().t(), q.double() @ wu.double().t()
+    assert gg.min() > 100
+    b = 1.0 if dt == BF else 2.0 ** -10
+    one = torch.ones(I, device="cuda")
+    h = B.glu_i8(q, wg, one, wu, one * b, x_scale=torch.ones(M, device="cuda"), out_dtype=dt)
+    same(h, (gg.float() * (uu.float() * b)).to(dt), "h")
