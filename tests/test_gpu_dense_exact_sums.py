@@ -88,6 +88,61 @@ def test_dw(product, tile, several, M, H, I, dt):
         same(t, (d.t() @ x.double()).float().to(dt), name)
 
 
+@pytest.mark.parametrize("M,H,I", [(1 << 20, 8, 8), (1 << 20, 24, 40), (300001, 8, 8), (2596, 1736, 1154), (971, 42, 41),
+                                   (3484, 530, 908), (2378, 773, 639), (64, 40, 8), (40, 64, 72), (32, 72, 8), (17, 8, 8)])
+@TYPES
+def test_dw_counts_every_step_once(M, H, I, dt):
+    """One row of each 64 (a K step, or half of one) contributes one, to one
+    element of each weight gradient: a step left out, or taken twice, is an
+    element that is off by one (32 for the up weight), and the sums are whole
+    numbers that both types hold."""
+    log(f"case dw steps {M} {H} {I} {dt}")
+    B = binding()
+    g = gen(M + H)
+    n = -(-M // 64)
+    row = torch.arange(n, device="cuda") * 64 + torch.randint(0, 64, (n,), generator=g, device="cuda")
+    row[-1] = M - 1                                   # the last row of all
+    row[0] = 0
+    i, c = (torch.randint(0, k, (n,), generator=g, device="cuda") for k in (I, H))
+    sign = whole(g, n, top=1).float()
+    sign[sign == 0] = 1
+    x = whole(g, M, H, dt=dt)
+    x[row] = 0
+    x[row, c] = 1
+    dh = torch.zeros(M, I, device="cuda", dtype=dt)
+    dh[row, i] = sign.to(dt)
+    gu = torch.ones(M, 2, I, device="cuda")
+    gu[:, 0] = 32
+    wg, wu = whole(g, I, H, dt=dt), whole(g, I, H, dt=dt)
+    want = torch.zeros(I, H, device="cuda", dtype=torch.float64)
+    want.index_put_((i, c), sign.double(), accumulate=True)
+    assert want.abs().max() <= 256
+    for k in {0, n // 2, n - 1}:                      # what the comparison would see without step k
+        less = want.clone()
+        less[i[k], c[k]] -= sign[k].double()
+        assert not torch.equal(less.to(dt), want.to(dt)) and not torch.equal((32 * less).to(dt), (32 * want).to(dt))
+    _, dwg, dwu = B.glu_backward(dh, x, wg, wu, gu, need_dx=False)
+    same(dwg, want.to(dt), "dw_gate")
+    same(dwu, (32 * want).to(dt), "dw_up")
+
+
+def test_the_longest_dw_on_whole_numbers():
+    """2^20 rows of whole numbers: sums up to 2^23 (dg) and 2^22 in steps of 32 (du) by eight workgroups' ranges."""
+    B = binding()
+    M = 1 << 20
+    for H, I in ((8, 8), (264, 40)):
+        log(f"case longest dw {H} {I}")
+        g = gen(H)
+        x, wg, wu = (whole(g, *s) for s in ((M, H), (I, H), (I, H)))
+        dh, gu, dg, du = step(g, M, I, BF)
+        got = B.glu_backward(dh, x, wg, wu, gu, need_dx=False)[1:]
+        for t, d in zip(got, (dg, du)):
+            want = d.t() @ x.double()
+            same(t, want.float().to(BF), "dw")
+            # the last K step missing would show
+            assert not torch.equal((want - d[-64:].t() @ x[-64:].double()).float().to(BF), t)
+
+
 @TYPES
 @pytest.mark.parametrize("product,tile,several,M,K,N", S.cases("linear"))
 def test_linear_i8(product, tile, several, M, K, N, dt):
