@@ -11,7 +11,7 @@ import torch
 import dense_common as D
 import dense_tile_sizes as S
 from gpu_common import binding, log
-from test_gpu_dense import BF, FP, IDS, gen
+from test_gpu_dense import BF, FP, IDS, block, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +172,37 @@ def test_glu_i8(product, tile, several, M, H, I, dt):
     one = torch.ones(I, device="cuda")
     h = B.glu_i8(q, wg, one, wu, one * b, x_scale=torch.ones(M, device="cuda"), out_dtype=dt)
     same(h, (gg.float() * (uu.float() * b)).to(dt), "h")
+
+
+@pytest.mark.parametrize("M", [20, 70])
+@TYPES
+def test_gradients_against_differences_along_their_signs(M, dt):
+    """Along the sign of a gradient the loss sum(dh * h) changes by the sum of its
+    absolute values, to which the bounds are small: a central difference in 64
+    bits tells the gradient from one that is 15% off (and from zero)."""
+    B = binding()
+    H, I = 96, 88
+    x, wg, wu, dh = block(M, M, H, I, dt)
+    for act in ("silu", "gelu_tanh"):
+        _, gu = B.glu_forward(x, wg, wu, act=act, save=True)
+        got = B.glu_backward(dh, x, wg, wu, gu, act=act)
+        bounds = D.grads(x, wg, wu, gu, dh, act, dt)
+        args = [t.double() for t in (x, wg, wu)]
+
+        def loss(p):
+            return (dh.double() * D.act(p[0] @ p[1].t(), act) * (p[0] @ p[2].t())).sum().item()
+
+        # what the rounding of the kept g and u moves the gradients by (|act'| <= 1.13, |act''| <= 1.2)
+        gg, uu, ag, au = D.products(x, wg, wu)
+        eg, eu = (H + 16) * D.U * ag, (H + 16) * D.U * au
+        e = dh.double().abs()
+        ddg, ddu = e * (1.13 * eu + (uu.abs() + eu) * 1.2 * eg), e * 1.13 * eg
+        extra = [ddg @ args[1].abs() + ddu @ args[2].abs(), ddg.t() @ args[0].abs(), ddu.t() @ args[0].abs()]
+        for k in range(3):
+            v = got[k].double().sign()
+            eps = 1e-6
+            up, dn = (loss([a + s * eps * v if i == k else a for i, a in enumerate(args)]) for s in (1, -1))
+            diff, mine = (up - dn) / (2 * eps), got[k].double().abs().sum().item()
+            slack = (bounds[k][1] + extra[k]).sum().item() + 1e-6 * abs(diff)
+            log(f"sign direction {act} {k}: difference {diff:.6f}, gradient {mine:.6f}, slack {slack:.4f}")
+            assert slack < 0.15 * mine and abs(diff - mine) <= slack
