@@ -889,8 +889,9 @@ template <int DT> __device__ __forceinline__ float low_part(float v) {
 }
 // Scale of a row whose largest |x| has the bits m, and its codes: q =
 // round-half-even of the exact x / s, |q| <= 127, 0 where s is not positive.
-// The fp32 product with the reciprocal (two roundings: off by at most 127 2^-24
-// = 7.6e-6) decides, four values at a time, unless one of them lies within 2e-5
+// The fp32 product with the reciprocal (off by less than 1.15e-5: 127 2^-24 from
+// the reciprocal's rounding, 2^-18 from a product between 64 and 128) decides,
+// four values at a time, unless one of them lies within 2e-5
 // of a half-integer or the reciprocal overflows (a subnormal scale); then
 // 53-bit quotients do: x - s (n + 1/2) is zero or at least 2^-32 of x, so 53
 // bits tell the two apart. (A wider margin sends whole waves there: with 1e-3 the
