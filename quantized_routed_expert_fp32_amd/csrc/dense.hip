@@ -21,15 +21,18 @@
 // du and the outputs together: 3.1e-3 of their norm in bf16 against 2.4e-3,
 // where rounding the outputs alone is 1.7e-3).
 //
-// What bounds the large products is the card's power: on normal data 16x16
-// matrix instructions alone run 2.02 PFLOP/s bf16 and 4.26 POP/s 8-bit, the
+// What bounds the large products is the card's power, and waits: on normal data
+// 16x16 matrix instructions alone run 2.02 PFLOP/s bf16 and 4.26 POP/s 8-bit, the
 // 32x32 ones 1.75 and 3.55 (zeros: 2.44 and 4.87 both), which is why every
-// product here is 16x16. With the loads into LDS the 8192 x 4096 x 8192
-// training step's three products run at 1.31 to 1.42 PFLOP/s (kernel times
-// 842, 794 and 818 us), 8192 x 4096 -> 8192 8-bit at 2.4 POP/s (229 us);
-// leaving the loads out of the loop would take 17% off, leaving zeros in the
-// operands 30%, at the same cycle count. A library's products of the same
-// shapes take 832, 916 and 1030 us, its 8-bit one runs at 2.1 POP/s.
+// product here is 16x16; in the products the matrix units are busy 55 to 67% of
+// the cycles, on zeros as on normal data, at a clock of 1.9 to 2.0 GHz on the
+// latter. Medians of 23 launches on one card (least in parentheses): the 8192 x
+// 4096 x 8192 training step's three products 931 (890), 877 (838) and 922 (882)
+// us, 1.18 to 1.31 PFLOP/s, 8192 x 4096 -> 8192 8-bit 283 (237) us, 1.95 to 2.32
+// POP/s; on another card, least, 826, 766, 794 and 227. Leaving the loads into
+// LDS out of the loop would take 17% off, leaving zeros in the operands 30%. A
+// library's products of the same shapes take 832, 916 and 1030 us; its largest
+// 8-bit ones run at 2.1 to 2.3 POP/s.
 #include "dense_launch.h"
 
 #include <algorithm>
@@ -1331,7 +1334,9 @@ hipError_t launch_dense(int dt, int epi, int form, int tile, const DenseArgs& a,
 
 // Whether a decode call quantises x in its own launch: where that costs each
 // workgroup little (half of what its threads can hold) and the workgroups run
-// in one round. 1 x 2048 -> 2048: 5.2 us against 3.5 + 2.5 and a launch between;
+// in one round. The rule goes by the time on the GPU, which is what a captured
+// decode step takes; an eager call of two launches takes 15 to 16 us whatever
+// they do, and would gain by one. 1 x 2048 -> 2048: 5.2 us against 3.5 + 2.5 and a launch between;
 // 16 x 2048 -> 2 x 512 (twice the bound): 9.6 us against 7.4 in two launches; 1 x
 // 4096 -> 2 x 8192 (two rounds): 20.9 against 17.3.
 bool dense_decode_quantises(int epi, int rows, int k, int np) {

@@ -285,9 +285,10 @@ int check_linear(const char* fn, const moe_linear* a) {
 // workgroup on a CU and with two, of the join of several ranges and of their
 // partial sums (bytes through memory). The weights are fitted so that the
 // choice agrees with graph replays of 95 products (rows 24..4096, hidden
-// 512..8192, inter 512..8192, every tile with 1 to 4 ranges timed for each):
-// its time is 0.3% above the best timed one on average, 8% at most (1024 x
-// 4096 -> 2048 in 38.2 us against 35.3). One tile for all would cost more: 700 x
+// 512..8192, inter 512..8192, every tile with 1 to 4 ranges timed for each; all
+// 95 are the fit's own, none held back): for 88 of them its time is 0.3% above
+// the best timed one on average, 8% at most (1024 x 4096 -> 2048 in 38.2 us
+// against 35.3); for the other 7 it takes 6 or 8 ranges, which were not timed. One tile for all would cost more: 700 x
 // 4096 -> 2 x 2000 takes 79 us on 256 x 256, 40 on 128 x 128, 33 on it in
 // 256-byte steps, 45 on 64 x 64; 512 x 2048 -> 2 x 512 takes 43, 18, 18 and 12.
 int moe::dense_tile(int epi, int np, int nq, int steps, int* splits) {
