@@ -428,6 +428,9 @@ int moe_glu_forward(const moe_glu* a, void* h, int64_t ldh, float* gu, void* ws,
  *                                                 rows to a high and a low part)
  *   dx = dg Wg + du Wu   [rows, hidden], row stride lddx
  *   dw_gate = dg^T x, dw_up = du^T x   [inter, hidden] contiguous
+ * Up to 32 rows the gradients are as exact as their own rounding; beyond, the
+ * rounding of dg and du makes it 1.4 times that in norm (bf16 2.4e-3 for 1.7e-3),
+ * so a row's dx has other last bits in a batch of 33 than in one of 32.
  * dx may be NULL, or dw_gate and dw_up both (not wanted, not computed).
  * fp16: dg and du beyond 65504 become infinite, as h does; all of them go into
  * the products times one power of two a call, divided out of the sums again, so
