@@ -236,8 +236,8 @@ def _own(st):
         dx, dw = qr.norm_backward(st["dy"], st["x"] if total is None else total, st["w"], rstd, dtotal=st["dtotal"])
         return dict(y=y, total=total, dx=dx, dw=dw)
     if c["kind"] == "balance":
-        losses, counts, lse = qr.balance_forward(st["logits"], st["ids"], mask=st["mask"], save=True)
-        d = qr.balance_backward(st["dloss"], st["logits"], c["k"], counts, lse, mask=st["mask"])
+        losses, counts = qr.balance_forward(st["logits"], st["ids"], mask=st["mask"], save=True)
+        d = qr.balance_backward(st["dloss"], st["logits"], counts, c["k"], mask=st["mask"])
         return dict(losses=losses, counts=counts[:-1], dlogits=d)
     if c["kind"] == "lora":
         return qr.lora_forward(st["x"], st["a"], st["b"], st["ids"], st["scale"], base=st["base"])
