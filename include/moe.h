@@ -382,7 +382,7 @@ int moe_route_failures(void* ws, uint64_t ws_bytes, int clear, uint32_t* count, 
  * one each, and so do two captured graphs that may run at once. Every result
  * depends on its inputs alone: sums have a fixed order, no atomics. */
 
-/* dtype of moe_quant_rows only (beside MOE_BF16 and MOE_FP16) */
+/* dtype of moe_quant_rows, moe_norm and moe_balance_* only (beside MOE_BF16 and MOE_FP16) */
 enum { MOE_FP32 = 16 };
 /* silu(g) = g / (1 + e^-g);
  * gelu_tanh(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
@@ -471,6 +471,139 @@ typedef struct moe_linear {
 int moe_linear_i8_workspace_size(const moe_linear* a, uint64_t* bytes);
 /* y [rows, out], row stride ldy. Errors as moe_glu_forward. */
 int moe_linear_i8(const moe_linear* a, void* y, int64_t ldy, void* ws, uint64_t ws_bytes, void* stream);
+
+/* --------------------------------- operators around the feed-forward block
+ *
+ * What stands before, beside and behind the products above: the norm that makes
+ * their rows (in 16 bits, or 8 with the scales that moe_linear_i8 and moe_glu_i8
+ * take), the balance loss of the router whose ids and logits moe_route gives, and
+ * low-rank adapters beside a shared projection. The conventions of the dense
+ * operators: sizes as there where not said otherwise, any address and row stride
+ * (elements) is read in place, outputs must not overlap inputs or the workspace
+ * except where said, workspaces need no clearing and keep nothing between calls,
+ * one for each call that may overlap another in time, sums in a fixed order. */
+
+/* Root-mean-square norm of rows, the residual's addition before it.
+ *   total = x + residual, fp32, rounded to dtype; without a residual x itself
+ *   rstd  = 1 / sqrt(mean(total^2) + eps)
+ *   w'    = w, or 1 + w with unit_offset
+ *   dtype   MOE_BF16 or MOE_FP16: residual, total, y and the gradients
+ *   x_dtype dtype, or (with a residual) MOE_FP32: what moe_experts_* return
+ *   w_dtype dtype or MOE_FP32; w [hidden] contiguous
+ *   eps     2^-126 .. 1
+ * A row that holds an infinity or NaN gives what the formulas do with it. */
+typedef struct moe_norm {
+  int32_t rows, hidden, dtype, x_dtype, w_dtype, unit_offset;
+  float eps;
+  const void* x;
+  int64_t ldx;
+  const void* residual;   /* or NULL */
+  int64_t ldresidual;
+  const void* w;
+} moe_norm;
+
+/* y = total rstd w', rounded once. total [rows, hidden] (row stride ldtotal) is
+ * given with a residual, and only then; it may be the residual itself, or x of
+ * dtype (same address and stride). rstd [rows] fp32 or NULL: what
+ * moe_norm_backward reads.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESHAPE, MOE_EHIP. */
+int moe_norm_forward(const moe_norm* a, void* total, int64_t ldtotal, void* y, int64_t ldy, float* rstd, void* stream);
+
+/* The same in 8 bits, as moe_quant_rows of v = fp32(total w') would give it, with
+ * rstd (common to the row) in the scale alone: s0 = fp32(max|v| / 127), q =
+ * round-half-even of the exact v / s0, scale[r] = s0 rstd. The codes depend on no
+ * sum. A row of zeros: scale 0, q 0; one with a v that is not finite: scale NaN, q 0.
+ *   q [rows, hidden], row stride ldq (elements behind hidden stay as they are)
+ *   y [rows, hidden] of dtype, the 16-bit result too, or NULL */
+int moe_norm_i8(const moe_norm* a, void* total, int64_t ldtotal, int8_t* q, int64_t ldq, float* scale, void* y,
+                int64_t ldy, void* stream);
+
+/* Workspace bytes of moe_norm_backward with dw (without: 0). */
+int moe_norm_backward_workspace_size(const moe_norm* a, uint64_t* bytes);
+
+/* Gradients from dy [rows, hidden] and rstd; a->x is what the forward call
+ * normalised (its total, or its x), a->residual NULL.
+ *   g = dy w', dx = rstd (g - total rstd^2 mean(g total)) + dtotal   [rows, hidden]
+ *       (dtotal [rows, hidden] or NULL: the gradient that reaches the total
+ *       itself). dx is the gradient of x and of the residual alike.
+ *   dw = sum_r dy total rstd   [hidden] of w_dtype, fp32 sums
+ * dx or dw may be NULL (not wanted). */
+int moe_norm_backward(const moe_norm* a, const float* rstd, const void* dy, int64_t lddy, const void* dtotal,
+                      int64_t lddtotal, void* dx, int64_t lddx, void* dw, void* ws, uint64_t ws_bytes, void* stream);
+
+/* Balance of a router over the n rows that mask keeps (all where it is NULL):
+ *   counts_e = picks of expert e, f_e = counts_e / (n k), p_r = softmax(logits_r)
+ *   losses[0] = experts sum_e f_e mean_r p_re      (1 where the load is even)
+ *   losses[1] = mean_r logsumexp(logits_r)^2
+ * No rows: both 0, and so are the gradients.
+ *   logits [rows, experts] of dtype MOE_BF16, MOE_FP16 or MOE_FP32, row stride
+ *          ldlogits (taps->logits of moe_route: experts + 1). -inf takes an expert
+ *          out; a row of nothing else, or with +inf or NaN, makes the losses NaN,
+ *          as it does the formulas. Rows that do not count are not read.
+ *   ids    [rows, k] int32 contiguous (moe_route's); outside 0..experts-1: no pick
+ *   mask   [rows] bytes, 0 or 1, or NULL
+ *   losses [2] fp32; counts [experts + 1] int32, the last one n
+ * experts 1..1024, k 1..min(experts, 64). */
+int moe_balance_workspace_size(int rows, int experts, uint64_t* bytes);
+int moe_balance_forward(const void* logits, int dtype, int64_t ldlogits, const int32_t* ids, const uint8_t* mask, int rows,
+                        int experts, int k, float* losses, int32_t* counts, void* ws, uint64_t ws_bytes, void* stream);
+
+/* dlogits [rows, experts] of dtype (row stride lddlogits) from dlosses [2] fp32 in
+ * device memory and the forward call's counts, which are constants to it:
+ *   p_re / n (dlosses[0] experts (f_e - sum_j f_j p_rj) + 2 dlosses[1] logsumexp_r)
+ * and zero for rows that do not count. */
+int moe_balance_backward(const float* dlosses, const void* logits, int dtype, int64_t ldlogits, const uint8_t* mask,
+                         int rows, int experts, int k, const int32_t* counts, void* dlogits, int64_t lddlogits,
+                         void* stream);
+
+enum moe_lora_kind { MOE_LORA_FORWARD = 0, MOE_LORA_BACKWARD = 1 };
+
+/* Low-rank adapters of many requests: row r has adapter i = ids[r].
+ *   dtype   MOE_BF16 or MOE_FP16: everything 16-bit below
+ *   x       [rows, in], row stride ldx
+ *   a       [adapters, rank, in], row stride lda, adapter stride stride_a
+ *   b       [adapters, out, rank], likewise ldb, stride_b
+ *   scale   [adapters] fp32
+ *   ids     [rows] int32 in any order; outside 0..adapters-1: no adapter
+ * rank 1..256, adapters 1..1024, adapter strides 0..2^40 elements. An adapter of a
+ * smaller rank stands with zeros behind its own. */
+typedef struct moe_lora {
+  int32_t rows, in, out, rank, adapters, dtype;
+  const void* x;
+  int64_t ldx;
+  const void* a;
+  int64_t lda, stride_a;
+  const void* b;
+  int64_t ldb, stride_b;
+  const float* scale;
+  const int32_t* ids;
+} moe_lora;
+
+int moe_lora_workspace_size(const moe_lora* a, int kind, uint64_t* bytes);
+
+/* t_r = a_i x_r (fp32 sums), y_r = base_r + scale_i b_i t_r, rounded once. base
+ * [rows, out] (the shared projection's result; NULL: zero) may be y itself (same
+ * address and stride). Rows with no adapter get base_r.
+ *   t [rows, rank] fp32 contiguous or NULL: what moe_lora_backward reads (zero for
+ *     rows with no adapter)
+ * t goes into its product as two 16-bit parts, which keep 16 bits of it in bf16 and
+ * 22 in fp16 (of the row's largest, for the small ones); for few rows (one launch
+ * and no workspace) in fp32: a row's last bits may differ between the two.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESHAPE, MOE_ENOSPACE, MOE_EHIP. */
+int moe_lora_forward(const moe_lora* a, const void* base, int64_t ldbase, void* y, int64_t ldy, float* t, void* ws,
+                     uint64_t ws_bytes, void* stream);
+
+/* Gradients from dy [rows, out] and the forward call's t:
+ *   u_r = b_i^T dy_r,  dx_r = dx_base_r + scale_i a_i^T u_r     [rows, in]
+ *     (dx_base [rows, in] or NULL: the gradient through the shared projection; it
+ *     may be dx itself, same address and stride)
+ *   da_i = scale_i sum_r u_r x_r^T  [adapters, rank, in], db_i = scale_i sum_r dy_r
+ *     t_r^T  [adapters, out, rank], contiguous; zero for adapters with no row
+ * dx may be NULL, or da and db both (then t is not read). scale and base have no
+ * gradient here (base's is dy). */
+int moe_lora_backward(const moe_lora* a, const void* dy, int64_t lddy, const float* t, const void* dx_base,
+                      int64_t lddx_base, void* dx, int64_t lddx, void* da, void* db, void* ws, uint64_t ws_bytes,
+                      void* stream);
 
 /* ----------------------------------------------------------- diagnostics */
 const char* moe_status_string(int status);

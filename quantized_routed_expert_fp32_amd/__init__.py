@@ -9,4 +9,7 @@ from .binding import (  # noqa: F401
     experts_decode, experts_grouped, workspace_size,
     glu_forward, glu_backward, glu_i8, quant_rows, linear_i8, glu_workspace_size,
     linear_i8_workspace_size,
+    norm_forward, norm_i8, norm_backward, norm_backward_workspace_size,
+    balance_forward, balance_backward, balance_workspace_size,
+    lora_forward, lora_backward, lora_workspace_size,
 )

@@ -79,15 +79,32 @@ class LinearC(C.Structure):
                 ("x", C.c_void_p), ("ldx", C.c_int64), ("s_x", C.c_void_p)]
 
 
+class NormC(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("hidden", C.c_int32), ("dtype", C.c_int32), ("x_dtype", C.c_int32),
+                ("w_dtype", C.c_int32), ("unit_offset", C.c_int32), ("eps", C.c_float), ("x", C.c_void_p),
+                ("ldx", C.c_int64), ("residual", C.c_void_p), ("ldresidual", C.c_int64), ("w", C.c_void_p)]
+
+
+class LoraC(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("in_", C.c_int32), ("out", C.c_int32), ("rank", C.c_int32),
+                ("adapters", C.c_int32), ("dtype", C.c_int32), ("x", C.c_void_p), ("ldx", C.c_int64),
+                ("a", C.c_void_p), ("lda", C.c_int64), ("stride_a", C.c_int64), ("b", C.c_void_p),
+                ("ldb", C.c_int64), ("stride_b", C.c_int64), ("scale", C.c_void_p), ("ids", C.c_void_p)]
+
+
 EXPORTS = ["moe_pack_size", "moe_pack_layer_host", "moe_layer_bind", "moe_pack_layer",
            "moe_workspace_size", "moe_route", "moe_experts_decode", "moe_experts_grouped",
            "moe_forward_windows", "moe_forward_windows_noalloc", "moe_route_failures",
            "moe_forward_exact", "moe_glu_workspace_size", "moe_glu_forward", "moe_glu_backward", "moe_glu_i8",
-           "moe_quant_rows", "moe_linear_i8_workspace_size", "moe_linear_i8", "moe_status_string", "moe_last_error", "moe_version"]
+           "moe_quant_rows", "moe_linear_i8_workspace_size", "moe_linear_i8",
+           "moe_norm_forward", "moe_norm_i8", "moe_norm_backward_workspace_size", "moe_norm_backward",
+           "moe_balance_workspace_size", "moe_balance_forward", "moe_balance_backward",
+           "moe_lora_workspace_size", "moe_lora_forward", "moe_lora_backward", "moe_status_string", "moe_last_error", "moe_version"]
 
 MOE_WS_DECODE, MOE_WS_GROUPED, MOE_WS_EXACT = 0, 1, 2
 MOE_FP32 = 16
 MOE_GLU_FORWARD, MOE_GLU_BACKWARD, MOE_GLU_I8 = 0, 1, 2
+MOE_LORA_FORWARD, MOE_LORA_BACKWARD = 0, 1
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 _lib = None
@@ -128,8 +145,21 @@ def lib() -> C.CDLL:
     L.moe_quant_rows.argtypes = [vp, i32, i32, i32, i64, vp, i64, vp, vp]
     L.moe_linear_i8_workspace_size.argtypes = [C.POINTER(LinearC), C.POINTER(u64)]
     L.moe_linear_i8.argtypes = [C.POINTER(LinearC), vp, i64, vp, u64, vp]
+    L.moe_norm_forward.argtypes = [C.POINTER(NormC), vp, i64, vp, i64, vp, vp]
+    L.moe_norm_i8.argtypes = [C.POINTER(NormC), vp, i64, vp, i64, vp, vp, i64, vp]
+    L.moe_norm_backward_workspace_size.argtypes = [C.POINTER(NormC), C.POINTER(u64)]
+    L.moe_norm_backward.argtypes = [C.POINTER(NormC), vp, vp, i64, vp, i64, vp, i64, vp, vp, u64, vp]
+    L.moe_balance_workspace_size.argtypes = [i32, i32, C.POINTER(u64)]
+    L.moe_balance_forward.argtypes = [vp, i32, i64, vp, vp, i32, i32, i32, vp, vp, vp, u64, vp]
+    L.moe_balance_backward.argtypes = [vp, vp, i32, i64, vp, i32, i32, i32, vp, vp, i64, vp]
+    L.moe_lora_workspace_size.argtypes = [C.POINTER(LoraC), i32, C.POINTER(u64)]
+    L.moe_lora_forward.argtypes = [C.POINTER(LoraC), vp, i64, vp, i64, vp, vp, u64, vp]
+    L.moe_lora_backward.argtypes = [C.POINTER(LoraC), vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, u64, vp]
     for f in ("moe_glu_workspace_size", "moe_glu_forward", "moe_glu_backward", "moe_glu_i8", "moe_quant_rows",
-              "moe_linear_i8_workspace_size", "moe_linear_i8"):
+              "moe_linear_i8_workspace_size", "moe_linear_i8", "moe_norm_forward", "moe_norm_i8",
+              "moe_norm_backward_workspace_size", "moe_norm_backward", "moe_balance_workspace_size",
+              "moe_balance_forward", "moe_balance_backward", "moe_lora_workspace_size", "moe_lora_forward",
+              "moe_lora_backward"):
         getattr(L, f).restype = C.c_int
     for f in ("moe_pack_size", "moe_pack_layer_host", "moe_layer_bind", "moe_pack_layer",
               "moe_workspace_size", "moe_route", "moe_experts_decode", "moe_experts_grouped",
@@ -770,3 +800,385 @@ def _linear_i8(a, dt, dev, y, ws, stream):
     if st:
         _check(st, "moe_linear_i8")
     return y
+
+
+# ----------------------------------- operators around the feed-forward block
+def _in(dev, stream, fn, *args):
+    """fn(*args) with device `dev` (and the stream, if one is given) current."""
+    ctx = _call_ctx(dev, stream)
+    if ctx is None:
+        return fn(*args)
+    with ctx:
+        return fn(*args)
+
+
+def _like(t, name, dtype, shape, dev):
+    """(tensor, row stride) of an output: the caller's, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev), shape[1]
+    return t, _rows2d(t, name, dtype, shape, dev)
+
+
+def _vector(t, name, n, dtype, dev):
+    """A contiguous output vector: the caller's, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty((n,), dtype=dtype, device=dev)
+    _flat(t, name, n, dtype, dev)
+    return t
+
+
+def _norm_args(x, weight, eps, residual, unit_offset):
+    """(argument block, result dtype, device index) of a norm call."""
+    import torch
+    dt = x.dtype if residual is None else residual.dtype
+    code = _half(x) if residual is None else _half(residual, "residual")
+    ldx = _rows2d(x, "x", torch.float32 if x.dtype is torch.float32 else dt)
+    dev = x.get_device()
+    R, H = x.shape
+    ldr = 0 if residual is None else _rows2d(residual, "residual", dt, (R, H), dev)
+    wt = torch.float32 if weight.dtype is torch.float32 else dt
+    a = NormC(R, H, code, code if x.dtype is dt else MOE_FP32, code if wt is dt else MOE_FP32, int(bool(unit_offset)),
+              eps, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+              _flat(weight, "weight", H, wt, dev))
+    return a, dt, dev
+
+
+def _total(total, residual, R, H, dt, dev):
+    """(tensor, address, row stride) of a call's total; none without a residual."""
+    if residual is None:
+        if total is not None:
+            raise MoeError("total: given without a residual")
+        return None, None, 0
+    total, ld = _like(total, "total", dt, (R, H), dev)
+    return total, total.data_ptr(), ld
+
+
+def norm_forward(x, weight, eps=1e-6, residual=None, unit_offset=False, save=False, total=None, y=None, rstd=None,
+                 stream=None):
+    """moe_norm_forward: (y, total, rstd), total = x + residual and y its root-mean-square
+    norm times weight (1 + weight with unit_offset). x [rows, hidden] of bf16 or fp16,
+    or with a residual of one of them fp32 (what experts() returns); weight of the same
+    type or fp32. total is None without a residual (it may be passed as the residual
+    itself: then it is updated in place), rstd without save (or rstd); total (or x)
+    and rstd are what norm_backward takes. Nothing has autograd history: without
+    save, operands that require a gradient are refused where grad mode is on."""
+    if not save and rstd is None:
+        _no_history("norm_forward", "take save=True and norm_backward, or ", "x weight residual", x, weight, residual)
+    a, dt, dev = _norm_args(x, weight, eps, residual, unit_offset)
+    return _in(dev, stream, _norm_forward, a, dt, dev, residual, save, total, y, rstd, stream)
+
+
+def _norm_forward(a, dt, dev, residual, save, total, y, rstd, stream):
+    import torch
+    R, H = a.rows, a.hidden
+    total, tp, ldt = _total(total, residual, R, H, dt, dev)
+    y, ldy = _like(y, "y", dt, (R, H), dev)
+    if save or rstd is not None:
+        rstd = _vector(rstd, "rstd", R, torch.float32, dev)
+    st = lib().moe_norm_forward(C.byref(a), tp, ldt, y.data_ptr(), ldy, None if rstd is None else rstd.data_ptr(),
+                                _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_norm_forward")
+    return y, total, rstd
+
+
+def norm_i8(x, weight, eps=1e-6, residual=None, unit_offset=False, want_y=False, total=None, q=None, scale=None, y=None,
+            stream=None):
+    """moe_norm_i8: (q, scale, total, y): the norm's result as int8 rows with an fp32
+    scale each, what linear_i8 and glu_i8 take as x and x_scale; y is the 16-bit result
+    too (with want_y or y, else None), total as in norm_forward. No gradients: operands
+    that require one are refused where grad mode is on."""
+    _no_history("norm_i8", "", "x weight residual", x, weight, residual)
+    a, dt, dev = _norm_args(x, weight, eps, residual, unit_offset)
+    return _in(dev, stream, _norm_i8, a, dt, dev, residual, want_y, total, q, scale, y, stream)
+
+
+def _norm_i8(a, dt, dev, residual, want_y, total, q, scale, y, stream):
+    import torch
+    R, H = a.rows, a.hidden
+    total, tp, ldt = _total(total, residual, R, H, dt, dev)
+    q, ldq = _like(q, "q", torch.int8, (R, H), dev)
+    scale = _vector(scale, "scale", R, torch.float32, dev)
+    ldy = 0
+    if want_y or y is not None:
+        y, ldy = _like(y, "y", dt, (R, H), dev)
+    st = lib().moe_norm_i8(C.byref(a), tp, ldt, q.data_ptr(), ldq, scale.data_ptr(), None if y is None else y.data_ptr(),
+                           ldy, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_norm_i8")
+    return q, scale, total, y
+
+
+def norm_backward_workspace_size(x, weight) -> int:
+    """moe_norm_backward_workspace_size of a call on these tensors, in bytes."""
+    return _norm_need(_norm_args(x, weight, 1e-6, None, False)[0])
+
+
+def _norm_need(a):
+    n = C.c_uint64()
+    st = lib().moe_norm_backward_workspace_size(C.byref(a), C.byref(n))
+    if st:
+        _check(st, "moe_norm_backward_workspace_size")
+    return n.value
+
+
+def norm_backward(dy, total, weight, rstd, dtotal=None, unit_offset=False, need_dx=True, need_dw=True, dx=None, dw=None,
+                  ws=None, stream=None):
+    """moe_norm_backward: (dx, dw) of norm_forward(..., save=True) from dy, its rstd and
+    what it normalised (its total, or x where it had no residual). dtotal is the gradient
+    that reaches the total itself; dx is the gradient of x and of the residual alike. None
+    in the place of a gradient that is not needed. Gradients of these gradients are not
+    computed: a dy or dtotal that requires one is refused."""
+    _no_history("norm_backward", "", "dy dtotal", dy, dtotal)
+    if not need_dx and not need_dw:
+        raise MoeError("norm_backward: neither need_dx nor need_dw")
+    if dtotal is not None and not need_dx:
+        raise MoeError("dtotal: given without need_dx, the only gradient that it is part of")
+    a, dt, dev = _norm_args(total, weight, 1e-6, None, unit_offset)
+    import torch
+    R, H = a.rows, a.hidden
+    lddy = _rows2d(dy, "dy", dt, (R, H), dev)
+    up, ldu = (None, 0) if dtotal is None else (dtotal.data_ptr(), _rows2d(dtotal, "dtotal", dt, (R, H), dev))
+    rp = _flat(rstd, "rstd", R, torch.float32, dev)
+    if rp is None:
+        raise MoeError("rstd: needed (norm_forward with save=True returns it)")
+    return _in(dev, stream, _norm_backward, a, dt, dev, rp, dy.data_ptr(), lddy, up, ldu,
+               weight.dtype, need_dx, need_dw, dx, dw, ws, stream)
+
+
+def _norm_backward(a, dt, dev, rp, dyp, lddy, up, ldu, wt, need_dx, need_dw, dx, dw, ws, stream):
+    R, H = a.rows, a.hidden
+    n = _norm_need(a) if need_dw else 0
+    ldx = 0
+    if need_dx:
+        dx, ldx = _like(dx, "dx", dt, (R, H), dev)
+    if need_dw:
+        dw = _vector(dw, "dw", H, wt, dev)
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_norm_backward(C.byref(a), rp, dyp, lddy, up, ldu, dx.data_ptr() if need_dx else None, ldx,
+                                 dw.data_ptr() if need_dw else None, wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_norm_backward")
+    return dx if need_dx else None, dw if need_dw else None
+
+
+def _balance_args(logits, mask):
+    """(dtype code, row stride, mask address, device index) of a balance call."""
+    import torch
+    code = MOE_FP32 if logits.dtype is torch.float32 else _half(logits, "logits")
+    ld = _rows2d(logits, "logits", logits.dtype)
+    dev = logits.get_device()
+    return code, ld, _flat(mask, "mask", logits.shape[0], torch.bool, dev), dev
+
+
+def balance_workspace_size(rows, experts) -> int:
+    """moe_balance_workspace_size, in bytes."""
+    n = C.c_uint64()
+    st = lib().moe_balance_workspace_size(rows, experts, C.byref(n))
+    if st:
+        _check(st, "moe_balance_workspace_size")
+    return n.value
+
+
+def balance_forward(logits, ids, mask=None, save=False, losses=None, counts=None, ws=None, stream=None):
+    """moe_balance_forward: (losses, counts) of a router's logits [rows, experts] (fp32,
+    bf16 or fp16; any row stride, so route's logits beside the shared gate's are
+    logits[:, :experts]) and its picks ids [rows, k] int32, over the rows that mask
+    [rows] (bool) keeps. losses fp32 [2]: the balance loss experts sum f_e mean(p_e) and
+    the z loss mean(logsumexp^2); counts int32 [experts + 1]: picks of each expert, and
+    the rows that count. No autograd history: without save=True (the caller runs
+    balance_backward, which takes counts), logits that require a gradient are refused
+    where grad mode is on."""
+    if not save:
+        _no_history("balance_forward", "take save=True and balance_backward, or ", "logits", logits)
+    import torch
+    code, ld, mp, dev = _balance_args(logits, mask)
+    if _rows2d(ids, "ids", torch.int32, (logits.shape[0], ids.shape[-1]), dev) != ids.shape[1]:
+        raise MoeError("ids: needs contiguous memory")
+    return _in(dev, stream, _balance_forward, logits, code, ld, ids, mp, dev, losses, counts, ws, stream)
+
+
+def _balance_forward(logits, code, ld, ids, mp, dev, losses, counts, ws, stream):
+    import torch
+    (R, E), k = logits.shape, ids.shape[1]
+    n = balance_workspace_size(R, E)
+    losses = _vector(losses, "losses", 2, torch.float32, dev)
+    counts = _vector(counts, "counts", E + 1, torch.int32, dev)
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_balance_forward(logits.data_ptr(), code, ld, ids.data_ptr(), mp, R, E, k, losses.data_ptr(),
+                                   counts.data_ptr(), wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_balance_forward")
+    return losses, counts
+
+
+def balance_backward(dlosses, logits, counts, k, mask=None, dlogits=None, stream=None):
+    """moe_balance_backward: dlogits [rows, experts] of the logits' type, from dlosses
+    fp32 [2] (on the device), the counts of balance_forward and its number of picks k.
+    Gradients of this gradient are not computed: dlosses that require one are refused."""
+    _no_history("balance_backward", "", "dlosses", dlosses)
+    import torch
+    code, ld, mp, dev = _balance_args(logits, mask)
+    if dlosses is None or counts is None:
+        raise MoeError("dlosses, counts: both needed")
+    dp = _flat(dlosses, "dlosses", 2, torch.float32, dev)
+    cp = _flat(counts, "counts", logits.shape[1] + 1, torch.int32, dev)
+    return _in(dev, stream, _balance_backward, dp, logits, code, ld, mp, dev, cp, k, dlogits, stream)
+
+
+def _balance_backward(dp, logits, code, ld, mp, dev, cp, k, dlogits, stream):
+    R, E = logits.shape
+    dlogits, ldd = _like(dlogits, "dlogits", logits.dtype, (R, E), dev)
+    st = lib().moe_balance_backward(dp, logits.data_ptr(), code, ld, mp, R, E, k, cp, dlogits.data_ptr(), ldd,
+                                    _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_balance_backward")
+    return dlogits
+
+
+def _stack3d(t, name, dtype, shape, dev):
+    """Checks a stack of matrices whose rows are contiguous; (row, matrix) strides in elements."""
+    if t.dim() != 3:
+        raise MoeError(f"{name}: {t.dim()}-D tensor, needs 3 dimensions")
+    if t.dtype is not dtype:
+        raise MoeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if any(n >> 31 for n in t.shape):
+        raise MoeError(f"{name}: shape {tuple(t.shape)}, needs sizes below 2^31")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise MoeError(f"{name}: shape {tuple(t.shape)}, needs {tuple(shape)}")
+    _on_device(t, name, dev)
+    s, ld, one = t.stride()
+    n, rows, cols = t.shape
+    if one != 1 and cols > 1:
+        raise MoeError(f"{name}: the elements of a row must be contiguous (strides {(s, ld, one)})")
+    return (ld if rows > 1 else cols), (s if n > 1 else 0)
+
+
+def _lora_args(x, a, b, ids, scale):
+    """(argument block, device index) of an adapter call."""
+    import torch
+    code, dt = _half(x), x.dtype
+    ldx = _rows2d(x, "x", dt)
+    dev = x.get_device()
+    lda, sta = _stack3d(a, "a", dt, None, dev)
+    (n, rank, K), (R, Kx) = a.shape, x.shape
+    if Kx != K:
+        raise MoeError(f"x: rows of {Kx} elements, a has {K} columns")
+    if b.dim() != 3:
+        raise MoeError(f"b: {b.dim()}-D tensor, needs 3 dimensions")
+    N = b.shape[1]
+    ldb, stb = _stack3d(b, "b", dt, (n, N, rank), dev)
+    if ids is None or scale is None:
+        raise MoeError("ids, scale: both needed")
+    c = LoraC(R, K, N, rank, n, code, x.data_ptr(), ldx, a.data_ptr(), lda, sta, b.data_ptr(), ldb, stb,
+              _flat(scale, "scale", n, torch.float32, dev), _flat(ids, "ids", R, torch.int32, dev))
+    return c, dev
+
+
+def _lora_need(c, kind):
+    n = C.c_uint64()
+    st = lib().moe_lora_workspace_size(C.byref(c), kind, C.byref(n))
+    if st:
+        _check(st, "moe_lora_workspace_size")
+    return n.value
+
+
+def lora_workspace_size(x, a, b, ids, scale, kind=MOE_LORA_FORWARD) -> int:
+    """moe_lora_workspace_size of a call on these tensors, in bytes."""
+    return _lora_need(_lora_args(x, a, b, ids, scale)[0], kind)
+
+
+def _lora_t(t, R, rank, dev):
+    import torch
+    if _rows2d(t, "t", torch.float32, (R, rank), dev) != rank:
+        raise MoeError("t: needs contiguous memory")
+    return t.data_ptr()
+
+
+def lora_forward(x, a, b, ids, scale, base=None, save=False, y=None, t=None, ws=None, stream=None):
+    """moe_lora_forward: y = base + scale[i] (x a[i]^T) b[i]^T with i = ids[row], [rows, out]
+    of x's dtype (bf16 or fp16): low-rank adapters a [adapters, rank, in] and b [adapters,
+    out, rank] of many requests beside a shared projection, whose result is base (it may
+    be passed as y: then it is updated in place). ids int32 [rows], outside 0..adapters-1:
+    no adapter; scale fp32 [adapters]. With save=True (or t) (y, t), t fp32 [rows, rank]
+    being what lora_backward takes. No autograd history: without save, operands that
+    require a gradient are refused where grad mode is on; scale's is never computed."""
+    if not save and t is None:
+        _no_history("lora_forward", "take save=True and lora_backward, or ", "x a b scale base", x, a, b, scale, base)
+    else:
+        _no_history("lora_forward", "", "scale", scale)
+    c, dev = _lora_args(x, a, b, ids, scale)
+    return _in(dev, stream, _lora_forward, c, x.dtype, dev, base, save, y, t, ws, stream)
+
+
+def _lora_forward(c, dt, dev, base, save, y, t, ws, stream):
+    import torch
+    R, N = c.rows, c.out
+    n = _lora_need(c, MOE_LORA_FORWARD)
+    bp, ldb = (None, 0) if base is None else (base.data_ptr(), _rows2d(base, "base", dt, (R, N), dev))
+    y, ldy = _like(y, "y", dt, (R, N), dev)
+    tp = None
+    if t is not None:
+        tp = _lora_t(t, R, c.rank, dev)
+    elif save:
+        t = torch.empty((R, c.rank), dtype=torch.float32, device=dev)
+        tp = t.data_ptr()
+    wp, wn, ws = _workspace(n, ws, dev)
+    st = lib().moe_lora_forward(C.byref(c), bp, ldb, y.data_ptr(), ldy, tp, wp, wn, _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_lora_forward")
+    return (y, t) if t is not None else y
+
+
+def lora_backward(dy, x, a, b, ids, scale, t=None, dx_base=None, need_dx=True, need_dw=True, dx=None, da=None, db=None,
+                  ws=None, stream=None):
+    """moe_lora_backward: (dx, da, db) of lora_forward(..., save=True) from dy and its t
+    (not read without need_dw). dx_base [rows, in] is added to dx: the gradient through the
+    shared projection (it may be passed as dx: then it is updated in place). The
+    gradient of base is dy itself. None in the place of a gradient that is not needed.
+    Gradients of these gradients are not computed: a dy or dx_base that requires one
+    is refused."""
+    _no_history("lora_backward", "", "dy dx_base", dy, dx_base)
+    if not need_dx and not need_dw:
+        raise MoeError("lora_backward: neither need_dx nor need_dw")
+    if dx_base is not None and not need_dx:
+        raise MoeError("dx_base: given without need_dx")
+    c, dev = _lora_args(x, a, b, ids, scale)
+    lddy = _rows2d(dy, "dy", x.dtype, (c.rows, c.out), dev)
+    if need_dw and t is None:
+        raise MoeError("t: needed for da and db (lora_forward with save=True returns it)")
+    tp = _lora_t(t, c.rows, c.rank, dev) if need_dw else None
+    return _in(dev, stream, _lora_backward, c, x.dtype, dev, dy.data_ptr(), lddy, tp, dx_base, need_dx, need_dw, dx, da,
+               db, ws, stream)
+
+
+def _lora_backward(c, dt, dev, dyp, lddy, tp, dx_base, need_dx, need_dw, dx, da, db, ws, stream):
+    import torch
+    R, K, N, n, rank = c.rows, c.in_, c.out, c.adapters, c.rank
+    need = _lora_need(c, MOE_LORA_BACKWARD)
+    bp, ldbase = (None, 0) if dx_base is None else (dx_base.data_ptr(), _rows2d(dx_base, "dx_base", dt, (R, K), dev))
+    ldx = 0
+    if need_dx:
+        dx, ldx = _like(dx, "dx", dt, (R, K), dev)
+    if need_dw:
+        da = _stack_out(da, "da", dt, (n, rank, K), dev)
+        db = _stack_out(db, "db", dt, (n, N, rank), dev)
+    wp, wn, ws = _workspace(need, ws, dev)
+    st = lib().moe_lora_backward(C.byref(c), dyp, lddy, tp, bp, ldbase, dx.data_ptr() if need_dx else None, ldx,
+                                 da.data_ptr() if need_dw else None, db.data_ptr() if need_dw else None, wp, wn,
+                                 _raw_stream(dev, stream))
+    if st:
+        _check(st, "moe_lora_backward")
+    return (dx if need_dx else None), (da if need_dw else None), (db if need_dw else None)
+
+
+def _stack_out(t, name, dtype, shape, dev):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _stack3d(t, name, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise MoeError(f"{name}: needs contiguous memory")
+    return t

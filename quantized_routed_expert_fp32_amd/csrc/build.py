@@ -20,8 +20,9 @@ CEIL_OUT = os.path.join(PKG, "libmoe_ceilings.so")   # bench.py's MFMA ceiling p
 BUILD = os.path.join(PKG, "_build")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
-HIP_SOURCES = ["route.hip", "decode.hip", "grouped.hip", "noalloc.hip", "dense.hip"]
-CXX_SOURCES = ["pack.cpp", "api.cpp", "dense_api.cpp"]
+HIP_SOURCES = ["route.hip", "decode.hip", "grouped.hip", "noalloc.hip", "dense.hip", "norm.hip", "balance.hip",
+               "lora.hip"]
+CXX_SOURCES = ["pack.cpp", "api.cpp", "dense_api.cpp", "block_api.cpp"]
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-ffp-contract=off",
                "-munsafe-fp-atomics", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                "-Wno-unused-result"]

@@ -5,7 +5,7 @@
 // the host tests exercise all host code paths without a GPU or GPU code.
 #include <hip/hip_runtime.h>
 
-#include "dense_launch.h"
+#include "block_launch.h"
 #include "moe_host.h"
 #include "moe_launch.h"
 
@@ -30,6 +30,19 @@ hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, i
                            const DensePairs&, float*, hipStream_t) {
   return hipErrorNoDevice;
 }
+
+hipError_t launch_norm(int, const NormArgs&, hipStream_t) { return hipErrorNoDevice; }
+int norm_grad_parts(int rows, int) { return rows < 512 ? rows : 512; }
+hipError_t launch_norm_grad(int, const NormGradArgs&, hipStream_t) { return hipErrorNoDevice; }
+int64_t balance_part_words(int rows, int experts) { return (rows < 256 ? rows : 256) * (2 * (int64_t)experts + 4); }
+hipError_t launch_balance(int, const BalanceArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_balance_grad(int, const BalanceArgs&, hipStream_t) { return hipErrorNoDevice; }
+bool lora_by_row(int rows, int, int, int) { return rows <= 16; }
+hipError_t launch_lora_sort(const LoraSort&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_lora_shrink(int, bool, int, const LoraShrink&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_lora_expand(int, bool, const LoraExpand&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_lora_grad(int, const LoraGrad&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_lora_row(int, const LoraRow&, hipStream_t) { return hipErrorNoDevice; }
 
 }  // namespace moe
 

@@ -1,0 +1,373 @@
+// Root-mean-square norm of rows with the residual's addition before it:
+//   total = x + residual                      (fp32, rounded to the result's type)
+//   y = total rstd w,  rstd = 1 / sqrt(mean(total^2) + eps)
+// or in 8 bits: v = total w in fp32, s0 = fp32(max|v| / 127), the codes of v / s0 and
+// the scale s0 rstd. rstd is common to a row and leaves the codes alone, so they
+// depend on no sum's order. And its gradients
+//   g = dy w,  dx = rstd (g - total rstd^2 mean(g total)) + dtotal,  dw = sum_r dy total rstd.
+//
+// A row is held in registers (its total, 16 bits an element) between the sum and
+// the result: one pass over memory, which bounds the long calls; the short ones
+// are bound by the launch and the row's own latency.
+#include "block_launch.h"
+#include "dense_rows.h"
+
+namespace moe {
+
+// ------------------------------------------------------------------- sums
+// over the TPR threads that hold a row: a wave, or the whole workgroup
+template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  if constexpr (TPR > 64) {
+    __syncthreads();                 // the last sum's readers are done
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) v += red[i];
+  }
+  return v;
+}
+template <int TPR> __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) m = max(m, red[i]);
+  }
+  return m;
+}
+
+// ------------------------------------------------------------------ chunks
+// A chunk is 8 elements. From 16-bit rows, or from fp32 ones (two loads).
+template <int T> __device__ __forceinline__ void load8(const void* row, int c, int cols, float* f) {
+  if constexpr (T == DT_F32) {
+    unpack16<DT_F32>(load_chunk<4, true>(row, (int64_t)c * 32, (int64_t)cols * 4), f);
+    if (c * 8 + 4 < cols) {
+      unpack16<DT_F32>(load_chunk<4, true>(row, (int64_t)c * 32 + 16, (int64_t)cols * 4), f + 4);
+    } else {
+#pragma unroll
+      for (int i = 4; i < 8; ++i) f[i] = 0.f;
+    }
+  } else {
+    unpack16<T>(load_chunk<2, true>(row, (int64_t)c * 16, (int64_t)cols * 2), f);
+  }
+}
+// the weights of chunk c, as the products take them
+template <int DT> __device__ __forceinline__ void weights8(const void* w, int w_dt, float add, int c, int cols, float* f) {
+  if (w_dt == DT_F32) load8<DT_F32>(w, c, cols, f);
+  else load8<DT>(w, c, cols, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] += add;      // no change where add is 0
+}
+__device__ __forceinline__ void store_chunk(void* row, int c, int cols, u32x4 v) {
+  uint16_t* o = static_cast<uint16_t*>(row) + c * 8;
+  if (c * 8 + 8 <= cols) __builtin_memcpy(o, &v, 16);      // at any alignment
+  else
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c * 8 + i < cols) o[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+}
+
+// 1 / sqrt(mean + eps) of a row whose elements are held as NC chunks a thread.
+// bf16 has the range of fp32, so the squares of a finite row may not: such a row is
+// taken times 2^-80 (the mean is then below 2^96, and eps below its rounding).
+template <int DT, int TPR, int NC>
+__device__ __forceinline__ float row_rstd(const u32x4* held, int cols, float eps, float* red) {
+  float ss = 0.f;
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    float f[8];
+    unpack16<DT>(held[h], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
+  }
+  ss = row_sum<TPR>(ss, red);
+  if constexpr (DT == DT_BF16) {
+    if (ss == __builtin_inff()) {               // the same for the whole row
+      const float down = __builtin_ldexpf(1.f, -80);
+      ss = 0.f;
+#pragma unroll
+      for (int h = 0; h < NC; ++h) {
+        float f[8];
+        unpack16<DT>(held[h], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += (f[i] * down) * (f[i] * down);
+      }
+      ss = row_sum<TPR>(ss, red);
+      return down / __builtin_sqrtf(ss / (float)cols);
+    }
+  }
+  return 1.f / __builtin_sqrtf(ss / (float)cols + eps);
+}
+
+// ---------------------------------------------------------------- the norm
+// TPR threads a row, NC chunks a thread: a wave a row where there are many, or
+// the workgroup for one.
+template <int DT, int XT, bool I8, int TPR, int NC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm(NormArgs a) {
+  constexpr int WG = TPR < 256 ? 256 : TPR;
+  __shared__ float red[TPR / 64];
+  __shared__ uint32_t redm[TPR / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t r = (int64_t)blockIdx.x * (WG / TPR) + threadIdx.x / TPR;
+  if (TPR < 256 && r >= a.rows) return;         // whole waves
+  const int chunks = (a.hidden + 7) / 8;
+  const char* xr = static_cast<const char*>(a.x) + r * a.ldx * (XT == DT_F32 ? 4 : 2);
+  const char* rr = static_cast<const char*>(a.res) + r * a.ldres * 2;
+  char* tr = static_cast<char*>(a.total) + r * a.ldtotal * 2;
+  u32x4 held[NC];
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    const int c = h * TPR + t;
+    held[h] = u32x4{0, 0, 0, 0};
+    if (c >= chunks) continue;
+    if (XT != DT_F32 && !a.res) {
+      held[h] = load_chunk<2, true>(xr, (int64_t)c * 16, (int64_t)a.hidden * 2);
+      continue;
+    }
+    float f[8], g[8];
+    load8<XT>(xr, c, a.hidden, f);
+    load8<DT>(rr, c, a.hidden, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += g[i];
+    held[h] = pack16<DT>(f);
+  }
+  if (a.res)
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c < chunks) store_chunk(tr, c, a.hidden, held[h]);
+    }
+  const float rstd = row_rstd<DT, TPR, NC>(held, a.hidden, a.eps, red);
+  if (a.rstd && t == 0) a.rstd[r] = rstd;
+  if constexpr (!I8) {
+    char* yr = static_cast<char*>(a.y) + r * a.ldy * 2;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+      float f[8], w[8];
+      unpack16<DT>(held[h], f);
+      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
+      store_chunk(yr, c, a.hidden, pack16<DT>(f));
+    }
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+      float f[8], w[8];
+      unpack16<DT>(held[h], f);
+      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c * 8 + i < a.hidden ? f[i] * w[i] : 0.f;
+      m = top_bits<DT_F32, 8>(f, m);
+    }
+    m = row_max<TPR>(m, redm);
+    const RowScale rs(m);
+    if (t == 0) a.scale[r] = rs.s * rstd;
+    int8_t* qr = a.q + r * a.ldq;
+    char* yr = static_cast<char*>(a.y) + r * a.ldy * 2;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+      float f[8], w[8];
+      unpack16<DT>(held[h], f);
+      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+      if (a.y) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = f[i] * rstd * w[i];
+        store_chunk(yr, c, a.hidden, pack16<DT>(y));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= w[i];
+      const uint32_t o[2] = {rs.codes4(f), rs.codes4(f + 4)};
+      if (c * 8 + 8 <= a.hidden) __builtin_memcpy(qr + c * 8, o, 8);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c * 8 + i < a.hidden) qr[c * 8 + i] = (int8_t)(o[i / 4] >> (8 * (i & 3)));
+    }
+  }
+}
+
+// ------------------------------------------------------------- its gradients
+// Workgroup b takes rows [b, b + 1) rows / gridDim, a wave (or the workgroup) a
+// row at a time; each thread sums dw of its own columns over its rows in fp32
+// registers, the waves' sums join through LDS, and k_norm_dw adds the workgroups'
+// in order.
+template <int DT, int TPR, int NC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_grad(NormGradArgs a) {
+  constexpr int WG = TPR < 256 ? 256 : TPR, RPW = WG / TPR;
+  __shared__ float red[TPR / 64];
+  __shared__ float cols[RPW > 1 ? NC * TPR * 8 : 1];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int chunks = (a.hidden + 7) / 8;
+  const int64_t r0 = (int64_t)a.rows * blockIdx.x / gridDim.x, r1 = (int64_t)a.rows * (blockIdx.x + 1) / gridDim.x;
+  float dw[NC][8] = {};
+  for (int64_t r = r0 + sub; r < r1; r += RPW) {
+    const char* xr = static_cast<const char*>(a.x) + r * a.ldx * 2;
+    const char* er = static_cast<const char*>(a.dy) + r * a.lddy * 2;
+    u32x4 xs[NC], es[NC];
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      xs[h] = es[h] = u32x4{0, 0, 0, 0};
+      if (c >= chunks) continue;
+      xs[h] = load_chunk<2, true>(xr, (int64_t)c * 16, (int64_t)a.hidden * 2);
+      es[h] = load_chunk<2, true>(er, (int64_t)c * 16, (int64_t)a.hidden * 2);
+    }
+    const float rstd = a.rstd[r];
+    float dot = 0.f;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+      float x[8], e[8], w[8];
+      unpack16<DT>(xs[h], x);
+      unpack16<DT>(es[h], e);
+      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = x[i] * rstd;
+        dot += e[i] * w[i] * n;
+        dw[h][i] += e[i] * n;
+      }
+    }
+    if (!a.dx) continue;
+    dot = row_sum<TPR>(dot, red) / (float)a.hidden;
+    const char* ur = static_cast<const char*>(a.dtotal) + r * a.lddtotal * 2;
+    char* dr = static_cast<char*>(a.dx) + r * a.lddx * 2;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+      float x[8], e[8], w[8], u[8] = {};
+      unpack16<DT>(xs[h], x);
+      unpack16<DT>(es[h], e);
+      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+      if (a.dtotal) load8<DT>(ur, c, a.hidden, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = rstd * (e[i] * w[i] - x[i] * rstd * dot) + u[i];
+      store_chunk(dr, c, a.hidden, pack16<DT>(e));
+    }
+  }
+  if (!a.dw) return;
+  float* part = a.part + (int64_t)blockIdx.x * a.hidden;
+  if constexpr (RPW > 1) {
+    // one wave's sums after the other's, in their order
+#pragma unroll 1
+    for (int s = 0; s < RPW; ++s) {
+      if (sub == s)
+#pragma unroll
+        for (int h = 0; h < NC; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float* at = cols + ((h * 8 + i) * TPR + t);
+            *at = s ? *at + dw[h][i] : dw[h][i];
+          }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.hidden; c += WG) {
+      const int ch = c / 8;
+      part[c] = cols[(ch / TPR * 8 + c % 8) * TPR + ch % TPR];
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < NC; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (h * TPR + t) * 8 + i;
+        if (c < a.hidden) part[c] = dw[h][i];
+      }
+  }
+}
+
+// dw[c]: the workgroups' sums, 32 columns a workgroup, each in 8 stretches joined in order
+template <int DT> __global__ __launch_bounds__(256) void k_norm_dw(NormGradArgs a, int parts) {
+  __shared__ float red[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
+  float v = 0.f;
+  if (c < a.hidden)
+    for (int p = parts * s / 8; p < parts * (s + 1) / 8; ++p) v += a.part[(int64_t)p * a.hidden + c];
+  red[s][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (s || c >= a.hidden) return;
+  for (int i = 1; i < 8; ++i) v += red[i][threadIdx.x & 31];
+  if (a.w_dt == DT_F32) static_cast<float*>(a.dw)[c] = v;
+  else static_cast<uint16_t*>(a.dw)[c] = to16<DT>(v);
+}
+
+// --------------------------------------------------------------- launchers
+template <int DT, int XT, bool I8, int TPR, int NC> static hipError_t norm_run(const NormArgs& a, hipStream_t s) {
+  constexpr int WG = TPR < 256 ? 256 : TPR, RPW = WG / TPR;
+  hipLaunchKernelGGL((k_norm<DT, XT, I8, TPR, NC>), dim3((a.rows + RPW - 1) / RPW), dim3(WG), 0, s, a);
+  return hipGetLastError();
+}
+// Threads of a row and chunks of a thread, the first that hold it: a wave a row
+// needs no barrier and takes the calls of many rows; few rows go over more threads.
+template <int DT, int XT, bool I8> static hipError_t norm_pick(const NormArgs& a, hipStream_t s) {
+  const int chunks = (a.hidden + 7) / 8;
+  if (a.rows > 1024 || chunks <= 64) {
+    if (chunks <= 64) return norm_run<DT, XT, I8, 64, 1>(a, s);
+    if (chunks <= 128) return norm_run<DT, XT, I8, 64, 2>(a, s);
+    if (chunks <= 256) return norm_run<DT, XT, I8, 64, 4>(a, s);
+    if (chunks <= 512) return norm_run<DT, XT, I8, 64, 8>(a, s);
+  }
+  if (chunks <= 256) return norm_run<DT, XT, I8, 256, 1>(a, s);
+  if (chunks <= 1024) return norm_run<DT, XT, I8, 1024, 1>(a, s);
+  if (chunks <= 2048) return norm_run<DT, XT, I8, 1024, 2>(a, s);
+  if (chunks <= 8192) return norm_run<DT, XT, I8, 1024, 8>(a, s);
+  return hipErrorInvalidValue;
+}
+template <int DT> static hipError_t norm_dt(const NormArgs& a, hipStream_t s) {
+  if (a.x_dt == DT_F32) return a.q ? norm_pick<DT, DT_F32, true>(a, s) : norm_pick<DT, DT_F32, false>(a, s);
+  return a.q ? norm_pick<DT, DT, true>(a, s) : norm_pick<DT, DT, false>(a, s);
+}
+hipError_t launch_norm(int dt, const NormArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) return norm_dt<DT_BF16>(a, s);
+  if (dt == DT_F16) return norm_dt<DT_F16>(a, s);
+  return hipErrorInvalidValue;
+}
+
+// Workgroups of the gradients: at most 512 (two a CU), at least 4 rows for each
+int norm_grad_parts(int rows, int hidden) {
+  const int per = hidden <= 4096 ? 4 : 1;
+  return (rows + per - 1) / per < 512 ? (rows + per - 1) / per : 512;
+}
+template <int DT, int TPR, int NC> static hipError_t grad_run(const NormGradArgs& a, hipStream_t s) {
+  const int parts = norm_grad_parts(a.rows, a.hidden);
+  hipLaunchKernelGGL((k_norm_grad<DT, TPR, NC>), dim3(parts), dim3(TPR < 256 ? 256 : TPR), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.dw) return e;
+  hipLaunchKernelGGL((k_norm_dw<DT>), dim3((a.hidden + 31) / 32), dim3(256), 0, s, a, parts);
+  return hipGetLastError();
+}
+template <int DT> static hipError_t grad_pick(const NormGradArgs& a, hipStream_t s) {
+  const int chunks = (a.hidden + 7) / 8;
+  if (chunks <= 64) return grad_run<DT, 64, 1>(a, s);
+  if (chunks <= 128) return grad_run<DT, 64, 2>(a, s);
+  if (chunks <= 256) return grad_run<DT, 64, 4>(a, s);
+  if (chunks <= 512) return grad_run<DT, 64, 8>(a, s);
+  if (chunks <= 2048) return grad_run<DT, 512, 4>(a, s);
+  if (chunks <= 4096) return grad_run<DT, 1024, 4>(a, s);
+  if (chunks <= 8192) return grad_run<DT, 1024, 8>(a, s);
+  return hipErrorInvalidValue;
+}
+hipError_t launch_norm_grad(int dt, const NormGradArgs& a, hipStream_t s) {
+  if (dt == DT_BF16) return grad_pick<DT_BF16>(a, s);
+  if (dt == DT_F16) return grad_pick<DT_F16>(a, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe
