@@ -244,7 +244,7 @@ int moe_norm_backward_workspace_size(const moe_norm* a, uint64_t* bytes) {
   if (!bytes) return bad(std::string(fn) + ": NULL bytes");
   const int st = check_norm(fn, a);
   if (st) return st;
-  *bytes = align256((uint64_t)norm_grad_parts(a->rows, a->hidden) * a->hidden * 4);
+  *bytes = align256((uint64_t)norm_grad_words(a->rows, a->hidden) * 4);
   return MOE_OK;
 }
 
@@ -260,7 +260,7 @@ int moe_norm_backward(const moe_norm* a, const float* rstd, const void* dy, int6
   if ((st = check_ld(fn, "lddy", lddy, a->hidden)) || (dtotal && (st = check_ld(fn, "lddtotal", lddtotal, a->hidden))) ||
       (dx && (st = check_ld(fn, "lddx", lddx, a->hidden))))
     return st;
-  const uint64_t need = dw ? align256((uint64_t)norm_grad_parts(a->rows, a->hidden) * a->hidden * 4) : 0;
+  const uint64_t need = dw ? align256((uint64_t)norm_grad_words(a->rows, a->hidden) * 4) : 0;
   if ((st = check_ws(fn, ws, ws_bytes, need))) return st;
   NormGradArgs g{};
   g.rows = a->rows;

@@ -34,10 +34,10 @@ struct NormGradArgs {
   const void* dtotal;               // or null
   void* dx;                         // or null
   void* dw;                         // or null, of w_dt
-  float* part;                      // [norm_grad_parts, hidden] sums of dw
+  float* part;                      // norm_grad_words(rows, hidden): the workgroups' sums of dw
   int64_t ldx, lddy, lddtotal, lddx;
 };
-int norm_grad_parts(int rows, int hidden);
+int64_t norm_grad_words(int rows, int hidden);
 hipError_t launch_norm_grad(int dt, const NormGradArgs& a, hipStream_t s);
 
 // --------------------------------------------------------------- balance

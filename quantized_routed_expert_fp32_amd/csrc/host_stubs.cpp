@@ -32,7 +32,7 @@ hipError_t launch_glu_grad(int, bool, int, const void*, int64_t, const float*, i
 }
 
 hipError_t launch_norm(int, const NormArgs&, hipStream_t) { return hipErrorNoDevice; }
-int norm_grad_parts(int rows, int) { return rows < 512 ? rows : 512; }
+int64_t norm_grad_words(int rows, int hidden) { return (rows < 512 ? rows : 512) * (int64_t)hidden; }
 hipError_t launch_norm_grad(int, const NormGradArgs&, hipStream_t) { return hipErrorNoDevice; }
 int64_t balance_part_words(int rows, int experts) { return (rows < 256 ? rows : 256) * (2 * (int64_t)experts + 4); }
 hipError_t launch_balance(int, const BalanceArgs&, hipStream_t) { return hipErrorNoDevice; }

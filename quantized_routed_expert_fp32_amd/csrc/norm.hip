@@ -14,6 +14,9 @@
 
 namespace moe {
 
+// a workgroup's sums of dw: whole chunks
+static __host__ __device__ int64_t part_ld(int hidden) { return (int64_t)(hidden + 7) / 8 * 8; }
+
 // ------------------------------------------------------------------- sums
 // over the TPR threads that hold a row: a wave, or the whole workgroup
 template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red) {
@@ -202,110 +205,117 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm(NormArgs a) {
 }
 
 // ------------------------------------------------------------- its gradients
-// Workgroup b takes rows [b, b + 1) rows / gridDim, a wave (or the workgroup) a
-// row at a time; each thread sums dw of its own columns over its rows in fp32
-// registers, the waves' sums join through LDS, and k_norm_dw adds the workgroups'
-// in order.
-template <int DT, int TPR, int NC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_grad(NormGradArgs a) {
-  constexpr int WG = TPR < 256 ? 256 : TPR, RPW = WG / TPR;
+// Workgroup b takes rows [b, b + 1) rows / gridDim one at a time, a chunk (NC, beyond
+// 8192 columns) a thread; the next row's loads are in flight while a row is reduced
+// and written. Each thread holds its columns' weights, and sums their dw over its
+// rows in fp32; k_norm_dw adds the workgroups' sums in order.
+template <int DT, int TPR, int NC> __global__ __launch_bounds__(TPR) void k_norm_grad(NormGradArgs a) {
   __shared__ float red[TPR / 64];
-  __shared__ float cols[RPW > 1 ? NC * TPR * 8 : 1];
-  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int t = threadIdx.x;
   const int chunks = (a.hidden + 7) / 8;
   const int64_t r0 = (int64_t)a.rows * blockIdx.x / gridDim.x, r1 = (int64_t)a.rows * (blockIdx.x + 1) / gridDim.x;
-  float dw[NC][8] = {};
-  for (int64_t r = r0 + sub; r < r1; r += RPW) {
+  float dw[NC][8] = {}, w[NC][8];
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    const int c = h * TPR + t;
+    if (c < chunks) weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w[h]);
+  }
+  u32x4 xs[NC], es[NC], us[NC];
+  float rstd = 0.f;
+  auto load = [&](int64_t r) {
     const char* xr = static_cast<const char*>(a.x) + r * a.ldx * 2;
     const char* er = static_cast<const char*>(a.dy) + r * a.lddy * 2;
-    u32x4 xs[NC], es[NC];
+    const char* ur = static_cast<const char*>(a.dtotal) + r * a.lddtotal * 2;
+    const int64_t end = (int64_t)a.hidden * 2;
 #pragma unroll
     for (int h = 0; h < NC; ++h) {
       const int c = h * TPR + t;
-      xs[h] = es[h] = u32x4{0, 0, 0, 0};
+      xs[h] = es[h] = us[h] = u32x4{0, 0, 0, 0};
       if (c >= chunks) continue;
-      xs[h] = load_chunk<2, true>(xr, (int64_t)c * 16, (int64_t)a.hidden * 2);
-      es[h] = load_chunk<2, true>(er, (int64_t)c * 16, (int64_t)a.hidden * 2);
+      xs[h] = load_chunk<2, true>(xr, (int64_t)c * 16, end);
+      es[h] = load_chunk<2, true>(er, (int64_t)c * 16, end);
+      if (a.dtotal) us[h] = load_chunk<2, true>(ur, (int64_t)c * 16, end);
     }
-    const float rstd = a.rstd[r];
+    rstd = a.rstd[r];
+  };
+  if (r0 < r1) load(r0);
+  for (int64_t r = r0; r < r1; ++r) {
+    u32x4 xv[NC], ev[NC], uv[NC];
+    const float rs = rstd;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      xv[h] = xs[h];
+      ev[h] = es[h];
+      uv[h] = us[h];
+    }
+    if (r + 1 < r1) load(r + 1);
     float dot = 0.f;
 #pragma unroll
     for (int h = 0; h < NC; ++h) {
-      const int c = h * TPR + t;
-      if (c >= chunks) continue;
-      float x[8], e[8], w[8];
-      unpack16<DT>(xs[h], x);
-      unpack16<DT>(es[h], e);
-      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
+      if (h * TPR + t >= chunks) continue;
+      float x[8], e[8];
+      unpack16<DT>(xv[h], x);
+      unpack16<DT>(ev[h], e);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float n = x[i] * rstd;
-        dot += e[i] * w[i] * n;
+        const float n = x[i] * rs;
+        dot += e[i] * w[h][i] * n;
         dw[h][i] += e[i] * n;
       }
     }
     if (!a.dx) continue;
     dot = row_sum<TPR>(dot, red) / (float)a.hidden;
-    const char* ur = static_cast<const char*>(a.dtotal) + r * a.lddtotal * 2;
     char* dr = static_cast<char*>(a.dx) + r * a.lddx * 2;
 #pragma unroll
     for (int h = 0; h < NC; ++h) {
       const int c = h * TPR + t;
       if (c >= chunks) continue;
-      float x[8], e[8], w[8], u[8] = {};
-      unpack16<DT>(xs[h], x);
-      unpack16<DT>(es[h], e);
-      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
-      if (a.dtotal) load8<DT>(ur, c, a.hidden, u);
+      float x[8], e[8], u[8];
+      unpack16<DT>(xv[h], x);
+      unpack16<DT>(ev[h], e);
+      unpack16<DT>(uv[h], u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = rstd * (e[i] * w[i] - x[i] * rstd * dot) + u[i];
+      for (int i = 0; i < 8; ++i) e[i] = rs * (e[i] * w[h][i] - x[i] * rs * dot) + u[i];
       store_chunk(dr, c, a.hidden, pack16<DT>(e));
     }
   }
   if (!a.dw) return;
-  float* part = a.part + (int64_t)blockIdx.x * a.hidden;
-  if constexpr (RPW > 1) {
-    // one wave's sums after the other's, in their order
-#pragma unroll 1
-    for (int s = 0; s < RPW; ++s) {
-      if (sub == s)
+  float* part = a.part + (int64_t)blockIdx.x * part_ld(a.hidden);
 #pragma unroll
-        for (int h = 0; h < NC; ++h)
+  for (int h = 0; h < NC; ++h) {
+    const int c = h * TPR + t;
+    if (c >= chunks) continue;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float* at = cols + ((h * 8 + i) * TPR + t);
-            *at = s ? *at + dw[h][i] : dw[h][i];
-          }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < a.hidden; c += WG) {
-      const int ch = c / 8;
-      part[c] = cols[(ch / TPR * 8 + c % 8) * TPR + ch % TPR];
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < NC; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = (h * TPR + t) * 8 + i;
-        if (c < a.hidden) part[c] = dw[h][i];
-      }
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(part + c * 8 + i) = f32x4{dw[h][i], dw[h][i + 1], dw[h][i + 2], dw[h][i + 3]};
   }
 }
 
-// dw[c]: the workgroups' sums, 32 columns a workgroup, each in 8 stretches joined in order
-template <int DT> __global__ __launch_bounds__(256) void k_norm_dw(NormGradArgs a, int parts) {
-  __shared__ float red[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), s = threadIdx.x >> 5;
-  float v = 0.f;
-  if (c < a.hidden)
-    for (int p = parts * s / 8; p < parts * (s + 1) / 8; ++p) v += a.part[(int64_t)p * a.hidden + c];
-  red[s][threadIdx.x & 31] = v;
+// dw[c]: the workgroups' sums, 32 columns a workgroup, four a thread, each in 128
+// stretches joined in order
+template <int DT> __global__ __launch_bounds__(1024) void k_norm_dw(NormGradArgs a, int parts) {
+  __shared__ float red[128][33];
+  __shared__ float red2[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 7) * 4, s = threadIdx.x >> 3;
+  const int64_t ld = part_ld(a.hidden);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (c < a.hidden) {
+    const int p1 = parts * (s + 1) / 128;
+#pragma unroll 4
+    for (int p = parts * s / 128; p < p1; ++p) v += *reinterpret_cast<const f32x4*>(a.part + p * ld + c);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[s][(threadIdx.x & 7) * 4 + i] = v[i];
   __syncthreads();
-  if (s || c >= a.hidden) return;
-  for (int i = 1; i < 8; ++i) v += red[i][threadIdx.x & 31];
-  if (a.w_dt == DT_F32) static_cast<float*>(a.dw)[c] = v;
-  else static_cast<uint16_t*>(a.dw)[c] = to16<DT>(v);
+  const int col = threadIdx.x & 31, g = threadIdx.x >> 5;
+  red2[g][col] = (red[g * 4][col] + red[g * 4 + 1][col]) + (red[g * 4 + 2][col] + red[g * 4 + 3][col]);
+  __syncthreads();
+  const int cc = blockIdx.x * 32 + col;
+  if (g || cc >= a.hidden) return;
+  float sum = red2[0][col];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) sum += red2[i][col];
+  if (a.w_dt == DT_F32) static_cast<float*>(a.dw)[cc] = sum;
+  else static_cast<uint16_t*>(a.dw)[cc] = to16<DT>(sum);
 }
 
 // --------------------------------------------------------------- launchers
@@ -340,27 +350,37 @@ hipError_t launch_norm(int dt, const NormArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-// Workgroups of the gradients: at most 512 (two a CU), at least 4 rows for each
-int norm_grad_parts(int rows, int hidden) {
-  const int per = hidden <= 4096 ? 4 : 1;
-  return (rows + per - 1) / per < 512 ? (rows + per - 1) / per : 512;
+// Threads of a row of the gradients: a chunk each, up to 1024
+static int grad_threads(int hidden) {
+  const int chunks = (hidden + 7) / 8;
+  int t = 64;
+  while (t < chunks && t < 1024) t *= 2;
+  return t;
 }
+// Workgroups of the gradients: 16 waves a CU, which keeps their sums at 8 MiB
+static int norm_grad_parts(int rows, int hidden) {
+  const int most = 262144 / grad_threads(hidden);
+  return rows < most ? rows : most;
+}
+int64_t norm_grad_words(int rows, int hidden) { return norm_grad_parts(rows, hidden) * part_ld(hidden); }
 template <int DT, int TPR, int NC> static hipError_t grad_run(const NormGradArgs& a, hipStream_t s) {
   const int parts = norm_grad_parts(a.rows, a.hidden);
-  hipLaunchKernelGGL((k_norm_grad<DT, TPR, NC>), dim3(parts), dim3(TPR < 256 ? 256 : TPR), 0, s, a);
+  hipLaunchKernelGGL((k_norm_grad<DT, TPR, NC>), dim3(parts), dim3(TPR), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
-  hipLaunchKernelGGL((k_norm_dw<DT>), dim3((a.hidden + 31) / 32), dim3(256), 0, s, a, parts);
+  hipLaunchKernelGGL((k_norm_dw<DT>), dim3((a.hidden + 31) / 32), dim3(1024), 0, s, a, parts);
   return hipGetLastError();
 }
 template <int DT> static hipError_t grad_pick(const NormGradArgs& a, hipStream_t s) {
+  switch (grad_threads(a.hidden)) {
+    case 64: return grad_run<DT, 64, 1>(a, s);
+    case 128: return grad_run<DT, 128, 1>(a, s);
+    case 256: return grad_run<DT, 256, 1>(a, s);
+    case 512: return grad_run<DT, 512, 1>(a, s);
+  }
   const int chunks = (a.hidden + 7) / 8;
-  if (chunks <= 64) return grad_run<DT, 64, 1>(a, s);
-  if (chunks <= 128) return grad_run<DT, 64, 2>(a, s);
-  if (chunks <= 256) return grad_run<DT, 64, 4>(a, s);
-  if (chunks <= 512) return grad_run<DT, 64, 8>(a, s);
-  if (chunks <= 2048) return grad_run<DT, 512, 4>(a, s);
-  if (chunks <= 4096) return grad_run<DT, 1024, 4>(a, s);
+  if (chunks <= 1024) return grad_run<DT, 1024, 1>(a, s);
+  if (chunks <= 2048) return grad_run<DT, 1024, 2>(a, s);
   if (chunks <= 8192) return grad_run<DT, 1024, 8>(a, s);
   return hipErrorInvalidValue;
 }
