@@ -14,6 +14,7 @@
 
 namespace moe {
 
+constexpr int NORM_WAVES = 8192;       // waves of a call at most, 32 a CU
 // a workgroup's sums of dw: whole chunks
 static __host__ __device__ int64_t part_ld(int hidden) { return (int64_t)(hidden + 7) / 8 * 8; }
 
@@ -109,97 +110,110 @@ __device__ __forceinline__ float row_rstd(const u32x4* held, int cols, float eps
 }
 
 // ---------------------------------------------------------------- the norm
-// TPR threads a row, NC chunks a thread: a wave a row where there are many, or
-// the workgroup for one.
-template <int DT, int XT, bool I8, int TPR, int NC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm(NormArgs a) {
-  constexpr int WG = TPR < 256 ? 256 : TPR;
+// A workgroup takes rows blockIdx, blockIdx + gridDim.. one at a time, a chunk (NC,
+// beyond 8192 columns) a thread, the next row's loads in flight while a row is reduced
+// and written; each thread holds its columns' weights.
+template <int DT, int XT, bool I8, int TPR, int NC> __global__ __launch_bounds__(TPR) void k_norm(NormArgs a) {
   __shared__ float red[TPR / 64];
   __shared__ uint32_t redm[TPR / 64];
-  const int t = threadIdx.x % TPR;
-  const int64_t r = (int64_t)blockIdx.x * (WG / TPR) + threadIdx.x / TPR;
-  if (TPR < 256 && r >= a.rows) return;         // whole waves
+  constexpr int XL = XT == DT_F32 ? 2 : 1;       // loads of a chunk of x
+  const int t = threadIdx.x;
   const int chunks = (a.hidden + 7) / 8;
-  const char* xr = static_cast<const char*>(a.x) + r * a.ldx * (XT == DT_F32 ? 4 : 2);
-  const char* rr = static_cast<const char*>(a.res) + r * a.ldres * 2;
-  char* tr = static_cast<char*>(a.total) + r * a.ldtotal * 2;
-  u32x4 held[NC];
+  u32x4 xs[NC][XL], rs[NC];
+  auto load = [&](int64_t r) {
+    const char* xr = static_cast<const char*>(a.x) + r * a.ldx * (XT == DT_F32 ? 4 : 2);
+    const char* rr = static_cast<const char*>(a.res) + r * a.ldres * 2;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) {
+      const int c = h * TPR + t;
+      if (c >= chunks) continue;
+#pragma unroll
+      for (int l = 0; l < XL; ++l) {
+        constexpr int ES = XT == DT_F32 ? 4 : 2;
+        xs[h][l] = u32x4{0, 0, 0, 0};
+        if (l == 0 || c * 8 + 4 < a.hidden)
+          xs[h][l] = load_chunk<ES, true>(xr, ((int64_t)c * XL + l) * 16, (int64_t)a.hidden * ES);
+      }
+      if (a.res) rs[h] = load_chunk<2, true>(rr, (int64_t)c * 16, (int64_t)a.hidden * 2);
+    }
+  };
+  load(blockIdx.x);
+  float w[NC][8];
 #pragma unroll
   for (int h = 0; h < NC; ++h) {
     const int c = h * TPR + t;
-    held[h] = u32x4{0, 0, 0, 0};
-    if (c >= chunks) continue;
-    if (XT != DT_F32 && !a.res) {
-      held[h] = load_chunk<2, true>(xr, (int64_t)c * 16, (int64_t)a.hidden * 2);
-      continue;
-    }
-    float f[8], g[8];
-    load8<XT>(xr, c, a.hidden, f);
-    load8<DT>(rr, c, a.hidden, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += g[i];
-    held[h] = pack16<DT>(f);
+    if (c < chunks) weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w[h]);
   }
-  if (a.res)
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    u32x4 held[NC];
 #pragma unroll
     for (int h = 0; h < NC; ++h) {
-      const int c = h * TPR + t;
-      if (c < chunks) store_chunk(tr, c, a.hidden, held[h]);
-    }
-  const float rstd = row_rstd<DT, TPR, NC>(held, a.hidden, a.eps, red);
-  if (a.rstd && t == 0) a.rstd[r] = rstd;
-  if constexpr (!I8) {
-    char* yr = static_cast<char*>(a.y) + r * a.ldy * 2;
-#pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      const int c = h * TPR + t;
-      if (c >= chunks) continue;
-      float f[8], w[8];
-      unpack16<DT>(held[h], f);
-      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
-      store_chunk(yr, c, a.hidden, pack16<DT>(f));
-    }
-  } else {
-    uint32_t m = 0;
-#pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      const int c = h * TPR + t;
-      if (c >= chunks) continue;
-      float f[8], w[8];
-      unpack16<DT>(held[h], f);
-      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = c * 8 + i < a.hidden ? f[i] * w[i] : 0.f;
-      m = top_bits<DT_F32, 8>(f, m);
-    }
-    m = row_max<TPR>(m, redm);
-    const RowScale rs(m);
-    if (t == 0) a.scale[r] = rs.s * rstd;
-    int8_t* qr = a.q + r * a.ldq;
-    char* yr = static_cast<char*>(a.y) + r * a.ldy * 2;
-#pragma unroll
-    for (int h = 0; h < NC; ++h) {
-      const int c = h * TPR + t;
-      if (c >= chunks) continue;
-      float f[8], w[8];
-      unpack16<DT>(held[h], f);
-      weights8<DT>(a.w, a.w_dt, a.w_add, c, a.hidden, w);
-      if (a.y) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = f[i] * rstd * w[i];
-        store_chunk(yr, c, a.hidden, pack16<DT>(y));
+      held[h] = u32x4{0, 0, 0, 0};
+      if (h * TPR + t >= chunks) continue;
+      if (XT != DT_F32 && !a.res) {
+        held[h] = xs[h][0];
+        continue;
       }
+      float f[8], g[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= w[i];
-      const uint32_t o[2] = {rs.codes4(f), rs.codes4(f + 4)};
-      if (c * 8 + 8 <= a.hidden) __builtin_memcpy(qr + c * 8, o, 8);
-      else
+      for (int l = 0; l < XL; ++l) unpack16<XT>(xs[h][l], f + 4 * l);
+      unpack16<DT>(rs[h], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c * 8 + i < a.hidden) qr[c * 8 + i] = (int8_t)(o[i / 4] >> (8 * (i & 3)));
+      for (int i = 0; i < 8; ++i) f[i] += g[i];
+      held[h] = pack16<DT>(f);
+    }
+    if (r + gridDim.x < a.rows) load(r + gridDim.x);
+    if (a.res) {
+      char* tr = static_cast<char*>(a.total) + r * a.ldtotal * 2;
+#pragma unroll
+      for (int h = 0; h < NC; ++h)
+        if (h * TPR + t < chunks) store_chunk(tr, h * TPR + t, a.hidden, held[h]);
+    }
+    const float rstd = row_rstd<DT, TPR, NC>(held, a.hidden, a.eps, red);
+    if (a.rstd && t == 0) a.rstd[r] = rstd;
+    char* yr = static_cast<char*>(a.y) + r * a.ldy * 2;
+    if (!I8 || a.y) {
+#pragma unroll
+      for (int h = 0; h < NC; ++h) {
+        const int c = h * TPR + t;
+        if (c >= chunks) continue;
+        float f[8];
+        unpack16<DT>(held[h], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[h][i];
+        store_chunk(yr, c, a.hidden, pack16<DT>(f));
+      }
+    }
+    if constexpr (I8) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int h = 0; h < NC; ++h) {
+        const int c = h * TPR + t;
+        if (c >= chunks) continue;
+        float f[8];
+        unpack16<DT>(held[h], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c * 8 + i < a.hidden ? f[i] * w[h][i] : 0.f;
+        m = top_bits<DT_F32, 8>(f, m);
+      }
+      const RowScale sc(row_max<TPR>(m, redm));
+      if (t == 0) a.scale[r] = sc.s * rstd;
+      int8_t* qr = a.q + r * a.ldq;
+#pragma unroll
+      for (int h = 0; h < NC; ++h) {
+        const int c = h * TPR + t;
+        if (c >= chunks) continue;
+        float f[8];
+        unpack16<DT>(held[h], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= w[h][i];
+        const uint32_t o[2] = {sc.codes4(f), sc.codes4(f + 4)};
+        if (c * 8 + 8 <= a.hidden) __builtin_memcpy(qr + c * 8, o, 8);
+        else
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c * 8 + i < a.hidden) qr[c * 8 + i] = (int8_t)(o[i / 4] >> (8 * (i & 3)));
+      }
     }
   }
 }
@@ -319,22 +333,26 @@ template <int DT> __global__ __launch_bounds__(1024) void k_norm_dw(NormGradArgs
 }
 
 // --------------------------------------------------------------- launchers
+// Threads of a row: a chunk each, up to 1024
+static int row_threads(int hidden) {
+  const int chunks = (hidden + 7) / 8;
+  int t = 64;
+  while (t < chunks && t < 1024) t *= 2;
+  return t;
+}
 template <int DT, int XT, bool I8, int TPR, int NC> static hipError_t norm_run(const NormArgs& a, hipStream_t s) {
-  constexpr int WG = TPR < 256 ? 256 : TPR, RPW = WG / TPR;
-  hipLaunchKernelGGL((k_norm<DT, XT, I8, TPR, NC>), dim3((a.rows + RPW - 1) / RPW), dim3(WG), 0, s, a);
+  const int most = NORM_WAVES * 64 / TPR;
+  hipLaunchKernelGGL((k_norm<DT, XT, I8, TPR, NC>), dim3(a.rows < most ? a.rows : most), dim3(TPR), 0, s, a);
   return hipGetLastError();
 }
-// Threads of a row and chunks of a thread, the first that hold it: a wave a row
-// needs no barrier and takes the calls of many rows; few rows go over more threads.
 template <int DT, int XT, bool I8> static hipError_t norm_pick(const NormArgs& a, hipStream_t s) {
-  const int chunks = (a.hidden + 7) / 8;
-  if (a.rows > 1024 || chunks <= 64) {
-    if (chunks <= 64) return norm_run<DT, XT, I8, 64, 1>(a, s);
-    if (chunks <= 128) return norm_run<DT, XT, I8, 64, 2>(a, s);
-    if (chunks <= 256) return norm_run<DT, XT, I8, 64, 4>(a, s);
-    if (chunks <= 512) return norm_run<DT, XT, I8, 64, 8>(a, s);
+  switch (row_threads(a.hidden)) {
+    case 64: return norm_run<DT, XT, I8, 64, 1>(a, s);
+    case 128: return norm_run<DT, XT, I8, 128, 1>(a, s);
+    case 256: return norm_run<DT, XT, I8, 256, 1>(a, s);
+    case 512: return norm_run<DT, XT, I8, 512, 1>(a, s);
   }
-  if (chunks <= 256) return norm_run<DT, XT, I8, 256, 1>(a, s);
+  const int chunks = (a.hidden + 7) / 8;
   if (chunks <= 1024) return norm_run<DT, XT, I8, 1024, 1>(a, s);
   if (chunks <= 2048) return norm_run<DT, XT, I8, 1024, 2>(a, s);
   if (chunks <= 8192) return norm_run<DT, XT, I8, 1024, 8>(a, s);
@@ -350,16 +368,9 @@ hipError_t launch_norm(int dt, const NormArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-// Threads of a row of the gradients: a chunk each, up to 1024
-static int grad_threads(int hidden) {
-  const int chunks = (hidden + 7) / 8;
-  int t = 64;
-  while (t < chunks && t < 1024) t *= 2;
-  return t;
-}
 // Workgroups of the gradients: 16 waves a CU, which keeps their sums at 8 MiB
 static int norm_grad_parts(int rows, int hidden) {
-  const int most = 262144 / grad_threads(hidden);
+  const int most = 4096 * 64 / row_threads(hidden);
   return rows < most ? rows : most;
 }
 int64_t norm_grad_words(int rows, int hidden) { return norm_grad_parts(rows, hidden) * part_ld(hidden); }
@@ -372,7 +383,7 @@ template <int DT, int TPR, int NC> static hipError_t grad_run(const NormGradArgs
   return hipGetLastError();
 }
 template <int DT> static hipError_t grad_pick(const NormGradArgs& a, hipStream_t s) {
-  switch (grad_threads(a.hidden)) {
+  switch (row_threads(a.hidden)) {
     case 64: return grad_run<DT, 64, 1>(a, s);
     case 128: return grad_run<DT, 128, 1>(a, s);
     case 256: return grad_run<DT, 256, 1>(a, s);
