@@ -95,8 +95,8 @@ int check_lora(const char* fn, const moe_lora* a) {
 }
 
 struct LoraPlan {
-  int rp, blocks, max_tiles, seg_rows, max_segs, slots;
-  uint64_t hist_off, perm_off, tiles_off, hi_off, lo_off, fac_off, segs_off, slot_off, span_off, u_off, top_off, part_off,
+  int rp, blocks, max_tiles, splits, seg_rows, max_segs, slots;
+  uint64_t hist_off, perm_off, tiles_off, hi_off, lo_off, fac_off, sums_off, segs_off, slot_off, span_off, u_off, top_off, part_off,
       total;
 };
 
@@ -108,7 +108,7 @@ LoraPlan plan_lora(const moe_lora* a, bool backward, bool dw) {
   p.rp = (int)up(a->rank, 32);
   p.blocks = (a->rows + LORA_SORT - 1) / LORA_SORT;
   // an adapter's last tile may be short
-  p.max_tiles = a->rows / LORA_TILE + std::min(a->adapters + 1, a->rows);
+  p.max_tiles = (int)up(a->rows / LORA_TILE + std::min(a->adapters + 1, a->rows), 8);
   Bump b;
   p.hist_off = b.take(p.blocks > 1 ? (uint64_t)p.blocks * (a->adapters + 1) * 4 : 0);
   p.perm_off = b.take(R * 4);
@@ -116,16 +116,18 @@ LoraPlan plan_lora(const moe_lora* a, bool backward, bool dw) {
   p.hi_off = b.take(R * p.rp * 2);
   p.lo_off = b.take(R * p.rp * 2);
   p.fac_off = b.take(R * 4);
+  p.splits = lora_splits(a->rows, backward ? a->out : a->in, a->rank);
+  p.sums_off = b.take((uint64_t)p.splits * R * up(a->rank, 4) * 4);
+  p.u_off = b.take(R * a->rank * 4);       // t where the caller does not keep it, or u
   if (backward) {
-    p.u_off = b.take(R * a->rank * 4);
     if (a->dtype == MOE_FP16) p.top_off = b.take((uint64_t)p.max_tiles * (LORA_TILE / 16) * 4 * 2);
   }
   if (dw) {
     // Rows of a segment: as many workgroups as fill the card twice, were the rows one
     // adapter's; every segment more costs its adapter's sums another trip through memory.
-    const int64_t tiles = ((a->in + 127) / 128 + (a->out + 127) / 128) * (int64_t)((a->rank + 63) / 64);
+    const int64_t tiles = ((a->in + 255) / 256 + (a->out + 255) / 256) * (int64_t)((a->rank + 63) / 64);
     p.seg_rows = (int)std::max<int64_t>(up((a->rows * tiles + 511) / 512, LORA_TILE), 256);
-    p.max_segs = a->rows / p.seg_rows + a->adapters;
+    p.max_segs = (int)up(a->rows / p.seg_rows + a->adapters, 8);
     // only adapters of several segments have slots: m segments hold over (m - 1) seg_rows >= m / 2 seg_rows rows
     p.slots = 2 * (a->rows / p.seg_rows);
     p.segs_off = b.take((uint64_t)p.max_segs * 16);
@@ -172,7 +174,10 @@ LoraShrink shrink_args(const moe_lora* a, const LoraPlan& p, uint8_t* w, int k, 
   s.perm = reinterpret_cast<const int*>(w + p.perm_off);
   s.tiles = reinterpret_cast<const int4*>(w + p.tiles_off);
   s.max_tiles = p.max_tiles;
-  s.t = t;
+  s.splits = p.splits;
+  s.part = reinterpret_cast<float*>(w + p.sums_off);
+  s.places = a->rows;
+  s.t = t ? t : reinterpret_cast<float*>(w + p.u_off);
   s.hi = reinterpret_cast<uint16_t*>(w + p.hi_off);
   s.lo = reinterpret_cast<uint16_t*>(w + p.lo_off);
   s.fac = reinterpret_cast<float*>(w + p.fac_off);
@@ -387,7 +392,7 @@ int moe_lora_forward(const moe_lora* a, const void* base, int64_t ldbase, void* 
   uint8_t* w = static_cast<uint8_t*>(ws);
   e = launch_lora_sort(sort_args(a, p, w), s);
   if (e == hipSuccess)
-    e = launch_lora_shrink(a->dtype, false, a->rows,
+    e = launch_lora_shrink(a->dtype, false,
                            shrink_args(a, p, w, a->in, a->x, a->ldx, a->a, a->lda, a->stride_a, t), s);
   if (e == hipSuccess)
     e = launch_lora_expand(a->dtype, false,
@@ -415,13 +420,13 @@ int moe_lora_backward(const moe_lora* a, const void* dy, int64_t lddy, const flo
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch_lora_sort(sort_args(a, p, w), s);
   float* u = reinterpret_cast<float*>(w + p.u_off);
-  LoraShrink k = shrink_args(a, p, w, a->out, dy, lddy, a->b, a->ldb, a->stride_b, da ? u : nullptr);
+  LoraShrink k = shrink_args(a, p, w, a->out, dy, lddy, a->b, a->ldb, a->stride_b, u);
   if (da && a->dtype == MOE_FP16) {
     k.top = reinterpret_cast<uint32_t*>(w + p.top_off);
     k.top2 = k.top + (int64_t)p.max_tiles * (LORA_TILE / 16);
     k.t2 = t;
   }
-  if (e == hipSuccess) e = launch_lora_shrink(a->dtype, true, a->rows, k, s);
+  if (e == hipSuccess) e = launch_lora_shrink(a->dtype, true, k, s);
   if (e == hipSuccess && dx)
     e = launch_lora_expand(a->dtype, true,
                            expand_args(a, p, w, a->in, a->a, a->lda, a->stride_a, dx_base, lddx_base, dx, lddx), s);

@@ -71,10 +71,10 @@ struct LoraSort {
   int blocks;                         // sorting workgroups
   int* hist;                          // [blocks, adapters + 1], blocks > 1
   int* perm;                          // [rows]
-  int4* tiles;                        // [max_tiles]: adapter (-1: none left), first place in perm, rows
-  int max_tiles;
+  int4* tiles;                        // [max_tiles]: adapter (-1: none left), first place in perm, rows, number
+  int max_tiles;                      // a multiple of 8
   // gradients (seg_rows = 0: none): every adapter has a segment at least
-  int seg_rows, max_segs;
+  int seg_rows, max_segs;             // multiples of LORA_TILE and of 8
   int4* segs;                         // [max_segs]: adapter (-1), first place, rows, first tile
   int* slot;                          // [max_segs]: where its partial sums go, -1: it is its adapter's only one
   int2* span;                         // [adapters]: first slot, segments (0: one)
@@ -91,7 +91,11 @@ struct LoraShrink {
   const int* perm;
   const int4* tiles;
   int max_tiles;
-  float* t;                           // fp32 [rows, rank], or null
+  int splits;                         // K ranges (lora_splits)
+  float* part;                        // [splits, places, rank to a multiple of 4] sums
+  int64_t places;                     // rows
+  float* t;                           // fp32 [rows, rank]
+  // by place in perm:
   uint16_t* hi;                       // [rows, rp] parts of t over a power of two a row (zero behind rank)
   uint16_t* lo;
   float* fac;                         // [rows] scale times that power
@@ -101,7 +105,8 @@ struct LoraShrink {
   const float* t2;
   uint32_t* top2;
 };
-hipError_t launch_lora_shrink(int dt, bool k_major, int rows, const LoraShrink& a, hipStream_t s);
+int lora_splits(int rows, int k, int rank);
+hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStream_t s);
 
 // dst[r] = base[r] + fac[r] (w_i t[r]) (k_major: w_i^T t[r]), cols wide
 struct LoraExpand {

@@ -30,14 +30,27 @@ constexpr int SORT_WG = 512, SORT_WAVES = SORT_WG / 64, SORT_BINS = 1025;
 // ------------------------------------------------------------------- sorting
 __device__ __forceinline__ int bin_of(int id, int adapters) { return (uint32_t)id < (uint32_t)adapters ? id : adapters; }
 
+// the wave's lanes with the same id (of so many bits), none for a negative one
+__device__ __forceinline__ uint64_t same(int id, int bits) {
+  uint64_t m = __ballot(id >= 0);
+  for (int i = 0; i < bits; ++i) {
+    const uint64_t set = __ballot(id >> i & 1);
+    m &= id >> i & 1 ? set : ~set;
+  }
+  return m;
+}
+
 __global__ __launch_bounds__(SORT_WG) void k_lora_hist(LoraSort a) {
   __shared__ int cnt[SORT_BINS];
   const int bins = a.adapters + 1;
   for (int b = threadIdx.x; b < bins; b += SORT_WG) cnt[b] = 0;
   __syncthreads();
+  const int bits = 32 - __builtin_clz(a.adapters), lane = threadIdx.x & 63;
   for (int i = threadIdx.x; i < LORA_SORT; i += SORT_WG) {
     const int r = blockIdx.x * LORA_SORT + i;
-    if (r < a.rows) atomicAdd(&cnt[bin_of(a.ids[r], a.adapters)], 1);
+    const int id = r < a.rows ? bin_of(a.ids[r], a.adapters) : -1;
+    const uint64_t m = same(id, bits);
+    if (id >= 0 && !(m & ((1ull << lane) - 1))) atomicAdd(&cnt[id], __popcll(m));     // whole numbers: any order
   }
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += SORT_WG) a.hist[(int64_t)blockIdx.x * bins + b] = cnt[b];
@@ -68,8 +81,9 @@ __device__ __forceinline__ Scan4 scan(Scan4 x, Scan4* wave_sum) {
 }
 
 // A stable counting sort, 8192 rows a workgroup: counts a wave in LDS, their
-// prefix sums, then each wave places its rows in order (a lane's place among the
-// wave's lanes of the same adapter from ballots over the id's bits).
+// prefix sums, then each wave places its rows. Lanes of the same adapter find each
+// other by ballots over the id's bits: runs of one adapter would queue at an LDS atomic
+// (8192 rows in runs: SORT_TIME).
 __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
   constexpr int PER = LORA_SORT / SORT_WG;      // steps of a wave
   constexpr int BPT = (SORT_BINS + SORT_WG - 1) / SORT_WG;
@@ -77,15 +91,29 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
   __shared__ int off[SORT_BINS + 1], tile[SORT_BINS + 1], seg[SORT_BINS + 1], slot[SORT_BINS + 1];
   __shared__ Scan4 wave_sum[SORT_WAVES];
   const int bins = a.adapters + 1, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < SORT_WAVES * SORT_BINS; i += SORT_WG) (&cnt[0][0])[i] = 0;
+  for (int b = threadIdx.x; b < bins; b += SORT_WG)
+#pragma unroll
+    for (int k = 0; k < SORT_WAVES; ++k) cnt[k][b] = 0;
   __syncthreads();
   const int64_t r0 = (int64_t)blockIdx.x * LORA_SORT + w * (PER * 64) + lane;
   int id[PER];
 #pragma unroll
   for (int s = 0; s < PER; ++s) id[s] = r0 + s * 64 < a.rows ? bin_of(a.ids[r0 + s * 64], a.adapters) : -1;
+  // a row's place among the wave's rows of its adapter; the counts are the wave's own
+  const int bits = 32 - __builtin_clz(a.adapters);
+  int local[PER];
 #pragma unroll
-  for (int s = 0; s < PER; ++s)
-    if (id[s] >= 0) atomicAdd(&cnt[w][id[s]], 1);
+  for (int s = 0; s < PER; ++s) {
+    const uint64_t m = same(id[s], bits);
+    local[s] = __popcll(m & ((1ull << lane) - 1));
+    if (id[s] >= 0) {
+      const int n = cnt[w][id[s]];
+      asm volatile("" ::: "memory");             // every lane has read: LDS runs in order
+      if (local[s] == 0) cnt[w][id[s]] = n + __popcll(m);
+      local[s] += n;
+    }
+    asm volatile("" ::: "memory");
+  }
   __syncthreads();
   // the bins' rows in the workgroups before this one and in all
   int all[BPT], before[BPT];
@@ -143,24 +171,9 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     }
   }
   __syncthreads();
-  const int bits = 32 - __builtin_clz(a.adapters);
 #pragma unroll
-  for (int s = 0; s < PER; ++s) {
-    const bool in = id[s] >= 0;
-    uint64_t same = __ballot(in);
-    for (int i = 0; i < bits; ++i) {
-      const uint64_t set = __ballot(in && (id[s] >> i & 1));
-      same &= id[s] >> i & 1 ? set : ~set;
-    }
-    if (in) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      const int base = cnt[w][id[s]];
-      a.perm[base + rank] = (int)(r0 + s * 64);
-      asm volatile("" ::: "memory");             // every lane has read: LDS runs in order
-      if (rank == 0) cnt[w][id[s]] = base + __popcll(same);
-    }
-    asm volatile("" ::: "memory");
-  }
+  for (int s = 0; s < PER; ++s)
+    if (id[s] >= 0) a.perm[cnt[w][id[s]] + local[s]] = (int)(r0 + s * 64);
   // the tables, shared among the workgroups: the bin of entry e is the last one that starts at or before it
   auto find = [&](const int* starts, int e) {
     int lo = 0, hi = bins;                        // starts[lo] <= e < starts[hi]
@@ -171,11 +184,18 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     }
     return lo;
   };
+  // Entry e is a workgroup's, which runs on XCD e mod 8: each XCD gets a run of
+  // neighbours, so that its L2 reads an adapter's weights (a segment's t) once.
+  auto entry = [&](int e, int total) {
+    const int x = e & 7, j = e >> 3, per = total >> 3, rem = total & 7;
+    return j < per + (x < rem) ? x * per + min(x, rem) + j : -1;
+  };
   for (int e = blockIdx.x * SORT_WG + threadIdx.x; e < a.max_tiles; e += gridDim.x * SORT_WG) {
     int4 v = make_int4(-1, 0, 0, 0);
-    if (e < tile[bins]) {
-      const int b = find(tile, e), i = (e - tile[b]) * LORA_TILE;
-      v = make_int4(b, off[b] + i, min(LORA_TILE, off[b + 1] - off[b] - i), 0);
+    const int k = entry(e, tile[bins]);
+    if (k >= 0) {
+      const int b = find(tile, k), i = (k - tile[b]) * LORA_TILE;
+      v = make_int4(b, off[b] + i, min(LORA_TILE, off[b + 1] - off[b] - i), k);
     }
     a.tiles[e] = v;
   }
@@ -183,8 +203,9 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     for (int e = blockIdx.x * SORT_WG + threadIdx.x; e < a.max_segs; e += gridDim.x * SORT_WG) {
       int4 v = make_int4(-1, 0, 0, 0);
       int sl = -1;
-      if (e < seg[bins]) {
-        const int b = find(seg, e), i = e - seg[b], n = off[b + 1] - off[b];
+      const int k = entry(e, seg[bins]);
+      if (k >= 0) {
+        const int b = find(seg, k), i = k - seg[b], n = off[b + 1] - off[b];
         v = make_int4(b, off[b] + i * a.seg_rows, min(a.seg_rows, n - i * a.seg_rows),
                       tile[b] + i * (a.seg_rows / LORA_TILE));
         if (seg[b + 1] - seg[b] > 1) sl = slot[b] + i;
@@ -213,391 +234,443 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7F800000u ? b : 0;
 }
 
+// 16-bit elements, zero in the place of infinities and NaN: what the low parts meet. A low
+// part of zero, or of the other sign than its high part, would make a NaN of the
+// infinity that the high part's product says.
+template <int DT> __device__ __forceinline__ u32x4 finite_or_zero(u32x4 v) {
+  constexpr uint32_t EXP = DT == DT_BF16 ? 0x7F80 : 0x7C00;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & EXP) == EXP) v[i] &= 0xFFFF0000u;
+    if ((v[i] >> 16 & EXP) == EXP) v[i] &= 0xFFFFu;
+  }
+  return v;
+}
+
 // ------------------------------------------------------------------- shrink
-// A workgroup: 16 MF rows of one tile, all of the rank in blocks of 16 NF. Its
-// W waves take chunks of 64 k in turn, each with all the rows and columns, so no
-// operand is loaded twice and nothing waits for another wave; their sums join
-// through LDS, half of the waves at a time. In a chunk lane quad c holds k = 32 u +
-// 8 c.. of row lane % 16: loads of 16 bytes at any alignment, the next chunk's in
-// flight. k-major weights go through a wave's own piece of LDS for the transposed read.
-template <int DT, bool KM, int MF, int NF, int W, bool BIG>
-__global__ __launch_bounds__(W * 64) void k_lora_shrink(LoraShrink a) {
-  constexpr int ROWS = MF * 16, COLS = NF * 16, WG = W * 64;
-  constexpr int JOIN = W / 2 * ROWS * COLS * 4;                   // half of the waves' sums
-  constexpr int SROW = COLS * 2 + 16, STAGE = KM ? W * 32 * SROW : 0;
-  constexpr int FCOLS = BIG ? 256 : COLS;
-  constexpr int AREA = JOIN > STAGE ? JOIN : STAGE;
-  __shared__ __align__(16) uint8_t area[AREA];
-  __shared__ __align__(16) float full[ROWS][FCOLS + 4];
-  __shared__ int s_row[ROWS];
-  __shared__ uint32_t s_top[2];
+// A workgroup of four waves: a tile's rows x 16 NF of the rank over one of several K
+// ranges, 64 k a step: rows and weights go through LDS, a wave takes 16 rows. The
+// loads of the next two steps are in flight in registers, 16 bytes a lane at any
+// alignment, whole lines of a row. The K ranges' sums go through memory to
+// k_lora_parts (joined by the last workgroup of a tile instead, the fences of every
+// workgroup cost 60 us more than that launch).
+constexpr int SHR_K = 64;
+// a row of sums in memory
+static __host__ __device__ int sum_ld(int rank) { return (rank + 3) & ~3; }
+template <int DT, bool KM, int NF> __global__ __launch_bounds__(256) void k_lora_shrink(LoraShrink a) {
+  constexpr int COLS = NF * 16, ROW = SHR_K * 2 + 16;
+  constexpr int WROW = KM ? COLS * 2 + 16 : ROW, WBYTES = KM ? SHR_K * WROW : COLS * ROW;
+  constexpr int STAGE = LORA_TILE * ROW + WBYTES;
+  constexpr int WL = (COLS * SHR_K * 2 / 16 + 255) / 256;         // chunks of weights a thread loads in a step
+  __shared__ __align__(16) uint8_t area[2 * STAGE];
+  __shared__ int s_row[LORA_TILE];
   const int4 tile = a.tiles[blockIdx.x];
-  const int first = tile.y + blockIdx.y * ROWS, n = min(tile.z - (int)blockIdx.y * ROWS, ROWS);
-  if (tile.x < 0 || n <= 0) return;
+  if (tile.x < 0 || tile.x == a.adapters) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const bool none = tile.x == a.adapters;
-  if (threadIdx.x < ROWS) s_row[threadIdx.x] = a.perm[first + min((int)threadIdx.x, n - 1)];
-  if (threadIdx.x < 2) s_top[threadIdx.x] = 0;
+  if (threadIdx.x < LORA_TILE) s_row[threadIdx.x] = a.perm[tile.y + min((int)threadIdx.x, tile.z - 1)];
   __syncthreads();
-  if (!none) {
-    const uint16_t* wi = static_cast<const uint16_t*>(a.w) + tile.x * a.stw;
-    const uint16_t* src[MF];
+  const int j0 = blockIdx.y * COLS, z = (int)((blockIdx.z + (uint32_t)tile.w) % gridDim.z);
+  const int steps = (a.k + SHR_K - 1) / SHR_K;
+  const int t0 = (int)((int64_t)steps * z / gridDim.z), t1 = (int)((int64_t)steps * (z + 1) / gridDim.z);
+  const uint16_t* wi = static_cast<const uint16_t*>(a.w) + tile.x * a.stw;
+  const int64_t end = (int64_t)a.k * 2;
+  // rows: 8 chunks each, 32 rows at a time; rows past the tile's repeat its last one
+  const int xr = threadIdx.x >> 3, xc = (threadIdx.x & 7) * 16;
+  const uint16_t* src[2];
 #pragma unroll
-    for (int m = 0; m < MF; ++m) src[m] = static_cast<const uint16_t*>(a.src) + s_row[m * 16 + col] * a.ldsrc;
-    const int chunks = (a.k + 63) / 64;
-    const int64_t end = (int64_t)a.k * 2;
-    uint8_t* const stage = area + (KM ? w * 32 * SROW : 0);
-#pragma unroll 1
-    for (int j0 = 0; j0 < a.rank; j0 += COLS) {
-      f32x4 acc[NF][MF];
+  for (int i = 0; i < 2; ++i) src[i] = static_cast<const uint16_t*>(a.src) + s_row[xr + i * 32] * a.ldsrc;
+  struct Step {
+    u32x4 x[2], w[WL];
+  };
+  auto load = [&](Step& s, int t) {
+    const int64_t at = (int64_t)t * (SHR_K * 2) + xc;
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
+    for (int i = 0; i < 2; ++i) s.x[i] = load_chunk<2, true>(src[i], at, end);
 #pragma unroll
-        for (int m = 0; m < MF; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const uint16_t* wr[NF];
-      if constexpr (!KM)
-#pragma unroll
-        for (int f = 0; f < NF; ++f) wr[f] = wi + min(j0 + f * 16 + col, a.rank - 1) * a.ldw;
-      // u: which half of the chunk; k-major: 32 k rows of 2 NF chunks of 16 bytes
-      u32x4 xv[2][MF], wv[2][NF];
-      auto load = [&](int ch) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t at = (int64_t)ch * 128 + u * 64 + quad * 16;
-#pragma unroll
-          for (int m = 0; m < MF; ++m) xv[u][m] = load_chunk<2>(src[m], at, end);
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            if constexpr (!KM) {
-              wv[u][f] = load_chunk<2>(wr[f], at, end);
-            } else {
-              const int q = f * 64 + lane, k = ch * 64 + u * 32 + q / (2 * NF), c = q % (2 * NF);
-              wv[u][f] = u32x4{0, 0, 0, 0};
-              if (k < a.k && j0 + c * 8 < a.rank)
-                wv[u][f] = load_chunk<2>(wi + k * a.ldw, (int64_t)(j0 + c * 8) * 2, (int64_t)a.rank * 2);
-            }
-          }
-        }
-      };
-      if (w < chunks) load(w);
-      for (int ch = w; ch < chunks; ch += W) {
-        u32x4 x0[2][MF], w0[2][NF];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int m = 0; m < MF; ++m) x0[u][m] = xv[u][m];
-#pragma unroll
-          for (int f = 0; f < NF; ++f) w0[u][f] = wv[u][f];
-        }
-        if (ch + W < chunks) load(ch + W);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (KM) {
-            asm volatile("" ::: "memory");
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-              const int q = f * 64 + lane;
-              *reinterpret_cast<u32x4*>(stage + q / (2 * NF) * SROW + q % (2 * NF) * 16) = w0[u][f];
-            }
-            asm volatile("" ::: "memory");         // the wave's own LDS runs in order
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-              w0[u][f] = read_tr(stage + (quad * 8 + (col >> 2)) * SROW + f * 32 + (col & 3) * 8, 4 * SROW);
-          }
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-#pragma unroll
-            for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(w0[u][f], x0[u][m], acc[f][m]);
-        }
+    for (int i = 0; i < WL; ++i) {
+      const int q = i * 256 + threadIdx.x;
+      s.w[i] = u32x4{0, 0, 0, 0};
+      if constexpr (!KM) {
+        const int r = j0 + q / 8;                // (rank rows past the last: zero)
+        if (q / 8 < COLS && r < a.rank) s.w[i] = load_chunk<2, true>(wi + r * a.ldw, at, end);
+      } else {
+        const int k = t * SHR_K + q / (COLS / 8), c = j0 + q % (COLS / 8) * 8;
+        if (q / (COLS / 8) < SHR_K && k < a.k && c < a.rank)
+          s.w[i] = load_chunk<2, true>(wi + k * a.ldw, (int64_t)c * 2, (int64_t)a.rank * 2);
       }
-      // lane: row m 16 + col, columns f 16 + quad 4..
+    }
+  };
+  f32x4 acc[NF];
 #pragma unroll
-      for (int half = W / 2; half; half /= 2) {
-        __syncthreads();                           // the area is free
-        f32x4* buf = reinterpret_cast<f32x4*>(area) + (w % half) * (NF * MF * 64) + lane;
-        if (w >= half && w < 2 * half)
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](const Step& s, int buf) {
+    uint8_t* const sx = area + buf * STAGE;
+    uint8_t* const sw = sx + LORA_TILE * ROW;
 #pragma unroll
-          for (int f = 0; f < NF; ++f)
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(sx + (xr + i * 32) * ROW + xc) = s.x[i];
 #pragma unroll
-            for (int m = 0; m < MF; ++m) buf[(f * MF + m) * 64] = acc[f][m];
-        __syncthreads();
-        if (w < half)
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-#pragma unroll
-            for (int m = 0; m < MF; ++m) acc[f][m] += buf[(f * MF + m) * 64];
+    for (int i = 0; i < WL; ++i) {
+      const int q = i * 256 + threadIdx.x;
+      if constexpr (!KM) {
+        if (q / 8 < COLS) *reinterpret_cast<u32x4*>(sw + q / 8 * WROW + q % 8 * 16) = s.w[i];
+      } else {
+        if (q / (COLS / 8) < SHR_K) *reinterpret_cast<u32x4*>(sw + q / (COLS / 8) * WROW + q % (COLS / 8) * 16) = s.w[i];
       }
-      if (w == 0)
+    }
+  };
+  auto multiply = [&](int buf) {
+    const uint8_t* const sx = area + buf * STAGE;
+    const uint8_t* const sw = sx + LORA_TILE * ROW;
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+    for (int u = 0; u < 2; ++u) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(sx + (w * 16 + col) * ROW + u * 64 + quad * 16);
 #pragma unroll
-          for (int m = 0; m < MF; ++m)
-            *reinterpret_cast<f32x4*>(&full[m * 16 + col][(BIG ? j0 : 0) + f * 16 + quad * 4]) = acc[f][m];
-      __syncthreads();                             // the next block's pieces lie where wave 0 has read
+      for (int f = 0; f < NF; ++f) {
+        u32x4 p;
+        if constexpr (!KM) p = *reinterpret_cast<const u32x4*>(sw + (f * 16 + col) * WROW + u * 64 + quad * 16);
+        else p = read_tr(sw + (u * 32 + quad * 8 + (col >> 2)) * WROW + f * 32 + (col & 3) * 8, 4 * WROW);
+        acc[f] = Elem<DT>::mma16(p, x, acc[f]);
+      }
+    }
+  };
+  // One barrier a step: a buffer is written again two steps on, when every wave
+  // has passed the barrier behind its readers.
+  Step s[2];
+  if (t0 < t1) load(s[0], t0);
+  if (t0 + 1 < t1) load(s[1], t0 + 1);
+  for (int t = t0; t < t1; t += 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (t + i >= t1) break;
+      step(s[i], i);
+      if (t + i + 2 < t1) load(s[i], t + i + 2);
+      __syncthreads();
+      multiply(i);
     }
   }
-  // a row's sums to memory: WG / ROWS threads a row
-  constexpr int TPR = WG / ROWS;
-  const int i = threadIdx.x / TPR, g = threadIdx.x % TPR;
-  const bool in = i < n;
-  const int64_t r = s_row[i];
-  uint32_t m = 0, m2 = 0;
-  if (!none)
-    for (int j = g; j < a.rank; j += TPR) m = max(m, finite_bits(full[i][j]));
-  if (a.t2)
-    for (int j = g; j < a.rank; j += TPR) m2 = max(m2, finite_bits(a.t2[r * a.rank + j]));
+  // lane: row w 16 + col, columns f 16 + quad 4..
+  const int i = w * 16 + col;
+  float* part = a.part + ((int64_t)z * a.places + tile.y + i) * sum_ld(a.rank);
+  if (i < tile.z)
 #pragma unroll
-  for (int d = TPR / 2; d; d >>= 1) {
+    for (int f = 0; f < NF; ++f) {
+      const int j = j0 + f * 16 + quad * 4;
+      if (j < a.rank) *reinterpret_cast<f32x4*>(part + j) = acc[f];
+    }
+}
+
+// A tile's rows, four threads each, four of the rank at a time: the K ranges' sums in
+// order to t, its largest value, then its parts.
+template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink a) {
+  __shared__ uint32_t s_top[LORA_TILE / 16][2];
+  const int4 tile = a.tiles[blockIdx.x];
+  if (tile.x < 0) return;
+  const bool none = tile.x == a.adapters;
+  if (threadIdx.x < LORA_TILE / 16 * 2) s_top[threadIdx.x / 2][threadIdx.x % 2] = 0;
+  __syncthreads();
+  const int i = threadIdx.x >> 2, g = (threadIdx.x & 3) * 4, ld = sum_ld(a.rank);
+  const bool in = i < tile.z;
+  const int64_t p = tile.y + i, r = a.perm[tile.y + min(i, tile.z - 1)];
+  float* const tr = a.t + r * a.rank;
+  uint32_t m = 0, m2 = 0;
+  if (in)
+    for (int j = g; j < a.rank; j += 16) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (!none) {
+        const float* at = a.part + p * ld + j;
+        v = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll 4
+        for (int z = 1; z < a.splits; ++z) v += *reinterpret_cast<const f32x4*>(at + (int64_t)z * a.places * ld);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (j + e >= a.rank) continue;
+        tr[j + e] = v[e];
+        m = max(m, finite_bits(v[e]));
+        if (a.t2) m2 = max(m2, finite_bits(a.t2[r * a.rank + j + e]));
+      }
+    }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
     m = max(m, (uint32_t)__shfl_xor((int)m, d));
     m2 = max(m2, (uint32_t)__shfl_xor((int)m2, d));
   }
   if (a.top) {
-    if (in && g == 0) {
-      atomicMax(&s_top[0], m);                     // a maximum: any order
-      atomicMax(&s_top[1], m2);
+    if (g == 0) {
+      atomicMax(&s_top[i / 16][0], m);             // a maximum: any order
+      atomicMax(&s_top[i / 16][1], m2);
     }
     __syncthreads();
-    if (threadIdx.x < MF) {
-      const int at = blockIdx.x * (LORA_TILE / 16) + blockIdx.y * MF + threadIdx.x;
-      a.top[at] = s_top[0];
-      a.top2[at] = s_top[1];
+    if (threadIdx.x < LORA_TILE / 16) {
+      a.top[tile.w * (LORA_TILE / 16) + threadIdx.x] = s_top[threadIdx.x][0];
+      a.top2[tile.w * (LORA_TILE / 16) + threadIdx.x] = s_top[threadIdx.x][1];
     }
   }
-  if (!in) return;
+  if (!in || none) return;
   // fp16: |t| below 2^14, in one row's own power of two
   const int e = DT == DT_F16 ? exponent(m) - 14 : 0;
-  if (g == 0) a.fac[r] = none ? 0.f : __builtin_ldexpf(a.scale[tile.x], e);
-  for (int j = g; j < a.rp; j += TPR) {
-    const float v = none || j >= a.rank ? 0.f : full[i][j];
-    if (a.t && j < a.rank) a.t[r * a.rank + j] = v;
-    if (none) continue;
-    const float s = DT == DT_F16 ? __builtin_ldexpf(v, -e) : v;
-    a.hi[r * a.rp + j] = to16<DT>(s);
-    a.lo[r * a.rp + j] = to16<DT>(low_part<DT>(s));
+  if (g == 0) a.fac[p] = __builtin_ldexpf(a.scale[tile.x], e);
+  for (int j = g; j < a.rp; j += 16) {
+    float v[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = j + k < a.rank ? tr[j + k] : 0.f;     // this thread's own stores
+      if constexpr (DT == DT_F16) v[k] = __builtin_ldexpf(v[k], -e);
+      l[k] = low_part<DT>(v[k]);
+    }
+    *reinterpret_cast<uint2*>(a.hi + p * a.rp + j) = make_uint2(to16<DT>(v[0]) | (uint32_t)to16<DT>(v[1]) << 16,
+                                                                to16<DT>(v[2]) | (uint32_t)to16<DT>(v[3]) << 16);
+    *reinterpret_cast<uint2*>(a.lo + p * a.rp + j) = make_uint2(to16<DT>(l[0]) | (uint32_t)to16<DT>(l[1]) << 16,
+                                                                to16<DT>(l[2]) | (uint32_t)to16<DT>(l[3]) << 16);
   }
 }
 
 // ------------------------------------------------------------------- expand
 // A workgroup of four waves: a tile's rows, EXP_COLS columns of the result, a wave
-// 64 rows x 32 columns at a time. The weights' rows are dealt to the fragments so
-// that a lane ends with 8 consecutive columns of a row (fragment f, place m: column
-// 8 (m / 4) + 4 f + m % 4): base and result move 16 bytes a lane, 64 a row. The
-// parts' products have sums of their own, joined where the high one is finite: an
-// infinite weight times a low part of zero would make a NaN of it. KB: blocks of 32
-// of the rank whose parts stay in registers (0: any rank, read each time).
-constexpr int EXP_COLS = 512;
+// 32 rows x 32 columns at a time, the next columns' loads in flight. The weights' rows
+// are dealt to the fragments so that a lane ends with 8 consecutive columns of a row
+// (fragment f, place m: column 8 (m / 4) + 4 f + m % 4): base and result move 16 bytes a
+// lane, 64 a row. KB: blocks of 32 of the rank whose parts stay in registers (0: any
+// rank, read each time).
+constexpr int EXP_COLS = 256;
 template <int DT, bool KM, int KB>
 __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
-  constexpr int MF = 4, F = 2, SROW = 80;
-  __shared__ __align__(16) uint8_t area[KM ? 4 * 32 * SROW : 16];
+  constexpr int MF = 2, F = 2, KU = KB ? KB : 1, SROW = 80;
+  __shared__ __align__(16) uint8_t area[KM ? 4 * KU * 32 * SROW : 16];
   const int4 tile = a.tiles[blockIdx.x];
   if (tile.x < 0) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
+  const int m0 = (w & 1) * 32;                     // the wave's rows
+  if (m0 >= tile.z) return;
   const bool none = tile.x == a.adapters;
-  const int kb = KB ? KB : a.rp / 32;
-  int64_t row[MF];
-  float fac[MF];
-  u32x4 th[KB ? KB : 1][MF], tl[KB ? KB : 1][MF];
+  const uint16_t* wi = static_cast<const uint16_t*>(a.w) + (none ? 0 : tile.x * a.stw);
+  uint8_t* const stage = area + (KM ? w * (KU * 32 * SROW) : 0);
+  int64_t row[MF], at[MF];
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
-    row[m] = a.perm[tile.y + min(m * 16 + col, tile.z - 1)];
-    fac[m] = none ? 0.f : a.fac[row[m]];
+    at[m] = tile.y + min(m0 + m * 16 + col, tile.z - 1);
+    row[m] = a.perm[at[m]];
   }
+  u32x4 th[KU][MF], tl[KU][MF];
   auto parts = [&](int k, u32x4* h, u32x4* l) {
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      h[m] = *reinterpret_cast<const u32x4*>(a.hi + row[m] * a.rp + k * 32 + quad * 8);
-      l[m] = *reinterpret_cast<const u32x4*>(a.lo + row[m] * a.rp + k * 32 + quad * 8);
+      h[m] = *reinterpret_cast<const u32x4*>(a.hi + at[m] * a.rp + k * 32 + quad * 8);
+      l[m] = *reinterpret_cast<const u32x4*>(a.lo + at[m] * a.rp + k * 32 + quad * 8);
     }
   };
-  if constexpr (KB > 0)
-    if (!none)
+  float fac[MF];
+  if (!none) {
+#pragma unroll
+    for (int m = 0; m < MF; ++m) fac[m] = a.fac[at[m]];
+    if constexpr (KB > 0)
 #pragma unroll
       for (int k = 0; k < KB; ++k) parts(k, th[k], tl[k]);
-  const uint16_t* wi = static_cast<const uint16_t*>(a.w) + (none ? 0 : tile.x * a.stw);
-  uint8_t* const stage = area + (KM ? w * 32 * SROW : 0);
-  const int c_end = min(a.cols, (int)(blockIdx.y + 1) * EXP_COLS);
-#pragma unroll 1
-  for (int c0 = blockIdx.y * EXP_COLS + w * 32; c0 < c_end; c0 += 128) {
-    const int c = c0 + quad * 8;                   // the lane's 8 columns
-    u32x4 bv[MF];
+  }
+  // weights of k block k: NT rows of the lane's columns; k-major 32 k rows of 4 chunks
+  auto weights = [&](int c0, int k, u32x4* v) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if constexpr (!KM) {
+        const int c = c0 + (col >> 2) * 8 + f * 4 + (col & 3);
+        v[f] = load_chunk<2, true>(wi + min(c, a.cols - 1) * a.ldw, (int64_t)(k * 32 + quad * 8) * 2, (int64_t)a.rank * 2);
+      } else {
+        const int kr = k * 32 + f * 16 + lane / 4, c = c0 + lane % 4 * 8;
+        v[f] = u32x4{0, 0, 0, 0};
+        if (kr < a.rank && c < a.cols) v[f] = load_chunk<2, true>(wi + kr * a.ldw, (int64_t)c * 2, (int64_t)a.cols * 2);
+      }
+    }
+  };
+  struct Cols {
+    u32x4 w[KU][F], b[MF];
+  };
+  auto load = [&](Cols& s, int c0) {
+    if constexpr (KB > 0)
+      if (!none)
+#pragma unroll
+        for (int k = 0; k < KB; ++k) weights(c0, k, s.w[k]);
+    const int c = c0 + quad * 8;
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      bv[m] = u32x4{0, 0, 0, 0};
+      s.b[m] = u32x4{0, 0, 0, 0};
       if (a.base && c < a.cols)
-        bv[m] = load_chunk<2, true>(static_cast<const uint16_t*>(a.base) + row[m] * a.ldbase, (int64_t)c * 2, (int64_t)a.cols * 2);
+        s.b[m] = load_chunk<2, true>(static_cast<const uint16_t*>(a.base) + row[m] * a.ldbase, (int64_t)c * 2, (int64_t)a.cols * 2);
     }
-    f32x4 hi[F][MF], lo[F][MF];
+  };
+  // tiles start with different columns, so that neighbours read different weights
+  const int y = (int)((blockIdx.y + (uint32_t)tile.w) % gridDim.y), c_end = min(a.cols, (y + 1) * EXP_COLS);
+  int c0 = y * EXP_COLS + (w >> 1) * 32;
+  Cols next;
+  if (c0 < c_end) load(next, c0);
+#pragma unroll 1
+  for (; c0 < c_end; c0 += 64) {
+    Cols cur = next;
+    if (c0 + 64 < c_end) load(next, c0 + 64);
+    f32x4 acc[F][MF];
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int m = 0; m < MF; ++m) hi[f][m] = lo[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int m = 0; m < MF; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (!none) {
 #pragma unroll
       for (int k = 0; k < (KB ? KB : 8); ++k) {
-        if (!KB && k >= kb) break;
+        if (!KB && k * 32 >= a.rp) break;
+        const int ku = KB ? k : 0;
+        if constexpr (KB == 0) {
+          weights(c0, k, cur.w[0]);
+          parts(k, th[0], tl[0]);
+        }
         u32x4 p[F];
-        if constexpr (!KM) {
-#pragma unroll
-          for (int f = 0; f < F; ++f) {
-            const int at = c0 + (col >> 2) * 8 + f * 4 + (col & 3);
-            p[f] = load_chunk<2>(wi + min(at, a.cols - 1) * a.ldw, (int64_t)(k * 32 + quad * 8) * 2, (int64_t)a.rank * 2);
-          }
-        } else {
-          // 32 k rows of 4 chunks of 16 bytes
-          u32x4 v[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int kr = k * 32 + (q * 64 + lane) / 4, cc = c0 + lane % 4 * 8;
-            v[q] = u32x4{0, 0, 0, 0};
-            if (kr < a.rank && cc < a.cols) v[q] = load_chunk<2, true>(wi + kr * a.ldw, (int64_t)cc * 2, (int64_t)a.cols * 2);
-          }
+        if constexpr (KM) {
+          uint8_t* const st = stage + ku * (32 * SROW);
           asm volatile("" ::: "memory");
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<u32x4*>(stage + (q * 64 + lane) / 4 * SROW + lane % 4 * 16) = v[q];
+          for (int f = 0; f < F; ++f) *reinterpret_cast<u32x4*>(st + (f * 16 + lane / 4) * SROW + lane % 4 * 16) = cur.w[ku][f];
           asm volatile("" ::: "memory");           // the wave's own LDS runs in order
 #pragma unroll
           for (int f = 0; f < F; ++f)
-            p[f] = read_tr(stage + (quad * 8 + (col >> 2)) * SROW + (col & 3) * 16 + f * 8, 4 * SROW);
+            p[f] = read_tr(st + (quad * 8 + (col >> 2)) * SROW + (col & 3) * 16 + f * 8, 4 * SROW);
+        } else {
+#pragma unroll
+          for (int f = 0; f < F; ++f) p[f] = cur.w[ku][f];
         }
-        if constexpr (KB == 0) parts(k, th[0], tl[0]);
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int f = 0; f < F; ++f) {
 #pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            hi[f][m] = Elem<DT>::mma16(p[f], th[KB ? k : 0][m], hi[f][m]);
-            lo[f][m] = Elem<DT>::mma16(p[f], tl[KB ? k : 0][m], lo[f][m]);
-          }
+          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(p[f], th[ku][m], acc[f][m]);
+          const u32x4 z = finite_or_zero<DT>(p[f]);
+#pragma unroll
+          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(z, tl[ku][m], acc[f][m]);
+        }
       }
     }
+    const int c = c0 + quad * 8;
     if (c >= a.cols) continue;
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      if (m * 16 + col >= tile.z) continue;
+      if (m0 + m * 16 + col >= tile.z) continue;
       float v[8];
-      unpack16<DT>(bv[m], v);
+      unpack16<DT>(cur.b[m], v);
       if (!none)
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float h = hi[f][m][e];
-            v[f * 4 + e] += fac[m] * (__builtin_fabsf(h) < __builtin_inff() ? h + lo[f][m][e] : h);
-          }
+        for (int e = 0; e < 8; ++e) v[e] += fac[m] * acc[e / 4][m][e % 4];
       const u32x4 o = pack16<DT>(v);
-      uint16_t* at = static_cast<uint16_t*>(a.dst) + row[m] * a.lddst + c;
-      if (c + 8 <= a.cols) __builtin_memcpy(at, &o, 16);      // at any alignment
+      uint16_t* to = static_cast<uint16_t*>(a.dst) + row[m] * a.lddst + c;
+      if (c + 8 <= a.cols) __builtin_memcpy(to, &o, 16);      // at any alignment
       else
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (c + e < a.cols) at[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+          if (c + e < a.cols) to[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
     }
   }
 }
 
 // ---------------------------------------------------------------- gradients
-// A workgroup of four waves: 64 of the rank x 128 columns of one segment's sums over
+// A workgroup of eight waves: 64 of the rank x 256 columns of one segment's sums over
 // its rows, 64 rows a step: the 16-bit rows and the parts of the fp32 ones go through
-// LDS (the next step's on their way in registers), both read transposed. da's lanes
-// end with 8 consecutive columns of a rank row, db's with 16 consecutive ranks of a
-// column's row: the operands change places.
-constexpr int GRAD_COLS = 128, GRAD_ROWS = 64;
+// LDS (the next step's on their way in registers, the places of the one after that
+// too), both read transposed. da's lanes end with 8 consecutive columns of a rank
+// row, db's with 16 consecutive ranks of a column's row: the operands change places.
+constexpr int GRAD_WG = 512, GRAD_COLS = 256, GRAD_ROWS = 64;
+constexpr int GRAD_XROW = GRAD_COLS * 2 + 16, GRAD_TROW = 128 + 16;      // bytes in LDS
 template <int DT, bool DB>
 __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot, int j0, int c0, uint8_t* sx, uint8_t* st,
-                                          uint32_t* s_top) {
-  constexpr int XROW = GRAD_COLS * 2 + 16, TROW = 128 + 16;
+                                          uint32_t* s_top, int (*s_perm)[GRAD_ROWS]) {
+  constexpr int XROW = GRAD_XROW, TROW = GRAD_TROW;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
   const int cols = DB ? a.out : a.in;
   const float* tp = DB ? a.t : a.u;
   const uint16_t* xp = static_cast<const uint16_t*>(DB ? a.dy : a.x);
   const int64_t ld = DB ? a.lddy : a.ldx;
+  auto place = [&](int i) { return i < seg.z ? a.perm[seg.y + i] : -1; };
+  if (threadIdx.x < 2 * GRAD_ROWS) s_perm[threadIdx.x / GRAD_ROWS][threadIdx.x % GRAD_ROWS] = place(threadIdx.x);
   int e = 0;                                       // fp16: parts are |t| 2^-e, below 2^14
   if constexpr (DT == DT_F16) {
     const uint32_t* top = (DB ? a.top_t : a.top_u) + seg.w * (LORA_TILE / 16);
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < (seg.z + 15) / 16; i += 256) m = max(m, top[i]);
+    for (int i = threadIdx.x; i < (seg.z + 15) / 16; i += GRAD_WG) m = max(m, top[i]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
     if (lane == 0) s_top[w] = m;
     __syncthreads();
-    e = exponent(max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]))) - 14;
+#pragma unroll
+    for (int i = 0; i < GRAD_WG / 64; ++i) m = max(m, s_top[i]);
+    e = exponent(m) - 14;
   }
-  // x: 16 chunks a row, 16 rows at a time; t: 4 threads a row, 16 of the rank each
-  const int xr = threadIdx.x >> 4, xc = threadIdx.x & 15, tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 16;
+  __syncthreads();
+  // x: 32 chunks a row, 16 rows at a time; t: 8 threads a row, 8 of the rank each
+  const int xr = threadIdx.x >> 5, xc = threadIdx.x & 31, tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
   u32x4 xv[4];
-  float tv[16];
-  auto row_of = [&](int i) { return i < seg.z ? a.perm[seg.y + i] : -1; };
-  auto load = [&](int i0) {
+  float tv[8];
+  int next = -1;
+  auto load = [&](const int* perm) {
+    int r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = perm[xr + i * 16];
+    const int rt = perm[tr];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = row_of(i0 + xr + i * 16);
       xv[i] = u32x4{0, 0, 0, 0};
-      if (r >= 0 && c0 + xc * 8 < cols)
-        xv[i] = load_chunk<2, true>(xp + r * ld, (int64_t)(c0 + xc * 8) * 2, (int64_t)cols * 2);
+      if (r[i] >= 0 && c0 + xc * 8 < cols)
+        xv[i] = load_chunk<2, true>(xp + r[i] * ld, (int64_t)(c0 + xc * 8) * 2, (int64_t)cols * 2);
     }
-    const int r = row_of(i0 + tr);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       u32x4 v = {0, 0, 0, 0};
-      if (r >= 0 && j0 + tc + i * 4 < a.rank)
-        v = load_chunk<4>(tp + (int64_t)r * a.rank, (int64_t)(j0 + tc + i * 4) * 4, (int64_t)a.rank * 4);
+      if (rt >= 0 && j0 + tc + i * 4 < a.rank)
+        v = load_chunk<4>(tp + (int64_t)rt * a.rank, (int64_t)(j0 + tc + i * 4) * 4, (int64_t)a.rank * 4);
       unpack16<DT_F32>(v, tv + i * 4);
     }
   };
-  f32x4 hi[2][4], lo[2][4];                        // [x fragment][t fragment]
+  f32x4 acc[2][4];                                 // [x fragment][t fragment]
 #pragma unroll
   for (int f = 0; f < 2; ++f)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hi[f][j] = lo[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (seg.z > 0) load(0);
-  for (int i0 = 0; i0 < seg.z; i0 += GRAD_ROWS) {
+    for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (seg.z > 0) load(s_perm[0]);
+  for (int i0 = 0, step = 0; i0 < seg.z; i0 += GRAD_ROWS, ++step) {
     __syncthreads();                               // the last step's readers are done
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(sx + (xr + i * 16) * XROW + xc * 16) = xv[i];
-    float low[16];
+    float low[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       if constexpr (DT == DT_F16) tv[i] = __builtin_ldexpf(tv[i], -e);
       low[i] = low_part<DT>(tv[i]);
     }
     uint8_t* h = st + tr * TROW + tc * 2;
-    uint8_t* l = h + GRAD_ROWS * TROW;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<u32x4*>(h + i * 16) = pack16<DT>(tv + i * 8);
-      *reinterpret_cast<u32x4*>(l + i * 16) = pack16<DT>(low + i * 8);
-    }
+    *reinterpret_cast<u32x4*>(h) = pack16<DT>(tv);
+    *reinterpret_cast<u32x4*>(h + GRAD_ROWS * TROW) = pack16<DT>(low);
+    if (step && threadIdx.x < GRAD_ROWS) s_perm[(step + 1) & 1][threadIdx.x] = next;
     __syncthreads();
-    if (i0 + GRAD_ROWS < seg.z) load(i0 + GRAD_ROWS);
+    if (threadIdx.x < GRAD_ROWS) next = place(i0 + 2 * GRAD_ROWS + threadIdx.x);
+    if (i0 + GRAD_ROWS < seg.z) load(s_perm[(step + 1) & 1]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int kr = k * 32 + quad * 8 + (col >> 2);
-      u32x4 x[2], th[4], tl[4];
+      u32x4 x[2], z[2];
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < 2; ++f) {
         x[f] = read_tr(sx + kr * XROW + w * 64 + (DB ? f * 32 + (col & 3) * 8 : (col & 3) * 16 + f * 8), 4 * XROW);
+        z[f] = finite_or_zero<DT>(x[f]);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint8_t* at = st + kr * TROW + (DB ? (col & 3) * 32 + j * 8 : j * 32 + (col & 3) * 8);
-        th[j] = read_tr(at, 4 * TROW);
-        tl[j] = read_tr(at + GRAD_ROWS * TROW, 4 * TROW);
-      }
+        const u32x4 th = read_tr(at, 4 * TROW), tl = read_tr(at + GRAD_ROWS * TROW, 4 * TROW);
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[f][j] = DB ? Elem<DT>::mma16(th[j], x[f], hi[f][j]) : Elem<DT>::mma16(x[f], th[j], hi[f][j]);
-          lo[f][j] = DB ? Elem<DT>::mma16(tl[j], x[f], lo[f][j]) : Elem<DT>::mma16(x[f], tl[j], lo[f][j]);
+        for (int f = 0; f < 2; ++f) {
+          acc[f][j] = DB ? Elem<DT>::mma16(th, x[f], acc[f][j]) : Elem<DT>::mma16(x[f], th, acc[f][j]);
+          acc[f][j] = DB ? Elem<DT>::mma16(tl, z[f], acc[f][j]) : Elem<DT>::mma16(z[f], tl, acc[f][j]);
         }
+      }
     }
   }
   const float scale = a.scale[seg.x];
   auto value = [&](int f, int j, int q) {
-    const float h = hi[f][j][q], v = __builtin_fabsf(h) < __builtin_inff() ? h + lo[f][j][q] : h;
-    return DT == DT_F16 ? __builtin_ldexpf(v, e) : v;
+    return DT == DT_F16 ? __builtin_ldexpf(acc[f][j][q], e) : acc[f][j][q];
   };
   // N consecutive values of a row of the result, from column c on of n: rounded, or
   // (one of several segments) as they are
@@ -650,14 +723,15 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
     }
   }
 }
-template <int DT> __global__ __launch_bounds__(256) void k_lora_grad(LoraGrad a, int in_tiles) {
-  __shared__ __align__(16) uint8_t sx[GRAD_ROWS * (GRAD_COLS * 2 + 16)], st[2 * GRAD_ROWS * 144];
-  __shared__ uint32_t s_top[4];
+template <int DT> __global__ __launch_bounds__(GRAD_WG) void k_lora_grad(LoraGrad a, int in_tiles) {
+  __shared__ __align__(16) uint8_t sx[GRAD_ROWS * GRAD_XROW], st[2 * GRAD_ROWS * GRAD_TROW];
+  __shared__ uint32_t s_top[GRAD_WG / 64];
+  __shared__ int s_perm[2][GRAD_ROWS];
   const int4 seg = a.segs[blockIdx.x];
   if (seg.x < 0) return;
   const int slot = a.slot[blockIdx.x], j0 = blockIdx.z * 64;
-  if ((int)blockIdx.y < in_tiles) lora_grad<DT, false>(a, seg, slot, j0, blockIdx.y * GRAD_COLS, sx, st, s_top);
-  else lora_grad<DT, true>(a, seg, slot, j0, (blockIdx.y - in_tiles) * GRAD_COLS, sx, st, s_top);
+  if ((int)blockIdx.y < in_tiles) lora_grad<DT, false>(a, seg, slot, j0, blockIdx.y * GRAD_COLS, sx, st, s_top, s_perm);
+  else lora_grad<DT, true>(a, seg, slot, j0, (blockIdx.y - in_tiles) * GRAD_COLS, sx, st, s_top, s_perm);
 }
 // the sums of adapters of several segments, in order
 template <int DT> __global__ __launch_bounds__(256) void k_lora_join(LoraGrad a) {
@@ -755,24 +829,24 @@ hipError_t launch_lora_sort(const LoraSort& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, bool KM, int MF, int NF, int W, bool BIG> static hipError_t shrink(const LoraShrink& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_lora_shrink<DT, KM, MF, NF, W, BIG>), dim3(a.max_tiles, LORA_TILE / 16 / MF), dim3(W * 64), 0, s, a);
+// K ranges of the long contraction: enough workgroups for two a CU, 256 k each at least
+int lora_splits(int rows, int k, int rank) {
+  const int tiles = (rows + LORA_TILE - 1) / LORA_TILE * ((rank + 63) / 64);
+  return std::max(1, std::min((512 + tiles - 1) / tiles, (k + 255) / 256));
+}
+template <int DT, bool KM> static hipError_t shrink(const LoraShrink& a, hipStream_t s) {
+  const dim3 grid(a.max_tiles, (a.rank + 63) / 64, a.splits), wg(256);
+  if (a.rank <= 16) hipLaunchKernelGGL((k_lora_shrink<DT, KM, 1>), grid, wg, 0, s, a);
+  else if (a.rank <= 32) hipLaunchKernelGGL((k_lora_shrink<DT, KM, 2>), grid, wg, 0, s, a);
+  else hipLaunchKernelGGL((k_lora_shrink<DT, KM, 4>), grid, wg, 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_lora_parts<DT>), dim3(a.max_tiles), wg, 0, s, a);
   return hipGetLastError();
 }
-template <int DT, bool KM, int MF, int W> static hipError_t shrink_rank(const LoraShrink& a, hipStream_t s) {
-  if (a.rank <= 16) return shrink<DT, KM, MF, 1, W, false>(a, s);
-  if (a.rank <= 32) return shrink<DT, KM, MF, 2, W, false>(a, s);
-  if (a.rank <= 64) return shrink<DT, KM, MF, 4, W, false>(a, s);
-  return shrink<DT, KM, 1, 4, W, true>(a, s);
-}
-template <int DT, bool KM> static hipError_t shrink_rows(int rows, const LoraShrink& a, hipStream_t s) {
-  // more rows a workgroup read the weights less often, where enough workgroups are left
-  if (rows <= 4096) return shrink_rank<DT, KM, 1, 8>(a, s);
-  return shrink_rank<DT, KM, 2, 8>(a, s);
-}
-hipError_t launch_lora_shrink(int dt, bool k_major, int rows, const LoraShrink& a, hipStream_t s) {
-  if (dt == DT_BF16) return k_major ? shrink_rows<DT_BF16, true>(rows, a, s) : shrink_rows<DT_BF16, false>(rows, a, s);
-  if (dt == DT_F16) return k_major ? shrink_rows<DT_F16, true>(rows, a, s) : shrink_rows<DT_F16, false>(rows, a, s);
+hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStream_t s) {
+  if (dt == DT_BF16) return k_major ? shrink<DT_BF16, true>(a, s) : shrink<DT_BF16, false>(a, s);
+  if (dt == DT_F16) return k_major ? shrink<DT_F16, true>(a, s) : shrink<DT_F16, false>(a, s);
   return hipErrorInvalidValue;
 }
 
@@ -791,7 +865,7 @@ hipError_t launch_lora_expand(int dt, bool k_major, const LoraExpand& a, hipStre
 
 template <int DT> static hipError_t grad(const LoraGrad& a, hipStream_t s) {
   const int ti = (a.in + GRAD_COLS - 1) / GRAD_COLS, to = (a.out + GRAD_COLS - 1) / GRAD_COLS;
-  hipLaunchKernelGGL((k_lora_grad<DT>), dim3(a.max_segs, ti + to, (a.rank + 63) / 64), dim3(256), 0, s, a, ti);
+  hipLaunchKernelGGL((k_lora_grad<DT>), dim3(a.max_segs, ti + to, (a.rank + 63) / 64), dim3(GRAD_WG), 0, s, a, ti);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.join) return e;
   const int64_t n = (int64_t)a.rank * (a.in + (int64_t)a.out);
