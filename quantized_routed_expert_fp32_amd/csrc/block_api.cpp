@@ -188,6 +188,7 @@ LoraExpand expand_args(const moe_lora* a, const LoraPlan& p, uint8_t* w, int col
                        int64_t stw, const void* base, int64_t ldbase, void* dst, int64_t lddst) {
   LoraExpand e{};
   e.cols = cols;
+  e.chunk = lora_chunk(a->rows, cols);
   e.rank = a->rank;
   e.rp = p.rp;
   e.adapters = a->adapters;

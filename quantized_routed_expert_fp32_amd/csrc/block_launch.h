@@ -111,6 +111,7 @@ hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStre
 // dst[r] = base[r] + fac[r] (w_i t[r]) (k_major: w_i^T t[r]), cols wide
 struct LoraExpand {
   int cols, rank, rp, adapters;
+  int chunk;                          // columns of a workgroup (lora_chunk)
   const void* w;                      // [adapters, cols, rank]; k-major [adapters, rank, cols]
   const void* base;                   // or null
   void* dst;
@@ -122,6 +123,7 @@ struct LoraExpand {
   const uint16_t* lo;
   const float* fac;
 };
+int lora_chunk(int rows, int cols);
 hipError_t launch_lora_expand(int dt, bool k_major, const LoraExpand& a, hipStream_t s);
 
 // da_i = scale_i sum_r u[r] x[r]^T, db_i = scale_i sum_r dy[r] t[r]^T

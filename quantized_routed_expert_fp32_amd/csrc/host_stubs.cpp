@@ -41,6 +41,7 @@ bool lora_by_row(int rows, int, int, int) { return rows <= 16; }
 hipError_t launch_lora_sort(const LoraSort&, hipStream_t) { return hipErrorNoDevice; }
 int lora_splits(int, int k, int) { return k > 256 ? 2 : 1; }
 hipError_t launch_lora_shrink(int, bool, const LoraShrink&, hipStream_t) { return hipErrorNoDevice; }
+int lora_chunk(int, int) { return 64; }
 hipError_t launch_lora_expand(int, bool, const LoraExpand&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_lora_grad(int, const LoraGrad&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_lora_row(int, const LoraRow&, hipStream_t) { return hipErrorNoDevice; }

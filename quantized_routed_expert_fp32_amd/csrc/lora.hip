@@ -25,6 +25,7 @@
 
 namespace moe {
 
+constexpr int EXP_WGS = 768;           // workgroups of k_lora_expand: three a CU
 constexpr int SORT_WG = 512, SORT_WAVES = SORT_WG / 64, SORT_BINS = 1025;
 
 // ------------------------------------------------------------------- sorting
@@ -234,9 +235,10 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7F800000u ? b : 0;
 }
 
-// 16-bit elements, zero in the place of infinities and NaN: what the low parts meet. A low
-// part of zero, or of the other sign than its high part, would make a NaN of the
-// infinity that the high part's product says.
+// 16-bit elements, zero in the place of infinities and NaN: what the low parts meet where
+// a result is not finite. A low part of zero, or of the other sign than its high part,
+// makes a NaN of the infinity that the high part's product says; so results that are
+// not finite (a look at each) are computed again with these.
 template <int DT> __device__ __forceinline__ u32x4 finite_or_zero(u32x4 v) {
   constexpr uint32_t EXP = DT == DT_BF16 ? 0x7F80 : 0x7C00;
 #pragma unroll
@@ -360,27 +362,26 @@ template <int DT, bool KM, int NF> __global__ __launch_bounds__(256) void k_lora
     }
 }
 
-// A tile's rows, four threads each, four of the rank at a time: the K ranges' sums in
+// 16 of a tile's rows, 16 threads each, four of the rank at a time: the K ranges' sums in
 // order to t, its largest value, then its parts.
 template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink a) {
-  __shared__ uint32_t s_top[LORA_TILE / 16][2];
+  __shared__ uint32_t s_top[4][2];
   const int4 tile = a.tiles[blockIdx.x];
-  if (tile.x < 0) return;
+  if (tile.x < 0 || (int)blockIdx.y * 16 >= tile.z) return;
   const bool none = tile.x == a.adapters;
-  if (threadIdx.x < LORA_TILE / 16 * 2) s_top[threadIdx.x / 2][threadIdx.x % 2] = 0;
-  __syncthreads();
-  const int i = threadIdx.x >> 2, g = (threadIdx.x & 3) * 4, ld = sum_ld(a.rank);
+  const int i = blockIdx.y * 16 + (threadIdx.x >> 4), g = (threadIdx.x & 15) * 4, ld = sum_ld(a.rank);
   const bool in = i < tile.z;
-  const int64_t p = tile.y + i, r = a.perm[tile.y + min(i, tile.z - 1)];
+  const int64_t p = tile.y + min(i, tile.z - 1), r = a.perm[p];
   float* const tr = a.t + r * a.rank;
   uint32_t m = 0, m2 = 0;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};                  // of the last four (up to rank 64 the only ones)
   if (in)
-    for (int j = g; j < a.rank; j += 16) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int j = g; j < a.rank; j += 64) {
+      v = f32x4{0.f, 0.f, 0.f, 0.f};
       if (!none) {
         const float* at = a.part + p * ld + j;
         v = *reinterpret_cast<const f32x4*>(at);
-#pragma unroll 4
+#pragma unroll 8
         for (int z = 1; z < a.splits; ++z) v += *reinterpret_cast<const f32x4*>(at + (int64_t)z * a.places * ld);
       }
 #pragma unroll
@@ -392,48 +393,53 @@ template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink
       }
     }
 #pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
+  for (int d = 1; d < 16; d <<= 1) {
     m = max(m, (uint32_t)__shfl_xor((int)m, d));
     m2 = max(m2, (uint32_t)__shfl_xor((int)m2, d));
   }
   if (a.top) {
-    if (g == 0) {
-      atomicMax(&s_top[i / 16][0], m);             // a maximum: any order
-      atomicMax(&s_top[i / 16][1], m2);
+    uint32_t w0 = m, w1 = m2;
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+      w0 = max(w0, (uint32_t)__shfl_xor((int)w0, d));
+      w1 = max(w1, (uint32_t)__shfl_xor((int)w1, d));
+    }
+    if ((threadIdx.x & 63) == 0) {
+      s_top[threadIdx.x >> 6][0] = w0;
+      s_top[threadIdx.x >> 6][1] = w1;
     }
     __syncthreads();
-    if (threadIdx.x < LORA_TILE / 16) {
-      a.top[tile.w * (LORA_TILE / 16) + threadIdx.x] = s_top[threadIdx.x][0];
-      a.top2[tile.w * (LORA_TILE / 16) + threadIdx.x] = s_top[threadIdx.x][1];
-    }
+    if (threadIdx.x < 2)
+      (threadIdx.x ? a.top2 : a.top)[tile.w * (LORA_TILE / 16) + blockIdx.y] =
+          max(max(s_top[0][threadIdx.x], s_top[1][threadIdx.x]), max(s_top[2][threadIdx.x], s_top[3][threadIdx.x]));
   }
   if (!in || none) return;
   // fp16: |t| below 2^14, in one row's own power of two
   const int e = DT == DT_F16 ? exponent(m) - 14 : 0;
   if (g == 0) a.fac[p] = __builtin_ldexpf(a.scale[tile.x], e);
-  for (int j = g; j < a.rp; j += 16) {
-    float v[4], l[4];
+  for (int j = g; j < a.rp; j += 64) {
+    float h[4], l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[k] = j + k < a.rank ? tr[j + k] : 0.f;     // this thread's own stores
-      if constexpr (DT == DT_F16) v[k] = __builtin_ldexpf(v[k], -e);
-      l[k] = low_part<DT>(v[k]);
+      // (beyond rank 64: this thread's own stores)
+      h[k] = j + k >= a.rank ? 0.f : a.rank <= 64 ? v[k] : tr[j + k];
+      if constexpr (DT == DT_F16) h[k] = __builtin_ldexpf(h[k], -e);
+      l[k] = low_part<DT>(h[k]);
     }
-    *reinterpret_cast<uint2*>(a.hi + p * a.rp + j) = make_uint2(to16<DT>(v[0]) | (uint32_t)to16<DT>(v[1]) << 16,
-                                                                to16<DT>(v[2]) | (uint32_t)to16<DT>(v[3]) << 16);
+    *reinterpret_cast<uint2*>(a.hi + p * a.rp + j) = make_uint2(to16<DT>(h[0]) | (uint32_t)to16<DT>(h[1]) << 16,
+                                                                to16<DT>(h[2]) | (uint32_t)to16<DT>(h[3]) << 16);
     *reinterpret_cast<uint2*>(a.lo + p * a.rp + j) = make_uint2(to16<DT>(l[0]) | (uint32_t)to16<DT>(l[1]) << 16,
                                                                 to16<DT>(l[2]) | (uint32_t)to16<DT>(l[3]) << 16);
   }
 }
 
 // ------------------------------------------------------------------- expand
-// A workgroup of four waves: a tile's rows, EXP_COLS columns of the result, a wave
+// A workgroup of four waves: a tile's rows, `chunk` columns of the result, a wave
 // 32 rows x 32 columns at a time, the next columns' loads in flight. The weights' rows
 // are dealt to the fragments so that a lane ends with 8 consecutive columns of a row
 // (fragment f, place m: column 8 (m / 4) + 4 f + m % 4): base and result move 16 bytes a
 // lane, 64 a row. KB: blocks of 32 of the rank whose parts stay in registers (0: any
 // rank, read each time).
-constexpr int EXP_COLS = 256;
 template <int DT, bool KM, int KB>
 __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
   constexpr int MF = 2, F = 2, KU = KB ? KB : 1, SROW = 80;
@@ -447,11 +453,18 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
   const bool none = tile.x == a.adapters;
   const uint16_t* wi = static_cast<const uint16_t*>(a.w) + (none ? 0 : tile.x * a.stw);
   uint8_t* const stage = area + (KM ? w * (KU * 32 * SROW) : 0);
-  int64_t row[MF], at[MF];
+  // the lane's rows: their places, and where its columns of them lie
+  int64_t at[MF];
+  const uint16_t* bp[MF];
+  uint16_t* dp[MF];
+  bool in[MF];
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
+    in[m] = m0 + m * 16 + col < tile.z;
     at[m] = tile.y + min(m0 + m * 16 + col, tile.z - 1);
-    row[m] = a.perm[at[m]];
+    const int64_t r = a.perm[at[m]];
+    bp[m] = static_cast<const uint16_t*>(a.base) + r * a.ldbase + quad * 8;
+    dp[m] = static_cast<uint16_t*>(a.dst) + r * a.lddst + quad * 8;
   }
   u32x4 th[KU][MF], tl[KU][MF];
   auto parts = [&](int k, u32x4* h, u32x4* l) {
@@ -461,7 +474,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
       l[m] = *reinterpret_cast<const u32x4*>(a.lo + at[m] * a.rp + k * 32 + quad * 8);
     }
   };
-  float fac[MF];
+  float fac[MF] = {};
   if (!none) {
 #pragma unroll
     for (int m = 0; m < MF; ++m) fac[m] = a.fac[at[m]];
@@ -469,8 +482,19 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
 #pragma unroll
       for (int k = 0; k < KB; ++k) parts(k, th[k], tl[k]);
   }
-  // weights of k block k: NT rows of the lane's columns; k-major 32 k rows of 4 chunks
-  auto weights = [&](int c0, int k, u32x4* v) {
+  // Weights of k block k: NT rows of the lane's columns; k-major 32 k rows of 4
+  // chunks. `whole`: nothing of what the wave loads lies behind its rows' ends.
+  const uint16_t* wp[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+    wp[f] = KM ? wi + (f * 16 + lane / 4) * a.ldw + lane % 4 * 8 : wi + ((col >> 2) * 8 + f * 4 + (col & 3)) * a.ldw + quad * 8;
+  auto weights = [&](bool whole, int c0, int k, u32x4* v) {
+    const int64_t off = KM ? (int64_t)k * 32 * a.ldw + c0 : (int64_t)c0 * a.ldw + k * 32;
+    if (whole) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) __builtin_memcpy(&v[f], wp[f] + off, 16);
+      return;
+    }
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       if constexpr (!KM) {
@@ -487,21 +511,29 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
     u32x4 w[KU][F], b[MF];
   };
   auto load = [&](Cols& s, int c0) {
+    const bool inside = c0 + 32 <= a.cols, whole = inside && a.rank % 32 == 0;
     if constexpr (KB > 0)
       if (!none)
 #pragma unroll
-        for (int k = 0; k < KB; ++k) weights(c0, k, s.w[k]);
-    const int c = c0 + quad * 8;
+        for (int k = 0; k < KB; ++k) weights(whole, c0, k, s.w[k]);
+    if (!a.base) {
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      s.b[m] = u32x4{0, 0, 0, 0};
-      if (a.base && c < a.cols)
-        s.b[m] = load_chunk<2, true>(static_cast<const uint16_t*>(a.base) + row[m] * a.ldbase, (int64_t)c * 2, (int64_t)a.cols * 2);
+      for (int m = 0; m < MF; ++m) s.b[m] = u32x4{0, 0, 0, 0};
+    } else if (inside) {
+#pragma unroll
+      for (int m = 0; m < MF; ++m) __builtin_memcpy(&s.b[m], bp[m] + c0, 16);
+    } else {
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        s.b[m] = u32x4{0, 0, 0, 0};
+        if (c0 + quad * 8 < a.cols)
+          s.b[m] = load_chunk<2, true>(bp[m] - quad * 8, (int64_t)(c0 + quad * 8) * 2, (int64_t)a.cols * 2);
+      }
     }
   };
   // tiles start with different columns, so that neighbours read different weights
-  const int y = (int)((blockIdx.y + (uint32_t)tile.w) % gridDim.y), c_end = min(a.cols, (y + 1) * EXP_COLS);
-  int c0 = y * EXP_COLS + (w >> 1) * 32;
+  const int y = (int)((blockIdx.y + (uint32_t)tile.w) % gridDim.y), c_end = min(a.cols, (y + 1) * a.chunk);
+  int c0 = y * a.chunk + (w >> 1) * 32;
   Cols next;
   if (c0 < c_end) load(next, c0);
 #pragma unroll 1
@@ -509,17 +541,18 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
     Cols cur = next;
     if (c0 + 64 < c_end) load(next, c0 + 64);
     f32x4 acc[F][MF];
+    // safe: low parts meet zeros where the weights are not finite
+    auto multiply = [&](bool safe) {
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int m = 0; m < MF; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (!none) {
+        for (int m = 0; m < MF; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < (KB ? KB : 8); ++k) {
         if (!KB && k * 32 >= a.rp) break;
         const int ku = KB ? k : 0;
         if constexpr (KB == 0) {
-          weights(c0, k, cur.w[0]);
+          weights(c0 + 32 <= a.cols && a.rank % 32 == 0, c0, k, cur.w[0]);
           parts(k, th[0], tl[0]);
         }
         u32x4 p[F];
@@ -540,41 +573,54 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
         for (int f = 0; f < F; ++f) {
 #pragma unroll
           for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(p[f], th[ku][m], acc[f][m]);
-          const u32x4 z = finite_or_zero<DT>(p[f]);
+          if (safe) p[f] = finite_or_zero<DT>(p[f]);
 #pragma unroll
-          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(z, tl[ku][m], acc[f][m]);
+          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(p[f], tl[ku][m], acc[f][m]);
         }
       }
+    };
+    if (!none) {
+      multiply(false);
+      float far = 0.f;
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) far = __builtin_fmaf(0.f, acc[f][m][e], far);
+      if (__any(far != 0.f)) multiply(true);
     }
     const int c = c0 + quad * 8;
-    if (c >= a.cols) continue;
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
-      if (m0 + m * 16 + col >= tile.z) continue;
       float v[8];
       unpack16<DT>(cur.b[m], v);
       if (!none)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += fac[m] * acc[e / 4][m][e % 4];
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(fac[m], acc[e / 4][m][e % 4], v[e]);
       const u32x4 o = pack16<DT>(v);
-      uint16_t* to = static_cast<uint16_t*>(a.dst) + row[m] * a.lddst + c;
-      if (c + 8 <= a.cols) __builtin_memcpy(to, &o, 16);      // at any alignment
+      if (!in[m]) continue;
+      if (c + 8 <= a.cols) __builtin_memcpy(dp[m] + c0, &o, 16);      // at any alignment
       else
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (c + e < a.cols) to[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+          if (c + e < a.cols) dp[m][c0 + e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
     }
   }
 }
 
 // ---------------------------------------------------------------- gradients
-// A workgroup of eight waves: 64 of the rank x 256 columns of one segment's sums over
-// its rows, 64 rows a step: the 16-bit rows and the parts of the fp32 ones go through
-// LDS (the next step's on their way in registers, the places of the one after that
-// too), both read transposed. da's lanes end with 8 consecutive columns of a rank
-// row, db's with 16 consecutive ranks of a column's row: the operands change places.
-constexpr int GRAD_WG = 512, GRAD_COLS = 256, GRAD_ROWS = 64;
-constexpr int GRAD_XROW = GRAD_COLS * 2 + 16, GRAD_TROW = 128 + 16;      // bytes in LDS
+// A workgroup of four waves: 64 of the rank x 256 columns of one segment's sums over
+// its rows (a wave 64 x 64), 64 rows a step: the 16-bit rows and the parts of the fp32
+// ones go through LDS (the next step's on their way in registers, the places of the
+// one after that too), both read transposed; a row's 32-byte pieces are moved about so
+// that the 8 rows that 32 lanes read together meet different banks. da's lanes end with
+// 4 consecutive columns of a rank row, db's with 4 ranks of a column's row: the
+// operands change places.
+constexpr int GRAD_WG = 256, GRAD_COLS = 256, GRAD_ROWS = 64;
+constexpr int GRAD_XROW = GRAD_COLS * 2, GRAD_TROW = 128;      // bytes in LDS
+__device__ __forceinline__ int swz_x(int k) { return (k & 3) | (k >> 3 & 1) << 2; }
+__device__ __forceinline__ int swz_t(int k) { return (k >> 1 & 1) | (k >> 3 & 1) << 1; }
 template <int DT, bool DB>
 __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot, int j0, int c0, uint8_t* sx, uint8_t* st,
                                           uint32_t* s_top, int (*s_perm)[GRAD_ROWS]) {
@@ -585,7 +631,6 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
   const uint16_t* xp = static_cast<const uint16_t*>(DB ? a.dy : a.x);
   const int64_t ld = DB ? a.lddy : a.ldx;
   auto place = [&](int i) { return i < seg.z ? a.perm[seg.y + i] : -1; };
-  if (threadIdx.x < 2 * GRAD_ROWS) s_perm[threadIdx.x / GRAD_ROWS][threadIdx.x % GRAD_ROWS] = place(threadIdx.x);
   int e = 0;                                       // fp16: parts are |t| 2^-e, below 2^14
   if constexpr (DT == DT_F16) {
     const uint32_t* top = (DB ? a.top_t : a.top_u) + seg.w * (LORA_TILE / 16);
@@ -599,132 +644,141 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
     for (int i = 0; i < GRAD_WG / 64; ++i) m = max(m, s_top[i]);
     e = exponent(m) - 14;
   }
-  __syncthreads();
-  // x: 32 chunks a row, 16 rows at a time; t: 8 threads a row, 8 of the rank each
-  const int xr = threadIdx.x >> 5, xc = threadIdx.x & 31, tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
-  u32x4 xv[4];
-  float tv[8];
+  // x: 32 chunks a row, 8 rows at a time; t: 4 threads a row, 16 of the rank each
+  const int xr = threadIdx.x >> 5, xc = threadIdx.x & 31, tr = threadIdx.x >> 2, tc = threadIdx.x & 3;
+  u32x4 xv[8];
+  float tv[16];
   int next = -1;
-  auto load = [&](const int* perm) {
-    int r[4];
+  // whether nothing of what the workgroup loads lies behind its rows' ends
+  const bool whole = c0 + GRAD_COLS <= cols && j0 + 64 <= a.rank;
+  auto load = [&](const int* perm, int left) {
+    if (whole && left >= GRAD_ROWS) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = perm[xr + i * 16];
-    const int rt = perm[tr];
+      for (int i = 0; i < 8; ++i) __builtin_memcpy(&xv[i], xp + perm[xr + i * 8] * ld + (c0 + xc * 8), 16);
+      const float* t = tp + (int64_t)perm[tr] * a.rank + (j0 + tc * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xv[i] = u32x4{0, 0, 0, 0};
-      if (r[i] >= 0 && c0 + xc * 8 < cols)
-        xv[i] = load_chunk<2, true>(xp + r[i] * ld, (int64_t)(c0 + xc * 8) * 2, (int64_t)cols * 2);
+      for (int i = 0; i < 4; ++i) __builtin_memcpy(tv + i * 4, t + i * 4, 16);
+      return;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 8; ++i) {
+      const int r = perm[xr + i * 8];
+      xv[i] = u32x4{0, 0, 0, 0};
+      if (r >= 0 && c0 + xc * 8 < cols) xv[i] = load_chunk<2, true>(xp + r * ld, (int64_t)(c0 + xc * 8) * 2, (int64_t)cols * 2);
+    }
+    const int r = perm[tr];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       u32x4 v = {0, 0, 0, 0};
-      if (rt >= 0 && j0 + tc + i * 4 < a.rank)
-        v = load_chunk<4>(tp + (int64_t)rt * a.rank, (int64_t)(j0 + tc + i * 4) * 4, (int64_t)a.rank * 4);
+      if (r >= 0 && j0 + tc * 16 + i * 4 < a.rank)
+        v = load_chunk<4>(tp + (int64_t)r * a.rank, (int64_t)(j0 + tc * 16 + i * 4) * 4, (int64_t)a.rank * 4);
       unpack16<DT_F32>(v, tv + i * 4);
     }
   };
-  f32x4 acc[2][4];                                 // [x fragment][t fragment]
+  f32x4 acc[4][4];                                 // [x fragment][t fragment]
+  auto rows = [&](bool safe) {
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 4; ++f)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (seg.z > 0) load(s_perm[0]);
-  for (int i0 = 0, step = 0; i0 < seg.z; i0 += GRAD_ROWS, ++step) {
-    __syncthreads();                               // the last step's readers are done
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4*>(sx + (xr + i * 16) * XROW + xc * 16) = xv[i];
-    float low[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (DT == DT_F16) tv[i] = __builtin_ldexpf(tv[i], -e);
-      low[i] = low_part<DT>(tv[i]);
-    }
-    uint8_t* h = st + tr * TROW + tc * 2;
-    *reinterpret_cast<u32x4*>(h) = pack16<DT>(tv);
-    *reinterpret_cast<u32x4*>(h + GRAD_ROWS * TROW) = pack16<DT>(low);
-    if (step && threadIdx.x < GRAD_ROWS) s_perm[(step + 1) & 1][threadIdx.x] = next;
+      for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (threadIdx.x < 2 * GRAD_ROWS) s_perm[threadIdx.x / GRAD_ROWS][threadIdx.x % GRAD_ROWS] = place(threadIdx.x);
     __syncthreads();
-    if (threadIdx.x < GRAD_ROWS) next = place(i0 + 2 * GRAD_ROWS + threadIdx.x);
-    if (i0 + GRAD_ROWS < seg.z) load(s_perm[(step + 1) & 1]);
+    if (seg.z > 0) load(s_perm[0], seg.z);
+    for (int i0 = 0, step = 0; i0 < seg.z; i0 += GRAD_ROWS, ++step) {
+      __syncthreads();                             // the last step's readers are done
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int kr = k * 32 + quad * 8 + (col >> 2);
-      u32x4 x[2], z[2];
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        x[f] = read_tr(sx + kr * XROW + w * 64 + (DB ? f * 32 + (col & 3) * 8 : (col & 3) * 16 + f * 8), 4 * XROW);
-        z[f] = finite_or_zero<DT>(x[f]);
+      for (int i = 0; i < 8; ++i) {
+        const int k = xr + i * 8;
+        *reinterpret_cast<u32x4*>(sx + k * XROW + ((xc >> 1) ^ swz_x(k)) * 32 + (xc & 1) * 16) = xv[i];
       }
+      float low[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* at = st + kr * TROW + (DB ? (col & 3) * 32 + j * 8 : j * 32 + (col & 3) * 8);
-        const u32x4 th = read_tr(at, 4 * TROW), tl = read_tr(at + GRAD_ROWS * TROW, 4 * TROW);
+      for (int i = 0; i < 16; ++i) {
+        if constexpr (DT == DT_F16) tv[i] = __builtin_ldexpf(tv[i], -e);
+        low[i] = safe ? low_part<DT>(tv[i]) : tv[i] - Row<DT>::f(to16<DT>(tv[i]));
+      }
+      uint8_t* h = st + tr * TROW + (tc ^ swz_t(tr)) * 32;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          acc[f][j] = DB ? Elem<DT>::mma16(th, x[f], acc[f][j]) : Elem<DT>::mma16(x[f], th, acc[f][j]);
-          acc[f][j] = DB ? Elem<DT>::mma16(tl, z[f], acc[f][j]) : Elem<DT>::mma16(z[f], tl, acc[f][j]);
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<u32x4*>(h + i * 16) = pack16<DT>(tv + i * 8);
+        *reinterpret_cast<u32x4*>(h + GRAD_ROWS * TROW + i * 16) = pack16<DT>(low + i * 8);
+      }
+      if (step && threadIdx.x < GRAD_ROWS) s_perm[(step + 1) & 1][threadIdx.x] = next;
+      __syncthreads();
+      if (threadIdx.x < GRAD_ROWS) next = place(i0 + 2 * GRAD_ROWS + threadIdx.x);
+      if (i0 + GRAD_ROWS < seg.z) load(s_perm[(step + 1) & 1], seg.z - i0 - GRAD_ROWS);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kr = k * 32 + quad * 8 + (col >> 2);         // kr + 4: the same pieces
+        u32x4 x[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) x[f] = read_tr(sx + kr * XROW + ((w * 4 + f) ^ swz_x(kr)) * 32 + (col & 3) * 8, 4 * XROW);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {              // the high parts, then the low ones
+          if (p && safe)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) x[f] = finite_or_zero<DT>(x[f]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4 t = read_tr(st + (p * GRAD_ROWS + kr) * TROW + (j ^ swz_t(kr)) * 32 + (col & 3) * 8, 4 * TROW);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) acc[f][j] = DB ? Elem<DT>::mma16(t, x[f], acc[f][j]) : Elem<DT>::mma16(x[f], t, acc[f][j]);
+          }
         }
       }
     }
-  }
+    __syncthreads();
+  };
+  rows(false);
+  float far = 0.f;
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) far = __builtin_fmaf(0.f, acc[f][j][q], far);
+  if (__syncthreads_or(far != 0.f)) rows(true);
   const float scale = a.scale[seg.x];
-  auto value = [&](int f, int j, int q) {
-    return DT == DT_F16 ? __builtin_ldexpf(acc[f][j][q], e) : acc[f][j][q];
-  };
-  // N consecutive values of a row of the result, from column c on of n: rounded, or
-  // (one of several segments) as they are
+  // four consecutive values of a row of the result, n long, from column c on: rounded,
+  // or (one of several segments) as they are
   const int64_t size = (int64_t)a.rank * cols;
-  float* part = slot < 0 ? nullptr : a.part + (int64_t)slot * a.rank * (a.in + a.out) + (DB ? (int64_t)a.rank * a.in : 0);
+  float* part = slot < 0 ? nullptr : a.part + (int64_t)slot * a.rank * (a.in + (int64_t)a.out) + (DB ? (int64_t)a.rank * a.in : 0);
   uint16_t* out = static_cast<uint16_t*>(DB ? a.db : a.da) + seg.x * size;
-  auto put8 = [&](int64_t row, int c, int n, const float* v) {
-    const int64_t at = row * n + c;
-    if (part) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) part[at + i] = v[i];
-      return;
-    }
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = scale * v[i];
-    const u32x4 o = pack16<DT>(s);
-    if (c + 8 <= n) __builtin_memcpy(out + at, &o, 16);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) out[at + i] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
-  };
-  if constexpr (!DB) {
-    const int c = c0 + w * 32 + quad * 8;
+  for (int f = 0; f < 4; ++f)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int rk = j0 + j * 16 + col;
-      if (rk >= a.rank || c >= cols) continue;
-      float v[8];
+      const int n = DB ? a.rank : cols;
+      const int row = DB ? c0 + w * 64 + f * 16 + col : j0 + j * 16 + col;
+      const int c = DB ? j0 + j * 16 + quad * 4 : c0 + w * 64 + f * 16 + quad * 4;
+      if (row >= (DB ? cols : a.rank) || c >= n) continue;
+      float v[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = value(q / 4, j, q % 4);
-      put8(rk, c, cols, v);
-    }
-  } else {
+      for (int q = 0; q < 4; ++q) {
+        v[q] = DT == DT_F16 ? __builtin_ldexpf(acc[f][j][q], e) : acc[f][j][q];
+        if (!part) v[q] *= scale;
+      }
+      const int64_t at = (int64_t)row * n + c;
+      if (part) {
+        if (c + 4 <= n) __builtin_memcpy(part + at, v, 16);    // at any alignment
+        else
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int c = c0 + w * 32 + f * 16 + col;
-      if (c >= cols) continue;
+          for (int q = 0; q < 4; ++q)
+            if (c + q < n) part[at + q] = v[q];
+      } else {
+        uint16_t b[4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int rk = j0 + quad * 16 + p * 8;
-        if (rk >= a.rank) continue;
-        float v[8];
+        for (int q = 0; q < 4; ++q) b[q] = to16<DT>(v[q]);
+        if (c + 4 <= n) __builtin_memcpy(out + at, b, 8);
+        else
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = value(f, p * 2 + q / 4, q % 4);
-        put8(c, rk, a.rank, v);
+          for (int q = 0; q < 4; ++q)
+            if (c + q < n) out[at + q] = b[q];
       }
     }
-  }
 }
-template <int DT> __global__ __launch_bounds__(GRAD_WG) void k_lora_grad(LoraGrad a, int in_tiles) {
-  __shared__ __align__(16) uint8_t sx[GRAD_ROWS * GRAD_XROW], st[2 * GRAD_ROWS * GRAD_TROW];
+template <int DT> __global__ __launch_bounds__(GRAD_WG, 2) void k_lora_grad(LoraGrad a, int in_tiles) {
+  __shared__ __align__(64) uint8_t sx[GRAD_ROWS * GRAD_XROW], st[2 * GRAD_ROWS * GRAD_TROW];
   __shared__ uint32_t s_top[GRAD_WG / 64];
   __shared__ int s_perm[2][GRAD_ROWS];
   const int4 seg = a.segs[blockIdx.x];
@@ -733,18 +787,38 @@ template <int DT> __global__ __launch_bounds__(GRAD_WG) void k_lora_grad(LoraGra
   if ((int)blockIdx.y < in_tiles) lora_grad<DT, false>(a, seg, slot, j0, blockIdx.y * GRAD_COLS, sx, st, s_top, s_perm);
   else lora_grad<DT, true>(a, seg, slot, j0, (blockIdx.y - in_tiles) * GRAD_COLS, sx, st, s_top, s_perm);
 }
-// the sums of adapters of several segments, in order
+// the sums of adapters of several segments, in order, four a thread
 template <int DT> __global__ __launch_bounds__(256) void k_lora_join(LoraGrad a) {
   const int2 span = a.span[blockIdx.y];
   if (!span.y) return;
-  const int64_t na = (int64_t)a.rank * a.in, nb = (int64_t)a.rank * a.out, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= na + nb) return;
-  const float* p = a.part + span.x * (na + nb) + i;
-  float v = p[0];
-  for (int s = 1; s < span.y; ++s) v += p[s * (na + nb)];
-  const uint16_t o = to16<DT>(a.scale[blockIdx.y] * v);
-  if (i < na) static_cast<uint16_t*>(a.da)[blockIdx.y * na + i] = o;
-  else static_cast<uint16_t*>(a.db)[blockIdx.y * nb + i - na] = o;
+  const int64_t na = (int64_t)a.rank * a.in, n = na + (int64_t)a.rank * a.out;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float* p = a.part + span.x * n + i;
+  const int m = (int)min(n - i, (int64_t)4);
+  float v[4] = {};
+  if (m == 4) {
+#pragma unroll 4
+    for (int s = 0; s < span.y; ++s) {
+      float f[4];
+      __builtin_memcpy(f, p + s * n, 16);          // at any alignment
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = s ? v[e] + f[e] : f[e];
+    }
+  } else {
+    for (int e = 0; e < m; ++e) {
+      v[e] = p[e];
+      for (int s = 1; s < span.y; ++s) v[e] += p[s * n + e];
+    }
+  }
+  const float scale = a.scale[blockIdx.y];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t k = i + e;
+    if (k >= n) continue;
+    if (k < na) static_cast<uint16_t*>(a.da)[blockIdx.y * na + k] = to16<DT>(scale * v[e]);
+    else static_cast<uint16_t*>(a.db)[blockIdx.y * (n - na) + k - na] = to16<DT>(scale * v[e]);
+  }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -841,7 +915,7 @@ template <int DT, bool KM> static hipError_t shrink(const LoraShrink& a, hipStre
   else hipLaunchKernelGGL((k_lora_shrink<DT, KM, 4>), grid, wg, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_lora_parts<DT>), dim3(a.max_tiles), wg, 0, s, a);
+  hipLaunchKernelGGL((k_lora_parts<DT>), dim3(a.max_tiles, LORA_TILE / 16), wg, 0, s, a);
   return hipGetLastError();
 }
 hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStream_t s) {
@@ -851,11 +925,16 @@ hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStre
 }
 
 template <int DT, bool KM> static hipError_t expand(const LoraExpand& a, hipStream_t s) {
-  const dim3 grid(a.max_tiles, (a.cols + EXP_COLS - 1) / EXP_COLS);
+  const dim3 grid(a.max_tiles, (a.cols + a.chunk - 1) / a.chunk);
   if (a.rp == 32) hipLaunchKernelGGL((k_lora_expand<DT, KM, 1>), grid, dim3(256), 0, s, a);
   else if (a.rp == 64) hipLaunchKernelGGL((k_lora_expand<DT, KM, 2>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_lora_expand<DT, KM, 0>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
+}
+// Columns of a workgroup: as few as leave three workgroups a CU
+int lora_chunk(int rows, int cols) {
+  const int64_t tiles = (rows + LORA_TILE - 1) / LORA_TILE;
+  return (int)((cols * tiles / EXP_WGS + 63) / 64 + (cols * tiles < EXP_WGS)) * 64;
 }
 hipError_t launch_lora_expand(int dt, bool k_major, const LoraExpand& a, hipStream_t s) {
   if (dt == DT_BF16) return k_major ? expand<DT_BF16, true>(a, s) : expand<DT_BF16, false>(a, s);
@@ -869,7 +948,7 @@ template <int DT> static hipError_t grad(const LoraGrad& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.join) return e;
   const int64_t n = (int64_t)a.rank * (a.in + (int64_t)a.out);
-  hipLaunchKernelGGL((k_lora_join<DT>), dim3((uint32_t)((n + 255) / 256), a.adapters), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_lora_join<DT>), dim3((uint32_t)((n + 1023) / 1024), a.adapters), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 hipError_t launch_lora_grad(int dt, const LoraGrad& a, hipStream_t s) {
