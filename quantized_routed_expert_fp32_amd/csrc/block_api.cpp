@@ -96,7 +96,7 @@ int check_lora(const char* fn, const moe_lora* a) {
 
 struct LoraPlan {
   int rp, blocks, max_tiles, splits, seg_rows, max_segs, slots;
-  uint64_t hist_off, perm_off, tiles_off, hi_off, lo_off, fac_off, sums_off, segs_off, slot_off, span_off, u_off, top_off, part_off,
+  uint64_t hist_off, tiles_off, rows_off, hi_off, lo_off, fac_off, sums_off, segs_off, slot_off, span_off, u_off, top_off, part_off,
       total;
 };
 
@@ -108,11 +108,11 @@ LoraPlan plan_lora(const moe_lora* a, bool backward, bool dw) {
   p.rp = (int)up(a->rank, 32);
   p.blocks = (a->rows + LORA_SORT - 1) / LORA_SORT;
   // an adapter's last tile may be short
-  p.max_tiles = (int)up(a->rows / LORA_TILE + std::min(a->adapters + 1, a->rows), 8);
+  p.max_tiles = a->rows / LORA_TILE + std::min(a->adapters + 1, a->rows);
   Bump b;
   p.hist_off = b.take(p.blocks > 1 ? (uint64_t)p.blocks * (a->adapters + 1) * 4 : 0);
-  p.perm_off = b.take(R * 4);
   p.tiles_off = b.take((uint64_t)p.max_tiles * 16);
+  p.rows_off = b.take((uint64_t)p.max_tiles * LORA_TILE * 4);
   p.hi_off = b.take(R * p.rp * 2);
   p.lo_off = b.take(R * p.rp * 2);
   p.fac_off = b.take(R * 4);
@@ -127,7 +127,7 @@ LoraPlan plan_lora(const moe_lora* a, bool backward, bool dw) {
     // adapter's; every segment more costs its adapter's sums another trip through memory.
     const int64_t tiles = ((a->in + 255) / 256 + (a->out + 255) / 256) * (int64_t)((a->rank + 63) / 64);
     p.seg_rows = (int)std::max<int64_t>(up((a->rows * tiles + 511) / 512, LORA_TILE), 256);
-    p.max_segs = (int)up(a->rows / p.seg_rows + a->adapters, 8);
+    p.max_segs = a->rows / p.seg_rows + a->adapters;
     // only adapters of several segments have slots: m segments hold over (m - 1) seg_rows >= m / 2 seg_rows rows
     p.slots = 2 * (a->rows / p.seg_rows);
     p.segs_off = b.take((uint64_t)p.max_segs * 16);
@@ -146,9 +146,9 @@ LoraSort sort_args(const moe_lora* a, const LoraPlan& p, uint8_t* w) {
   s.ids = a->ids;
   s.blocks = p.blocks;
   s.hist = reinterpret_cast<int*>(w + p.hist_off);
-  s.perm = reinterpret_cast<int*>(w + p.perm_off);
   s.tiles = reinterpret_cast<int4*>(w + p.tiles_off);
   s.max_tiles = p.max_tiles;
+  s.tile_rows = reinterpret_cast<int*>(w + p.rows_off);
   s.seg_rows = p.seg_rows;
   s.max_segs = p.max_segs;
   s.segs = reinterpret_cast<int4*>(w + p.segs_off);
@@ -171,7 +171,7 @@ LoraShrink shrink_args(const moe_lora* a, const LoraPlan& p, uint8_t* w, int k, 
   s.ldw = ldw;
   s.stw = stw;
   s.scale = a->scale;
-  s.perm = reinterpret_cast<const int*>(w + p.perm_off);
+  s.rows = reinterpret_cast<const int*>(w + p.rows_off);
   s.tiles = reinterpret_cast<const int4*>(w + p.tiles_off);
   s.max_tiles = p.max_tiles;
   s.splits = p.splits;
@@ -199,7 +199,7 @@ LoraExpand expand_args(const moe_lora* a, const LoraPlan& p, uint8_t* w, int col
   e.ldbase = ldbase;
   e.dst = dst;
   e.lddst = lddst;
-  e.perm = reinterpret_cast<const int*>(w + p.perm_off);
+  e.rows = reinterpret_cast<const int*>(w + p.rows_off);
   e.tiles = reinterpret_cast<const int4*>(w + p.tiles_off);
   e.max_tiles = p.max_tiles;
   e.hi = reinterpret_cast<const uint16_t*>(w + p.hi_off);
@@ -444,7 +444,7 @@ int moe_lora_backward(const moe_lora* a, const void* dy, int64_t lddy, const flo
     g.dy = dy;
     g.lddy = lddy;
     g.scale = a->scale;
-    g.perm = k.perm;
+    g.rows = k.rows;
     g.segs = reinterpret_cast<const int4*>(w + p.segs_off);
     g.slot = reinterpret_cast<const int*>(w + p.slot_off);
     g.span = reinterpret_cast<const int2*>(w + p.span_off);

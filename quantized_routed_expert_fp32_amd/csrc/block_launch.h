@@ -70,11 +70,11 @@ struct LoraSort {
   const int32_t* ids;
   int blocks;                         // sorting workgroups
   int* hist;                          // [blocks, adapters + 1], blocks > 1
-  int* perm;                          // [rows]
-  int4* tiles;                        // [max_tiles]: adapter (-1: none left), first place in perm, rows, number
-  int max_tiles;                      // a multiple of 8
+  int4* tiles;                        // [max_tiles]: adapter (-1: none left), first place in the order, rows, number
+  int max_tiles;
+  int* tile_rows;                     // [max_tiles, LORA_TILE]: the rows of each (its last one again behind them)
   // gradients (seg_rows = 0: none): every adapter has a segment at least
-  int seg_rows, max_segs;             // multiples of LORA_TILE and of 8
+  int seg_rows, max_segs;             // (a multiple of LORA_TILE)
   int4* segs;                         // [max_segs]: adapter (-1), first place, rows, first tile
   int* slot;                          // [max_segs]: where its partial sums go, -1: it is its adapter's only one
   int2* span;                         // [adapters]: first slot, segments (0: one)
@@ -88,14 +88,14 @@ struct LoraShrink {
   const void* w;                      // [adapters, rank, k]; k-major [adapters, k, rank]
   int64_t ldsrc, ldw, stw;
   const float* scale;
-  const int* perm;
+  const int* rows;                    // LoraSort's tile_rows
   const int4* tiles;
   int max_tiles;
   int splits;                         // K ranges (lora_splits)
   float* part;                        // [splits, places, rank to a multiple of 4] sums
   int64_t places;                     // rows
   float* t;                           // fp32 [rows, rank]
-  // by place in perm:
+  // by place in the order:
   uint16_t* hi;                       // [rows, rp] parts of t over a power of two a row (zero behind rank)
   uint16_t* lo;
   float* fac;                         // [rows] scale times that power
@@ -116,7 +116,7 @@ struct LoraExpand {
   const void* base;                   // or null
   void* dst;
   int64_t ldw, stw, ldbase, lddst;
-  const int* perm;
+  const int* rows;
   const int4* tiles;
   int max_tiles;
   const uint16_t* hi;
@@ -135,7 +135,7 @@ struct LoraGrad {
   const void* dy;
   int64_t ldx, lddy;
   const float* scale;
-  const int* perm;
+  const int* rows;                    // tile_rows
   const int4* segs;
   const int* slot;
   const int2* span;

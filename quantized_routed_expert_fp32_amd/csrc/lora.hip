@@ -25,8 +25,8 @@
 
 namespace moe {
 
-constexpr int EXP_WGS = 768;           // workgroups of k_lora_expand: three a CU
-constexpr int SORT_WG = 512, SORT_WAVES = SORT_WG / 64, SORT_BINS = 1025;
+constexpr int EXP_WGS = 1024;          // workgroups of k_lora_expand: four a CU
+constexpr int SORT_WG = 1024, SORT_WAVES = SORT_WG / 64, SORT_BINS = 1025;
 
 // ------------------------------------------------------------------- sorting
 __device__ __forceinline__ int bin_of(int id, int adapters) { return (uint32_t)id < (uint32_t)adapters ? id : adapters; }
@@ -83,13 +83,13 @@ __device__ __forceinline__ Scan4 scan(Scan4 x, Scan4* wave_sum) {
 
 // A stable counting sort, 8192 rows a workgroup: counts a wave in LDS, their
 // prefix sums, then each wave places its rows. Lanes of the same adapter find each
-// other by ballots over the id's bits: runs of one adapter would queue at an LDS atomic
-// (8192 rows in runs: SORT_TIME).
+// other by ballots over the id's bits: runs of one adapter would queue at an LDS
+// atomic. One workgroup's latency: 9 us for 777 rows, 13 for 8192.
 __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
   constexpr int PER = LORA_SORT / SORT_WG;      // steps of a wave
   constexpr int BPT = (SORT_BINS + SORT_WG - 1) / SORT_WG;
-  __shared__ int cnt[SORT_WAVES][SORT_BINS];
-  __shared__ int off[SORT_BINS + 1], tile[SORT_BINS + 1], seg[SORT_BINS + 1], slot[SORT_BINS + 1];
+  __shared__ uint16_t cnt[SORT_WAVES][SORT_BINS];   // a wave's counts, then its first places in the workgroup
+  __shared__ int off[SORT_BINS + 1], tile[SORT_BINS + 1], seg[SORT_BINS + 1], slot[SORT_BINS + 1], first[SORT_BINS];
   __shared__ Scan4 wave_sum[SORT_WAVES];
   const int bins = a.adapters + 1, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   for (int b = threadIdx.x; b < bins; b += SORT_WG)
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     if (id[s] >= 0) {
       const int n = cnt[w][id[s]];
       asm volatile("" ::: "memory");             // every lane has read: LDS runs in order
-      if (local[s] == 0) cnt[w][id[s]] = n + __popcll(m);
+      if (local[s] == 0) cnt[w][id[s]] = (uint16_t)(n + __popcll(m));
       local[s] += n;
     }
     asm volatile("" ::: "memory");
@@ -150,10 +150,11 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     tile[b] = at.v[1];
     seg[b] = at.v[2];
     slot[b] = at.v[3];
-    int to = at.v[0] + before[i];
+    first[b] = before[i];
+    int to = 0;
     for (int k = 0; k < SORT_WAVES; ++k) {
       const int n = cnt[k][b];
-      cnt[k][b] = to;
+      cnt[k][b] = (uint16_t)to;
       to += n;
     }
     at.v[0] += all[i];
@@ -174,7 +175,15 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
   __syncthreads();
 #pragma unroll
   for (int s = 0; s < PER; ++s)
-    if (id[s] >= 0) a.perm[cnt[w][id[s]] + local[s]] = (int)(r0 + s * 64);
+    if (id[s] >= 0) {
+      // place in its adapter's tiles; an adapter's last row stands for the rows that its
+      // last tile lacks
+      const int b = id[s], q = first[b] + cnt[w][b] + local[s], r = (int)(r0 + s * 64);
+      int* to = a.tile_rows + (int64_t)tile[b] * LORA_TILE + q;
+      *to = r;
+      if (q == off[b + 1] - off[b] - 1)
+        for (int i = 1; (q + i) % LORA_TILE; ++i) to[i] = r;
+    }
   // the tables, shared among the workgroups: the bin of entry e is the last one that starts at or before it
   auto find = [&](const int* starts, int e) {
     int lo = 0, hi = bins;                        // starts[lo] <= e < starts[hi]
@@ -185,18 +194,11 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     }
     return lo;
   };
-  // Entry e is a workgroup's, which runs on XCD e mod 8: each XCD gets a run of
-  // neighbours, so that its L2 reads an adapter's weights (a segment's t) once.
-  auto entry = [&](int e, int total) {
-    const int x = e & 7, j = e >> 3, per = total >> 3, rem = total & 7;
-    return j < per + (x < rem) ? x * per + min(x, rem) + j : -1;
-  };
   for (int e = blockIdx.x * SORT_WG + threadIdx.x; e < a.max_tiles; e += gridDim.x * SORT_WG) {
     int4 v = make_int4(-1, 0, 0, 0);
-    const int k = entry(e, tile[bins]);
-    if (k >= 0) {
-      const int b = find(tile, k), i = (k - tile[b]) * LORA_TILE;
-      v = make_int4(b, off[b] + i, min(LORA_TILE, off[b + 1] - off[b] - i), k);
+    if (e < tile[bins]) {
+      const int b = find(tile, e), i = (e - tile[b]) * LORA_TILE;
+      v = make_int4(b, off[b] + i, min(LORA_TILE, off[b + 1] - off[b] - i), e);
     }
     a.tiles[e] = v;
   }
@@ -204,9 +206,8 @@ __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
     for (int e = blockIdx.x * SORT_WG + threadIdx.x; e < a.max_segs; e += gridDim.x * SORT_WG) {
       int4 v = make_int4(-1, 0, 0, 0);
       int sl = -1;
-      const int k = entry(e, seg[bins]);
-      if (k >= 0) {
-        const int b = find(seg, k), i = k - seg[b], n = off[b + 1] - off[b];
+      if (e < seg[bins]) {
+        const int b = find(seg, e), i = e - seg[b], n = off[b + 1] - off[b];
         v = make_int4(b, off[b] + i * a.seg_rows, min(a.seg_rows, n - i * a.seg_rows),
                       tile[b] + i * (a.seg_rows / LORA_TILE));
         if (seg[b + 1] - seg[b] > 1) sl = slot[b] + i;
@@ -254,8 +255,9 @@ template <int DT> __device__ __forceinline__ u32x4 finite_or_zero(u32x4 v) {
 // ranges, 64 k a step: rows and weights go through LDS, a wave takes 16 rows. The
 // loads of the next two steps are in flight in registers, 16 bytes a lane at any
 // alignment, whole lines of a row. The K ranges' sums go through memory to
-// k_lora_parts (joined by the last workgroup of a tile instead, the fences of every
-// workgroup cost 60 us more than that launch).
+// k_lora_parts. 4096 x 4096 to rank 64: 13.3 us, and 5.6 for k_lora_parts (joined by
+// the last workgroup of a tile instead, 96: every workgroup's fence writes an L2 back);
+// 8192 rows 26 us, 2.6 TB/s of x.
 constexpr int SHR_K = 64;
 // a row of sums in memory
 static __host__ __device__ int sum_ld(int rank) { return (rank + 3) & ~3; }
@@ -270,7 +272,7 @@ template <int DT, bool KM, int NF> __global__ __launch_bounds__(256) void k_lora
   if (tile.x < 0 || tile.x == a.adapters) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  if (threadIdx.x < LORA_TILE) s_row[threadIdx.x] = a.perm[tile.y + min((int)threadIdx.x, tile.z - 1)];
+  if (threadIdx.x < LORA_TILE) s_row[threadIdx.x] = a.rows[blockIdx.x * LORA_TILE + threadIdx.x];
   __syncthreads();
   const int j0 = blockIdx.y * COLS, z = (int)((blockIdx.z + (uint32_t)tile.w) % gridDim.z);
   const int steps = (a.k + SHR_K - 1) / SHR_K;
@@ -371,7 +373,7 @@ template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink
   const bool none = tile.x == a.adapters;
   const int i = blockIdx.y * 16 + (threadIdx.x >> 4), g = (threadIdx.x & 15) * 4, ld = sum_ld(a.rank);
   const bool in = i < tile.z;
-  const int64_t p = tile.y + min(i, tile.z - 1), r = a.perm[p];
+  const int64_t p = tile.y + min(i, tile.z - 1), r = a.rows[blockIdx.x * LORA_TILE + i];
   float* const tr = a.t + r * a.rank;
   uint32_t m = 0, m2 = 0;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};                  // of the last four (up to rank 64 the only ones)
@@ -434,177 +436,181 @@ template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink
 }
 
 // ------------------------------------------------------------------- expand
-// A workgroup of four waves: a tile's rows, `chunk` columns of the result, a wave
-// 32 rows x 32 columns at a time, the next columns' loads in flight. The weights' rows
-// are dealt to the fragments so that a lane ends with 8 consecutive columns of a row
-// (fragment f, place m: column 8 (m / 4) + 4 f + m % 4): base and result move 16 bytes a
-// lane, 64 a row. KB: blocks of 32 of the rank whose parts stay in registers (0: any
-// rank, read each time).
-template <int DT, bool KM, int KB>
-__global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
-  constexpr int MF = 2, F = 2, KU = KB ? KB : 1, SROW = 80;
-  __shared__ __align__(16) uint8_t area[KM ? 4 * KU * 32 * SROW : 16];
+// A workgroup of four waves: a tile's rows (16 a wave), `chunk` columns of the result,
+// 64 columns and 32 KB of the rank a step. The weights go through LDS, read from memory
+// once for the four; the loads of the next two steps are in flight in registers. The
+// weights' rows are dealt to the fragments so that a lane ends with 8 consecutive
+// columns of a row, twice (fragment f, place m: column 32 (f / 2) + 8 (m / 4) + 4 (f % 2)
+// + m % 4): base and result move 16 bytes a lane, 64 a row, whole lines in two. 8192 x
+// rank 64 -> 4096: 48 us, 2.8 TB/s of base and result, where a copy in the same pattern
+// with all loads at the start takes 30; with 2 waves a SIMD instead of 4 it takes 55.
+template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraExpand a) {
+  constexpr int F = 4, WROW = KM ? 144 : KB * 64 + 16, STAGE = KM ? KB * 32 * WROW : 64 * WROW;
+  constexpr int CPR = KM ? 8 : KB * 4, WL = KB;    // chunks of a staged row, loads of a thread
+  __shared__ __align__(16) uint8_t area[2 * STAGE];
   const int4 tile = a.tiles[blockIdx.x];
   if (tile.x < 0) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int m0 = (w & 1) * 32;                     // the wave's rows
-  if (m0 >= tile.z) return;
   const bool none = tile.x == a.adapters;
-  const uint16_t* wi = static_cast<const uint16_t*>(a.w) + (none ? 0 : tile.x * a.stw);
-  uint8_t* const stage = area + (KM ? w * (KU * 32 * SROW) : 0);
-  // the lane's rows: their places, and where its columns of them lie
-  int64_t at[MF];
-  const uint16_t* bp[MF];
-  uint16_t* dp[MF];
-  bool in[MF];
+  const int i = w * 16 + col;                      // the lane's row of the tile
+  const bool in = i < tile.z;
+  const int64_t r = a.rows[blockIdx.x * LORA_TILE + i], at = tile.y + min(i, tile.z - 1);
+  const uint16_t* const bp = static_cast<const uint16_t*>(a.base) + r * a.ldbase + quad * 8;
+  uint16_t* const dp = static_cast<uint16_t*>(a.dst) + r * a.lddst + quad * 8;
+  const uint16_t* const wi = static_cast<const uint16_t*>(a.w) + (none ? 0 : tile.x * a.stw);
+  const float fac = none ? 0.f : a.fac[at];
+  const int nk = none ? 1 : (a.rp + KB * 32 - 1) / (KB * 32);
+  u32x4 th[KB], tl[KB];
+  auto parts = [&](int kk) {
 #pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    in[m] = m0 + m * 16 + col < tile.z;
-    at[m] = tile.y + min(m0 + m * 16 + col, tile.z - 1);
-    const int64_t r = a.perm[at[m]];
-    bp[m] = static_cast<const uint16_t*>(a.base) + r * a.ldbase + quad * 8;
-    dp[m] = static_cast<uint16_t*>(a.dst) + r * a.lddst + quad * 8;
-  }
-  u32x4 th[KU][MF], tl[KU][MF];
-  auto parts = [&](int k, u32x4* h, u32x4* l) {
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      h[m] = *reinterpret_cast<const u32x4*>(a.hi + at[m] * a.rp + k * 32 + quad * 8);
-      l[m] = *reinterpret_cast<const u32x4*>(a.lo + at[m] * a.rp + k * 32 + quad * 8);
+    for (int k = 0; k < KB; ++k) {
+      const int j = (kk * KB + k) * 32 + quad * 8;
+      th[k] = tl[k] = u32x4{0, 0, 0, 0};
+      if (j >= a.rp) continue;
+      th[k] = *reinterpret_cast<const u32x4*>(a.hi + at * a.rp + j);
+      tl[k] = *reinterpret_cast<const u32x4*>(a.lo + at * a.rp + j);
     }
   };
-  float fac[MF] = {};
-  if (!none) {
-#pragma unroll
-    for (int m = 0; m < MF; ++m) fac[m] = a.fac[at[m]];
-    if constexpr (KB > 0)
-#pragma unroll
-      for (int k = 0; k < KB; ++k) parts(k, th[k], tl[k]);
-  }
-  // Weights of k block k: NT rows of the lane's columns; k-major 32 k rows of 4
-  // chunks. `whole`: nothing of what the wave loads lies behind its rows' ends.
-  const uint16_t* wp[F];
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-    wp[f] = KM ? wi + (f * 16 + lane / 4) * a.ldw + lane % 4 * 8 : wi + ((col >> 2) * 8 + f * 4 + (col & 3)) * a.ldw + quad * 8;
-  auto weights = [&](bool whole, int c0, int k, u32x4* v) {
-    const int64_t off = KM ? (int64_t)k * 32 * a.ldw + c0 : (int64_t)c0 * a.ldw + k * 32;
-    if (whole) {
-#pragma unroll
-      for (int f = 0; f < F; ++f) __builtin_memcpy(&v[f], wp[f] + off, 16);
-      return;
-    }
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      if constexpr (!KM) {
-        const int c = c0 + (col >> 2) * 8 + f * 4 + (col & 3);
-        v[f] = load_chunk<2, true>(wi + min(c, a.cols - 1) * a.ldw, (int64_t)(k * 32 + quad * 8) * 2, (int64_t)a.rank * 2);
-      } else {
-        const int kr = k * 32 + f * 16 + lane / 4, c = c0 + lane % 4 * 8;
-        v[f] = u32x4{0, 0, 0, 0};
-        if (kr < a.rank && c < a.cols) v[f] = load_chunk<2, true>(wi + kr * a.ldw, (int64_t)c * 2, (int64_t)a.cols * 2);
-      }
-    }
-  };
-  struct Cols {
-    u32x4 w[KU][F], b[MF];
-  };
-  auto load = [&](Cols& s, int c0) {
-    const bool inside = c0 + 32 <= a.cols, whole = inside && a.rank % 32 == 0;
-    if constexpr (KB > 0)
-      if (!none)
-#pragma unroll
-        for (int k = 0; k < KB; ++k) weights(whole, c0, k, s.w[k]);
-    if (!a.base) {
-#pragma unroll
-      for (int m = 0; m < MF; ++m) s.b[m] = u32x4{0, 0, 0, 0};
-    } else if (inside) {
-#pragma unroll
-      for (int m = 0; m < MF; ++m) __builtin_memcpy(&s.b[m], bp[m] + c0, 16);
-    } else {
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        s.b[m] = u32x4{0, 0, 0, 0};
-        if (c0 + quad * 8 < a.cols)
-          s.b[m] = load_chunk<2, true>(bp[m] - quad * 8, (int64_t)(c0 + quad * 8) * 2, (int64_t)a.cols * 2);
-      }
-    }
-  };
+  if (!none) parts(0);
   // tiles start with different columns, so that neighbours read different weights
-  const int y = (int)((blockIdx.y + (uint32_t)tile.w) % gridDim.y), c_end = min(a.cols, (y + 1) * a.chunk);
-  int c0 = y * a.chunk + (w >> 1) * 32;
-  Cols next;
-  if (c0 < c_end) load(next, c0);
-#pragma unroll 1
-  for (; c0 < c_end; c0 += 64) {
-    Cols cur = next;
-    if (c0 + 64 < c_end) load(next, c0 + 64);
-    f32x4 acc[F][MF];
-    // safe: low parts meet zeros where the weights are not finite
-    auto multiply = [&](bool safe) {
+  const int y = (int)((blockIdx.y + (uint32_t)tile.w) % gridDim.y);
+  const int cb = y * a.chunk, steps = (min(a.cols, cb + a.chunk) - cb + 63) / 64 * nk;
+  struct Step {
+    u32x4 w[WL], b[2];
+  };
+  auto load = [&](Step& s, int n) {
+    const int c0 = cb + n / nk * 64, kk = n % nk;
+    // whether nothing of what the workgroup loads lies behind its rows' ends
+    const bool inside = c0 + 64 <= a.cols;
+    if (!none) {
+      const int q0 = threadIdx.x / CPR, qc = threadIdx.x % CPR * 8;
+      constexpr int RPL = 256 / CPR;               // staged rows of a load
+      if (inside && (kk + 1) * KB * 32 <= a.rank) {
+        const uint16_t* p = KM ? wi + (int64_t)(kk * KB * 32 + q0) * a.ldw + c0 + qc
+                               : wi + (int64_t)(c0 + q0) * a.ldw + kk * KB * 32 + qc;
 #pragma unroll
-      for (int f = 0; f < F; ++f)
+        for (int l = 0; l < WL; ++l) __builtin_memcpy(&s.w[l], p + l * RPL * a.ldw, 16);
+      } else {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) acc[f][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < (KB ? KB : 8); ++k) {
-        if (!KB && k * 32 >= a.rp) break;
-        const int ku = KB ? k : 0;
-        if constexpr (KB == 0) {
-          weights(c0 + 32 <= a.cols && a.rank % 32 == 0, c0, k, cur.w[0]);
-          parts(k, th[0], tl[0]);
-        }
-        u32x4 p[F];
-        if constexpr (KM) {
-          uint8_t* const st = stage + ku * (32 * SROW);
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int f = 0; f < F; ++f) *reinterpret_cast<u32x4*>(st + (f * 16 + lane / 4) * SROW + lane % 4 * 16) = cur.w[ku][f];
-          asm volatile("" ::: "memory");           // the wave's own LDS runs in order
-#pragma unroll
-          for (int f = 0; f < F; ++f)
-            p[f] = read_tr(st + (quad * 8 + (col >> 2)) * SROW + (col & 3) * 16 + f * 8, 4 * SROW);
-        } else {
-#pragma unroll
-          for (int f = 0; f < F; ++f) p[f] = cur.w[ku][f];
-        }
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-#pragma unroll
-          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(p[f], th[ku][m], acc[f][m]);
-          if (safe) p[f] = finite_or_zero<DT>(p[f]);
-#pragma unroll
-          for (int m = 0; m < MF; ++m) acc[f][m] = Elem<DT>::mma16(p[f], tl[ku][m], acc[f][m]);
+        for (int l = 0; l < WL; ++l) {
+          const int row = (KM ? kk * KB * 32 : c0) + q0 + l * RPL, e = (KM ? c0 : kk * KB * 32) + qc;
+          s.w[l] = u32x4{0, 0, 0, 0};
+          if (row < (KM ? a.rank : a.cols) && e < (KM ? a.cols : a.rank))
+            s.w[l] = load_chunk<2, true>(wi + row * a.ldw, (int64_t)e * 2, (int64_t)(KM ? a.cols : a.rank) * 2);
         }
       }
-    };
-    if (!none) {
-      multiply(false);
-      float far = 0.f;
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) far = __builtin_fmaf(0.f, acc[f][m][e], far);
-      if (__any(far != 0.f)) multiply(true);
     }
-    const int c = c0 + quad * 8;
+    if (kk) return;
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      float v[8];
-      unpack16<DT>(cur.b[m], v);
-      if (!none)
+    for (int h = 0; h < 2; ++h) {
+      s.b[h] = u32x4{0, 0, 0, 0};
+      if (!a.base) continue;
+      const int c = c0 + h * 32;
+      if (inside) __builtin_memcpy(&s.b[h], bp + c, 16);
+      else if (c + quad * 8 < a.cols)
+        s.b[h] = load_chunk<2, true>(bp - quad * 8, (int64_t)(c + quad * 8) * 2, (int64_t)a.cols * 2);
+    }
+  };
+  f32x4 acc[F];
+  // safe: low parts meet zeros where the weights are not finite
+  auto multiply = [&](int buf, bool safe) {
+    const uint8_t* const sw = area + buf * STAGE;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(fac[m], acc[e / 4][m][e % 4], v[e]);
-      const u32x4 o = pack16<DT>(v);
-      if (!in[m]) continue;
-      if (c + 8 <= a.cols) __builtin_memcpy(dp[m] + c0, &o, 16);      // at any alignment
-      else
+    for (int k = 0; k < KB; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < a.cols) dp[m][c0 + e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+      for (int f = 0; f < F; ++f) {
+        u32x4 p;
+        if constexpr (KM)
+          p = read_tr(sw + (k * 32 + quad * 8 + (col >> 2)) * WROW + (f >> 1) * 64 + (col & 3) * 16 + (f & 1) * 8, 4 * WROW);
+        else
+          p = *reinterpret_cast<const u32x4*>(sw + ((f >> 1) * 32 + (col >> 2) * 8 + (f & 1) * 4 + (col & 3)) * WROW +
+                                              k * 64 + quad * 16);
+        acc[f] = Elem<DT>::mma16(p, th[k], acc[f]);
+        if (safe) p = finite_or_zero<DT>(p);
+        acc[f] = Elem<DT>::mma16(p, tl[k], acc[f]);
+      }
+  };
+  auto clear = [&]() {
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  auto finite = [&]() {
+    float far = 0.f;
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) far = __builtin_fmaf(0.f, acc[f][e], far);
+    return far == 0.f;
+  };
+  auto stage = [&](const Step& s, int buf) {
+    constexpr int RPL = 256 / CPR;
+    uint8_t* const sw = area + buf * STAGE + threadIdx.x / CPR * WROW + threadIdx.x % CPR * 16;
+#pragma unroll
+    for (int l = 0; l < WL; ++l) *reinterpret_cast<u32x4*>(sw + l * RPL * WROW) = s.w[l];
+  };
+  // One barrier a step: a buffer is written again two steps on, when every wave has
+  // passed the barrier behind its readers.
+  Step s[2];
+  u32x4 base[2];
+  if (steps > 0) load(s[0], 0);
+  if (steps > 1) load(s[1], 1);
+  for (int n = 0; n < steps; n += 2) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (n + b >= steps) break;
+      const int c0 = cb + (n + b) / nk * 64, kk = (n + b) % nk;
+      if (!none) stage(s[b], b);
+      if (kk == 0) {
+        base[0] = s[b].b[0];
+        base[1] = s[b].b[1];
+        clear();
+      }
+      if (n + b + 2 < steps) load(s[b], n + b + 2);
+      if (!none) {
+        __syncthreads();
+        if (nk > 1) parts(kk);
+        multiply(b, false);
+      }
+      if (kk != nk - 1) continue;
+      // not finite: again with zeros for the low parts (a rank over one step's from
+      // memory, a wave by itself)
+      if (!none && __any(!finite())) {
+        clear();
+        if (nk == 1) {
+          multiply(b, true);
+        } else {
+          for (int j = 0; j < a.rank; ++j) {
+            const int64_t ti = at * a.rp + j;
+            const float h = Row<DT>::f(a.hi[ti]), l = Row<DT>::f(a.lo[ti]);
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = min(c0 + (f >> 1) * 32 + quad * 8 + (f & 1) * 4 + e, a.cols - 1);
+                const float wv = Row<DT>::f(KM ? wi[j * a.ldw + c] : wi[c * a.ldw + j]);
+                acc[f][e] += wv * h;
+                if (__builtin_fabsf(wv) < __builtin_inff()) acc[f][e] += wv * l;
+              }
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + h * 32 + quad * 8;
+        float v[8];
+        unpack16<DT>(base[h], v);
+        if (!none)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(fac, acc[h * 2 + e / 4][e % 4], v[e]);
+        const u32x4 o = pack16<DT>(v);
+        if (!in) continue;
+        if (c + 8 <= a.cols) __builtin_memcpy(dp + c0 + h * 32, &o, 16);      // at any alignment
+        else
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < a.cols) dp[c0 + h * 32 + e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+      }
     }
   }
 }
@@ -616,21 +622,22 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraExpand a) {
 // one after that too), both read transposed; a row's 32-byte pieces are moved about so
 // that the 8 rows that 32 lanes read together meet different banks. da's lanes end with
 // 4 consecutive columns of a rank row, db's with 4 ranks of a column's row: the
-// operands change places.
+// operands change places. 8192 rows of 4096, rank 64, both gradients: 69 us (eight waves
+// of 64 x 32 with rows padded instead of moved about, and a mask at every product, 107).
 constexpr int GRAD_WG = 256, GRAD_COLS = 256, GRAD_ROWS = 64;
 constexpr int GRAD_XROW = GRAD_COLS * 2, GRAD_TROW = 128;      // bytes in LDS
 __device__ __forceinline__ int swz_x(int k) { return (k & 3) | (k >> 3 & 1) << 2; }
 __device__ __forceinline__ int swz_t(int k) { return (k >> 1 & 1) | (k >> 3 & 1) << 1; }
 template <int DT, bool DB>
 __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot, int j0, int c0, uint8_t* sx, uint8_t* st,
-                                          uint32_t* s_top, int (*s_perm)[GRAD_ROWS]) {
+                                          uint32_t* s_top, int (*s_rows)[GRAD_ROWS]) {
   constexpr int XROW = GRAD_XROW, TROW = GRAD_TROW;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
   const int cols = DB ? a.out : a.in;
   const float* tp = DB ? a.t : a.u;
   const uint16_t* xp = static_cast<const uint16_t*>(DB ? a.dy : a.x);
   const int64_t ld = DB ? a.lddy : a.ldx;
-  auto place = [&](int i) { return i < seg.z ? a.perm[seg.y + i] : -1; };
+  auto place = [&](int i) { return i < seg.z ? a.rows[(int64_t)seg.w * LORA_TILE + i] : -1; };
   int e = 0;                                       // fp16: parts are |t| 2^-e, below 2^14
   if constexpr (DT == DT_F16) {
     const uint32_t* top = (DB ? a.top_t : a.top_u) + seg.w * (LORA_TILE / 16);
@@ -651,22 +658,22 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
   int next = -1;
   // whether nothing of what the workgroup loads lies behind its rows' ends
   const bool whole = c0 + GRAD_COLS <= cols && j0 + 64 <= a.rank;
-  auto load = [&](const int* perm, int left) {
+  auto load = [&](const int* rows, int left) {
     if (whole && left >= GRAD_ROWS) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) __builtin_memcpy(&xv[i], xp + perm[xr + i * 8] * ld + (c0 + xc * 8), 16);
-      const float* t = tp + (int64_t)perm[tr] * a.rank + (j0 + tc * 16);
+      for (int i = 0; i < 8; ++i) __builtin_memcpy(&xv[i], xp + rows[xr + i * 8] * ld + (c0 + xc * 8), 16);
+      const float* t = tp + (int64_t)rows[tr] * a.rank + (j0 + tc * 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) __builtin_memcpy(tv + i * 4, t + i * 4, 16);
       return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = perm[xr + i * 8];
+      const int r = rows[xr + i * 8];
       xv[i] = u32x4{0, 0, 0, 0};
       if (r >= 0 && c0 + xc * 8 < cols) xv[i] = load_chunk<2, true>(xp + r * ld, (int64_t)(c0 + xc * 8) * 2, (int64_t)cols * 2);
     }
-    const int r = perm[tr];
+    const int r = rows[tr];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 v = {0, 0, 0, 0};
@@ -676,14 +683,14 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
     }
   };
   f32x4 acc[4][4];                                 // [x fragment][t fragment]
-  auto rows = [&](bool safe) {
+  auto sums = [&](bool safe) {
 #pragma unroll
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (threadIdx.x < 2 * GRAD_ROWS) s_perm[threadIdx.x / GRAD_ROWS][threadIdx.x % GRAD_ROWS] = place(threadIdx.x);
+    if (threadIdx.x < 2 * GRAD_ROWS) s_rows[threadIdx.x / GRAD_ROWS][threadIdx.x % GRAD_ROWS] = place(threadIdx.x);
     __syncthreads();
-    if (seg.z > 0) load(s_perm[0], seg.z);
+    if (seg.z > 0) load(s_rows[0], seg.z);
     for (int i0 = 0, step = 0; i0 < seg.z; i0 += GRAD_ROWS, ++step) {
       __syncthreads();                             // the last step's readers are done
 #pragma unroll
@@ -703,10 +710,10 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
         *reinterpret_cast<u32x4*>(h + i * 16) = pack16<DT>(tv + i * 8);
         *reinterpret_cast<u32x4*>(h + GRAD_ROWS * TROW + i * 16) = pack16<DT>(low + i * 8);
       }
-      if (step && threadIdx.x < GRAD_ROWS) s_perm[(step + 1) & 1][threadIdx.x] = next;
+      if (step && threadIdx.x < GRAD_ROWS) s_rows[(step + 1) & 1][threadIdx.x] = next;
       __syncthreads();
       if (threadIdx.x < GRAD_ROWS) next = place(i0 + 2 * GRAD_ROWS + threadIdx.x);
-      if (i0 + GRAD_ROWS < seg.z) load(s_perm[(step + 1) & 1], seg.z - i0 - GRAD_ROWS);
+      if (i0 + GRAD_ROWS < seg.z) load(s_rows[(step + 1) & 1], seg.z - i0 - GRAD_ROWS);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int kr = k * 32 + quad * 8 + (col >> 2);         // kr + 4: the same pieces
@@ -729,7 +736,7 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
     }
     __syncthreads();
   };
-  rows(false);
+  sums(false);
   float far = 0.f;
 #pragma unroll
   for (int f = 0; f < 4; ++f)
@@ -737,7 +744,7 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) far = __builtin_fmaf(0.f, acc[f][j][q], far);
-  if (__syncthreads_or(far != 0.f)) rows(true);
+  if (__syncthreads_or(far != 0.f)) sums(true);
   const float scale = a.scale[seg.x];
   // four consecutive values of a row of the result, n long, from column c on: rounded,
   // or (one of several segments) as they are
@@ -780,12 +787,12 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
 template <int DT> __global__ __launch_bounds__(GRAD_WG, 2) void k_lora_grad(LoraGrad a, int in_tiles) {
   __shared__ __align__(64) uint8_t sx[GRAD_ROWS * GRAD_XROW], st[2 * GRAD_ROWS * GRAD_TROW];
   __shared__ uint32_t s_top[GRAD_WG / 64];
-  __shared__ int s_perm[2][GRAD_ROWS];
+  __shared__ int s_rows[2][GRAD_ROWS];
   const int4 seg = a.segs[blockIdx.x];
   if (seg.x < 0) return;
   const int slot = a.slot[blockIdx.x], j0 = blockIdx.z * 64;
-  if ((int)blockIdx.y < in_tiles) lora_grad<DT, false>(a, seg, slot, j0, blockIdx.y * GRAD_COLS, sx, st, s_top, s_perm);
-  else lora_grad<DT, true>(a, seg, slot, j0, (blockIdx.y - in_tiles) * GRAD_COLS, sx, st, s_top, s_perm);
+  if ((int)blockIdx.y < in_tiles) lora_grad<DT, false>(a, seg, slot, j0, blockIdx.y * GRAD_COLS, sx, st, s_top, s_rows);
+  else lora_grad<DT, true>(a, seg, slot, j0, (blockIdx.y - in_tiles) * GRAD_COLS, sx, st, s_top, s_rows);
 }
 // the sums of adapters of several segments, in order, four a thread
 template <int DT> __global__ __launch_bounds__(256) void k_lora_join(LoraGrad a) {
@@ -927,11 +934,10 @@ hipError_t launch_lora_shrink(int dt, bool k_major, const LoraShrink& a, hipStre
 template <int DT, bool KM> static hipError_t expand(const LoraExpand& a, hipStream_t s) {
   const dim3 grid(a.max_tiles, (a.cols + a.chunk - 1) / a.chunk);
   if (a.rp == 32) hipLaunchKernelGGL((k_lora_expand<DT, KM, 1>), grid, dim3(256), 0, s, a);
-  else if (a.rp == 64) hipLaunchKernelGGL((k_lora_expand<DT, KM, 2>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_lora_expand<DT, KM, 0>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_lora_expand<DT, KM, 2>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
-// Columns of a workgroup: as few as leave three workgroups a CU
+// Columns of a workgroup: as few as leave four workgroups a CU
 int lora_chunk(int rows, int cols) {
   const int64_t tiles = (rows + LORA_TILE - 1) / LORA_TILE;
   return (int)((cols * tiles / EXP_WGS + 63) / 64 + (cols * tiles < EXP_WGS)) * 64;
