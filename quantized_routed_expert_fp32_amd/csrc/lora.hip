@@ -7,8 +7,8 @@
 //
 //  * k_lora_row: few rows, one launch, a workgroup a row.
 //  * k_lora_sort: the rows by adapter, cut into tiles of one adapter each.
-//  * k_lora_shrink: t or u, the long contraction: operands straight from memory into
-//    matrix instructions, its K range over the waves of a workgroup.
+//  * k_lora_shrink, k_lora_parts: t or u, the long contraction, its K range over
+//    several workgroups whose sums are joined in order.
 //  * k_lora_expand: y or dx, the short contraction, one pass over base and result.
 //  * k_lora_grad (k_lora_join): da and db, contractions over an adapter's rows.
 // Ranks are small, so all of them are bound by the bytes of x, base, y and the
@@ -84,7 +84,8 @@ __device__ __forceinline__ Scan4 scan(Scan4 x, Scan4* wave_sum) {
 // A stable counting sort, 8192 rows a workgroup: counts a wave in LDS, their
 // prefix sums, then each wave places its rows. Lanes of the same adapter find each
 // other by ballots over the id's bits: runs of one adapter would queue at an LDS
-// atomic. One workgroup's latency: 9 us for 777 rows, 13 for 8192.
+// atomic. One workgroup's latency: 10 us for 777 rows, 14 for
+// 4096, 17 for 8192.
 __global__ __launch_bounds__(SORT_WG) void k_lora_sort(LoraSort a) {
   constexpr int PER = LORA_SORT / SORT_WG;      // steps of a wave
   constexpr int BPT = (SORT_BINS + SORT_WG - 1) / SORT_WG;
@@ -255,9 +256,9 @@ template <int DT> __device__ __forceinline__ u32x4 finite_or_zero(u32x4 v) {
 // ranges, 64 k a step: rows and weights go through LDS, a wave takes 16 rows. The
 // loads of the next two steps are in flight in registers, 16 bytes a lane at any
 // alignment, whole lines of a row. The K ranges' sums go through memory to
-// k_lora_parts. 4096 x 4096 to rank 64: 13.3 us, and 5.6 for k_lora_parts (joined by
+// k_lora_parts. 4096 x 4096 to rank 64: 12.4 us, and 5.7 for k_lora_parts (joined by
 // the last workgroup of a tile instead, 96: every workgroup's fence writes an L2 back);
-// 8192 rows 26 us, 2.6 TB/s of x.
+// 8192 rows 22 to 25 us, 2.7 to 3.0 TB/s of x.
 constexpr int SHR_K = 64;
 // a row of sums in memory
 static __host__ __device__ int sum_ld(int rank) { return (rank + 3) & ~3; }
@@ -442,7 +443,7 @@ template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink
 // weights' rows are dealt to the fragments so that a lane ends with 8 consecutive
 // columns of a row, twice (fragment f, place m: column 32 (f / 2) + 8 (m / 4) + 4 (f % 2)
 // + m % 4): base and result move 16 bytes a lane, 64 a row, whole lines in two. 8192 x
-// rank 64 -> 4096: 48 us, 2.8 TB/s of base and result, where a copy in the same pattern
+// rank 64 -> 4096: 48 to 50 us, 2.7 TB/s of base and result, where a copy in the same pattern
 // with all loads at the start takes 30; with 2 waves a SIMD instead of 4 it takes 55.
 template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraExpand a) {
   constexpr int F = 4, WROW = KM ? 144 : KB * 64 + 16, STAGE = KM ? KB * 32 * WROW : 64 * WROW;
@@ -622,7 +623,7 @@ template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_l
 // one after that too), both read transposed; a row's 32-byte pieces are moved about so
 // that the 8 rows that 32 lanes read together meet different banks. da's lanes end with
 // 4 consecutive columns of a rank row, db's with 4 ranks of a column's row: the
-// operands change places. 8192 rows of 4096, rank 64, both gradients: 69 us (eight waves
+// operands change places. 8192 rows of 4096, rank 64, both gradients: 69 to 72 us (eight waves
 // of 64 x 32 with rows padded instead of moved about, and a mask at every product, 107).
 constexpr int GRAD_WG = 256, GRAD_COLS = 256, GRAD_ROWS = 64;
 constexpr int GRAD_XROW = GRAD_COLS * 2, GRAD_TROW = 128;      // bytes in LDS
