@@ -746,7 +746,7 @@ __device__ __forceinline__ void lora_grad(const LoraGrad& a, int4 seg, int slot,
 #pragma unroll
       for (int q = 0; q < 4; ++q) far = __builtin_fmaf(0.f, acc[f][j][q], far);
   if (__syncthreads_or(far != 0.f)) sums(true);
-  const float scale = a.scale[seg.x];
+  const float scale = seg.z ? a.scale[seg.x] : 0.f;       // (no row: zeros, whatever stands in the scale)
   // four consecutive values of a row of the result, n long, from column c on: rounded,
   // or (one of several segments) as they are
   const int64_t size = (int64_t)a.rank * cols;
