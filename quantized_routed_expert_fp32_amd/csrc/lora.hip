@@ -550,6 +550,17 @@ template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_l
 #pragma unroll
     for (int l = 0; l < WL; ++l) *reinterpret_cast<u32x4*>(sw + l * RPL * WROW) = s.w[l];
   };
+  // one value of the result: the row's parts from t0 on, column c of the weights
+  auto one_sum = [&](int64_t t0, int c) {
+    float v = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < a.rank; ++j) {
+      const float wv = Row<DT>::f(KM ? wi[j * a.ldw + c] : wi[c * a.ldw + j]);
+      v += wv * Row<DT>::f(a.hi[t0 + j]);
+      if (__builtin_fabsf(wv) < __builtin_inff()) v += wv * Row<DT>::f(a.lo[t0 + j]);
+    }
+    return v;
+  };
   // One barrier a step: a buffer is written again two steps on, when every wave has
   // passed the barrier behind its readers.
   Step s[2];
@@ -574,26 +585,21 @@ template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_l
         multiply(b, false);
       }
       if (kk != nk - 1) continue;
-      // not finite: again with zeros for the low parts (a rank over one step's from
-      // memory, a wave by itself)
+      // not finite: again with zeros for the low parts. A rank of several steps: those values
+      // alone, from memory, a wave by itself; the others keep the sums that they have.
       if (!none && __any(!finite())) {
-        clear();
         if (nk == 1) {
+          clear();
           multiply(b, true);
         } else {
-          for (int j = 0; j < a.rank; ++j) {
-            const int64_t ti = at * a.rp + j;
-            const float h = Row<DT>::f(a.hi[ti]), l = Row<DT>::f(a.lo[ti]);
 #pragma unroll
-            for (int f = 0; f < F; ++f)
+          for (int f = 0; f < F; ++f)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int c = min(c0 + (f >> 1) * 32 + quad * 8 + (f & 1) * 4 + e, a.cols - 1);
-                const float wv = Row<DT>::f(KM ? wi[j * a.ldw + c] : wi[c * a.ldw + j]);
-                acc[f][e] += wv * h;
-                if (__builtin_fabsf(wv) < __builtin_inff()) acc[f][e] += wv * l;
-              }
-          }
+            for (int e = 0; e < 4; ++e) {
+              if (__builtin_fabsf(acc[f][e]) < __builtin_inff()) continue;
+              const int c = min(c0 + (f >> 1) * 32 + quad * 8 + (f & 1) * 4 + e, a.cols - 1);
+              acc[f][e] = one_sum(at * a.rp, c);
+            }
         }
       }
 #pragma unroll
