@@ -86,7 +86,11 @@ template <int G, int NI> __device__ __forceinline__ float softmax(float (&v)[NI]
   return m + logf(z);
 }
 
-// A workgroup's sums in the workspace: ep sums of p, ep counts, lse^2, rows
+// A workgroup's sums in the workspace: ep sums of p (fp32), ep counts, lse^2 (64 bits), rows.
+// A thread adds its own rows of p in fp32 (in long calls rows / 8192 of them, beyond 256
+// experts rows / 2048); everything behind that, and lse^2 from its product on, is added in
+// 64 bits: one chain of fp32 additions over a workgroup's 32 groups cost the z loss of 64
+// rows 1.0e-7 where its own rounding is 3e-8.
 struct Part {
   int ep;
   int64_t words;
@@ -94,9 +98,9 @@ struct Part {
 };
 
 // The workgroups' sums in order, by one workgroup: 16 bytes a load, each column
-// in up to 16 stretches (fp32; joined in 64 bits).
+// in up to 16 stretches.
 __device__ __forceinline__ void join(const BalanceArgs& a, int parts) {
-  __shared__ f32x4 seg[BAL_WG];
+  __shared__ double seg[BAL_WG][4];
   __shared__ double loss[BAL_WG / 64];
   __shared__ double zsum;
   __shared__ int rows;
@@ -108,15 +112,18 @@ __device__ __forceinline__ void join(const BalanceArgs& a, int parts) {
     const float* at = a.part + u * 4;
     const int p0 = (int)((int64_t)parts * s / segs), p1 = (int)((int64_t)parts * (s + 1) / segs);
     if (u < q) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      double v[4] = {0, 0, 0, 0};
 #pragma unroll 8
-      for (int i = p0; i < p1; ++i) v += *reinterpret_cast<const f32x4*>(at + i * p.words);
-      seg[threadIdx.x] = v;
+      for (int i = p0; i < p1; ++i) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(at + i * p.words);
+        for (int e = 0; e < 4; ++e) v[e] += f[e];
+      }
+      for (int e = 0; e < 4; ++e) seg[threadIdx.x][e] = v[e];
     } else {
       i32x4 v = {0, 0, 0, 0};
 #pragma unroll 8
       for (int i = p0; i < p1; ++i) v += *reinterpret_cast<const i32x4*>(at + i * p.words);
-      seg[threadIdx.x] = __builtin_bit_cast(f32x4, v);
+      for (int e = 0; e < 4; ++e) seg[threadIdx.x][e] = v[e];          // exact
     }
   }
   if (threadIdx.x < 64) {
@@ -124,8 +131,8 @@ __device__ __forceinline__ void join(const BalanceArgs& a, int parts) {
     int n = 0;
     for (int i = threadIdx.x; i < parts; i += 64) {
       const float* at = a.part + i * p.words + 2 * p.ep;
-      z += at[0];
-      n += __float_as_int(at[1]);
+      z += *reinterpret_cast<const double*>(at);
+      n += __float_as_int(at[2]);
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
@@ -141,15 +148,15 @@ __device__ __forceinline__ void join(const BalanceArgs& a, int parts) {
   double mine = 0;
   if ((int)threadIdx.x < q) {
     double v[4] = {0, 0, 0, 0};
-    i32x4 c = {0, 0, 0, 0};
-    for (int i = 0; i < segs; ++i) {
-      const f32x4 f = seg[i * units + u];
-      c += __builtin_bit_cast(i32x4, seg[i * units + q + u]);
-      for (int e = 0; e < 4; ++e) v[e] += f[e];
-    }
+    double c[4] = {0, 0, 0, 0};
+    for (int i = 0; i < segs; ++i)
+      for (int e = 0; e < 4; ++e) {
+        v[e] += seg[i * units + u][e];
+        c[e] += seg[i * units + q + u][e];
+      }
     for (int e = 0; e < 4; ++e)
       if (u * 4 + e < a.experts) {
-        a.counts[u * 4 + e] = c[e];
+        a.counts[u * 4 + e] = (int)c[e];
         mine += v[e] * c[e];
       }
   }
@@ -171,13 +178,14 @@ template <int T, int G, int NI> __global__ __launch_bounds__(BAL_WG) void k_bala
   constexpr int GROUPS = BAL_WG / G, COLS = G * NI * 4;
   __shared__ float sp[GROUPS * COLS];               // 8 KiB NI
   __shared__ int hist[COLS];
-  __shared__ float sz[GROUPS];
+  __shared__ double sz[GROUPS];
   __shared__ int sn[GROUPS];
   const int g = threadIdx.x % G, grp = threadIdx.x / G;
   for (int c = threadIdx.x; c < COLS; c += BAL_WG) hist[c] = 0;
   __syncthreads();
   const int64_t r0 = (int64_t)a.rows * blockIdx.x / gridDim.x, r1 = (int64_t)a.rows * (blockIdx.x + 1) / gridDim.x;
-  float sum[NI][4] = {}, z2 = 0.f;
+  float sum[NI][4] = {};
+  double z2 = 0;
   int n = 0;
   for (int64_t r = r0 + grp; r < r1; r += GROUPS) {
     if (a.mask && !a.mask[r]) continue;             // (all lanes of the group)
@@ -190,7 +198,7 @@ template <int T, int G, int NI> __global__ __launch_bounds__(BAL_WG) void k_bala
       if ((uint32_t)id < (uint32_t)a.experts) atomicAdd(&hist[id], 1);      // whole numbers: any order
     }
     const float lse = softmax<G, NI>(v);
-    z2 += lse * lse;
+    z2 += (double)lse * lse;
     ++n;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -208,20 +216,20 @@ template <int T, int G, int NI> __global__ __launch_bounds__(BAL_WG) void k_bala
   const Part p(a.experts);
   float* part = a.part + blockIdx.x * p.words;
   for (int c = threadIdx.x; c < p.ep; c += BAL_WG) {
-    float v = 0.f;
+    double v = 0;
     for (int i = 0; i < GROUPS; ++i) v += sp[i * COLS + c];
-    part[c] = v;
+    part[c] = (float)v;
     part[p.ep + c] = __int_as_float(hist[c]);
   }
   if (threadIdx.x == 0) {
-    float z = 0.f;
+    double z = 0;
     int rows = 0;
     for (int i = 0; i < GROUPS; ++i) {
       z += sz[i];
       rows += sn[i];
     }
-    part[2 * p.ep] = z;
-    part[2 * p.ep + 1] = __int_as_float(rows);
+    *reinterpret_cast<double*>(part + 2 * p.ep) = z;
+    part[2 * p.ep + 2] = __int_as_float(rows);
   }
   if (gridDim.x == 1) {
     __syncthreads();
