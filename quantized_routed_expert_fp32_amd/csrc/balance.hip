@@ -55,14 +55,15 @@ template <int T> __device__ __forceinline__ void logits4(const void* row, int c,
   }
 }
 
-// e^d of d <= 0 (NaN stays): 2^(d log2 e) with the product's rounding and the rest of
-// log2 e made good, 2 ulp; below 2^-126 zero. Half the instructions of expf: the
-// forward kernel takes 18 to 20 us for 65536 x 256, with expf 22.
+// e^d of d <= 0 = 2^n 2^f, n the whole number next to d log2 e, f the rest (log2 e in two
+// parts, the first one's product exact), 2^f from the hardware. Off by 0.97 ulp at most over all
+// fp32 arguments (expf: 0.86), subnormal results by one step. The forward kernel takes 19.8 us for
+// 65536 x 256 fp32, with expf 22. A NaN is lost here (softmax has it).
 __device__ __forceinline__ float exp_neg(float d) {
-  constexpr float L = 1.44269502f, REST = 1.92596303e-8f, LN2 = 0.693147182f;
-  d = d < -200.f ? -200.f : d;
-  const float t = d * L, rest = __builtin_fmaf(d, L, -t) + d * REST;
-  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, LN2, 1.f);
+  constexpr float L = 1.44269502f, REST = 1.92596303e-8f;
+  d = __builtin_fmaxf(d, -200.f);
+  const float n = __builtin_rintf(d * L), f = __builtin_fmaf(d, REST, __builtin_fmaf(d, L, -n));
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 // p of a row in place of its logits; its logsumexp
 template <int G, int NI> __device__ __forceinline__ float softmax(float (&v)[NI][4]) {
@@ -77,7 +78,7 @@ template <int G, int NI> __device__ __forceinline__ float softmax(float (&v)[NI]
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) z += v[i][e] = exp_neg(v[i][e] - m);
-  z = over<G>(z, add);
+  z = over<G>(z, add) + (m - m);                  // NaN where the largest is not finite
   const float inv = 1.f / z;
 #pragma unroll
   for (int i = 0; i < NI; ++i)

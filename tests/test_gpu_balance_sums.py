@@ -1,4 +1,5 @@
-"""The balance losses' sums over rows, on logits whose every other rounding is known."""
+"""The balance losses' sums over rows, and probabilities below the normal numbers, on
+logits whose every other rounding is known."""
 import math
 
 import pytest
@@ -56,3 +57,29 @@ def test_balance_loss_sums(R, E):
     parts = 1 if R <= 256 else min(-(-R // 32), 256)
     adds = -(-(-(-R // parts)) // groups)
     assert abs(losses[0].item() - want) <= (adds + 2) * U * want
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E", [5, 64, 300])
+def test_probabilities_below_the_normal_numbers(E, dt):
+    """e^-88 and e^-96 are subnormal in fp32, and count: their gradients are normal numbers where the
+    z loss weighs much. The exponential and its product with 1 / z round to 2^-149 each."""
+    log(f"case balance subnormal {E} {dt}")
+    B = binding()
+    R = 40
+    l = torch.full((R, E), -math.inf, device="cuda")
+    l[:, 0], l[:, 1], l[:, 2], l[:, 3] = 1024.0, 1024.0 - 88.0, 1024.0 - 96.0, 1024.0 - 85.0
+    l = l.to(dt)
+    ids = torch.zeros(R, 1, dtype=torch.int32, device="cuda")
+    losses, counts = B.balance_forward(l, ids)
+    assert losses[1].item() == 2.0 ** 20
+    d = torch.tensor([0.0, 1e6], device="cuda")
+    got = B.balance_backward(d, l, counts, 1)
+    for c in (1, 2, 3):
+        far = 1024.0 - l[0, c].item()                  # (939 is 940 in bf16)
+        p = math.exp(-far)
+        factor = 2 * 1e6 * 1024.0 / R
+        want = torch.full((R,), p * factor, dtype=torch.float64)
+        bound = torch.full((R,), ((far + 10) * U * p + 2 * 2.0 ** -149) * factor, dtype=torch.float64)
+        K.close(got[:, c], want, K.rounded(want, bound, dt), f"dlogits {far}")
+    assert (got[:, 4:] == 0).all()
