@@ -506,6 +506,23 @@ def _no_history(fn, instead, names, *operands):
                        "call it under torch.no_grad()")
 
 
+_forward_ad = None
+
+
+def _no_tangent(fn, names, *operands):
+    """Refuses operands that carry a tangent of forward-mode differentiation, which the
+    result would lack without a word (torch.no_grad() leaves that mode on)."""
+    global _forward_ad
+    if _forward_ad is None:                 # (kept: an import statement costs a call 0.7 us)
+        from torch.autograd import forward_ad as _forward_ad
+    if getattr(_forward_ad, "_current_level", 0) < 0:      # outside every dual_level
+        return
+    for name, t in zip(names.split(), operands):
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise MoeError(f"{fn}: {name} carries a tangent of forward-mode differentiation, which this call does "
+                           "not compute: pass forward_ad.unpack_dual(..).primal")
+
+
 def _act_code(act):
     if act not in ACTIVATIONS:
         raise MoeError(f"act: {act!r} is not one of {', '.join(ACTIVATIONS)}")
@@ -592,6 +609,7 @@ def glu_forward(x, w_gate, w_up, act="silu", save=False, h=None, gu=None, ws=Non
     dtype (bf16 or fp16); with save=True (h, gu), gu fp32 [rows, 2, inter] being what
     glu_backward takes. h has no autograd history: without save (or gu), operands
     that require a gradient are refused where grad mode is on."""
+    _no_tangent("glu_forward", "x w_gate w_up", x, w_gate, w_up)
     if not save and gu is None:
         _no_history("glu_forward", "take save=True and glu_backward, or ", "x w_gate w_up", x, w_gate, w_up)
     a, dt, dev = _glu_args(x, w_gate, w_up, act)
@@ -636,6 +654,7 @@ def glu_backward(dh, x, w_gate, w_up, gu, act="silu", need_dx=True, need_dw=True
     """moe_glu_backward: (dx, dw_gate, dw_up) of glu_forward(..., save=True) from
     dh and its gu; None in the place of a gradient that is not needed. Gradients
     of these gradients are not computed: a dh that requires one is refused."""
+    _no_tangent("glu_backward", "dh x w_gate w_up gu", dh, x, w_gate, w_up, gu)
     _no_history("glu_backward", "", "dh", dh)
     a, dt, dev = _glu_args(x, w_gate, w_up, act)
     if not need_dx and not need_dw:
@@ -684,6 +703,7 @@ def glu_i8(x, w_gate, s_gate, w_up, s_up, act="silu", x_scale=None, out_dtype=No
     channel scales [inter]; x in bf16/fp16 (quantised a token inside the call),
     or int8 with x_scale [rows] (then out_dtype is h's type, bf16 by default). No
     gradients: operands that require one are refused where grad mode is on."""
+    _no_tangent("glu_i8", "x s_gate s_up x_scale", x, s_gate, s_up, x_scale)
     _no_history("glu_i8", "", "x s_gate s_up x_scale", x, s_gate, s_up, x_scale)
     if s_gate is None or s_up is None:
         raise MoeError("s_gate, s_up: needed with int8 weights")
@@ -779,6 +799,7 @@ def linear_i8(x, w, s_w, bias=None, x_scale=None, out_dtype=None, y=None, ws=Non
     scales s_w [out]; x in bf16/fp16 (quantised a token inside the call), or
     int8 with x_scale [rows] (then out_dtype is y's type, bf16 by default). No
     gradients: operands that require one are refused where grad mode is on."""
+    _no_tangent("linear_i8", "x s_w bias x_scale", x, s_w, bias, x_scale)
     _no_history("linear_i8", "", "x s_w bias x_scale", x, s_w, bias, x_scale)
     a, dt, dev = _linear_args(x, w, s_w, bias, x_scale, out_dtype)
     ctx = _call_ctx(dev, stream)
@@ -864,6 +885,7 @@ def norm_forward(x, weight, eps=1e-6, residual=None, unit_offset=False, save=Fal
     itself: then it is updated in place), rstd without save (or rstd); total (or x)
     and rstd are what norm_backward takes. Nothing has autograd history: without
     save, operands that require a gradient are refused where grad mode is on."""
+    _no_tangent("norm_forward", "x weight residual", x, weight, residual)
     if not save and rstd is None:
         _no_history("norm_forward", "take save=True and norm_backward, or ", "x weight residual", x, weight, residual)
     a, dt, dev = _norm_args(x, weight, eps, residual, unit_offset)
@@ -890,6 +912,7 @@ def norm_i8(x, weight, eps=1e-6, residual=None, unit_offset=False, want_y=False,
     scale each, what linear_i8 and glu_i8 take as x and x_scale; y is the 16-bit result
     too (with want_y or y, else None), total as in norm_forward. No gradients: operands
     that require one are refused where grad mode is on."""
+    _no_tangent("norm_i8", "x weight residual", x, weight, residual)
     _no_history("norm_i8", "", "x weight residual", x, weight, residual)
     a, dt, dev = _norm_args(x, weight, eps, residual, unit_offset)
     return _in(dev, stream, _norm_i8, a, dt, dev, residual, want_y, total, q, scale, y, stream)
@@ -931,6 +954,7 @@ def norm_backward(dy, total, weight, rstd, dtotal=None, unit_offset=False, need_
     that reaches the total itself; dx is the gradient of x and of the residual alike. None
     in the place of a gradient that is not needed. Gradients of these gradients are not
     computed: a dy or dtotal that requires one is refused."""
+    _no_tangent("norm_backward", "dy total weight rstd dtotal", dy, total, weight, rstd, dtotal)
     _no_history("norm_backward", "", "dy dtotal", dy, dtotal)
     if not need_dx and not need_dw:
         raise MoeError("norm_backward: neither need_dx nor need_dw")
@@ -991,6 +1015,7 @@ def balance_forward(logits, ids, mask=None, save=False, losses=None, counts=None
     the rows that count. No autograd history: without save=True (the caller runs
     balance_backward, which takes counts), logits that require a gradient are refused
     where grad mode is on."""
+    _no_tangent("balance_forward", "logits", logits)
     if not save:
         _no_history("balance_forward", "take save=True and balance_backward, or ", "logits", logits)
     import torch
@@ -1018,6 +1043,7 @@ def balance_backward(dlosses, logits, counts, k, mask=None, dlogits=None, stream
     """moe_balance_backward: dlogits [rows, experts] of the logits' type, from dlosses
     fp32 [2] (on the device), the counts of balance_forward and its number of picks k.
     Gradients of this gradient are not computed: dlosses that require one are refused."""
+    _no_tangent("balance_backward", "dlosses logits", dlosses, logits)
     _no_history("balance_backward", "", "dlosses", dlosses)
     import torch
     code, ld, mp, dev = _balance_args(logits, mask)
@@ -1105,6 +1131,7 @@ def lora_forward(x, a, b, ids, scale, base=None, save=False, y=None, t=None, ws=
     no adapter; scale fp32 [adapters]. With save=True (or t) (y, t), t fp32 [rows, rank]
     being what lora_backward takes. No autograd history: without save, operands that
     require a gradient are refused where grad mode is on; scale's is never computed."""
+    _no_tangent("lora_forward", "x a b scale base", x, a, b, scale, base)
     if not save and t is None:
         _no_history("lora_forward", "take save=True and lora_backward, or ", "x a b scale base", x, a, b, scale, base)
     else:
@@ -1140,6 +1167,7 @@ def lora_backward(dy, x, a, b, ids, scale, t=None, dx_base=None, need_dx=True, n
     gradient of base is dy itself. None in the place of a gradient that is not needed.
     Gradients of these gradients are not computed: a dy or dx_base that requires one
     is refused."""
+    _no_tangent("lora_backward", "dy x a b scale t dx_base", dy, x, a, b, scale, t, dx_base)
     _no_history("lora_backward", "", "dy dx_base", dy, dx_base)
     if not need_dx and not need_dw:
         raise MoeError("lora_backward: neither need_dx nor need_dw")
