@@ -596,7 +596,7 @@ int moe_lora_forward(const moe_lora* a, const void* base, int64_t ldbase, void* 
 /* Gradients from dy [rows, out] and the forward call's t:
  *   u_r = b_i^T dy_r,  dx_r = dx_base_r + scale_i a_i^T u_r     [rows, in]
  *     (dx_base [rows, in] or NULL: the gradient through the shared projection; it
- *     may be dx itself, same address and stride)
+ *     may be dx itself, same address and stride, and without da and db dy too)
  *   da_i = scale_i sum_r u_r x_r^T  [adapters, rank, in], db_i = scale_i sum_r dy_r
  *     t_r^T  [adapters, out, rank], contiguous; zero for adapters with no row
  * dx may be NULL, or da and db both (then t is not read). scale and base have no

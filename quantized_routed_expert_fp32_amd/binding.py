@@ -1163,8 +1163,9 @@ def lora_backward(dy, x, a, b, ids, scale, t=None, dx_base=None, need_dx=True, n
                   ws=None, stream=None):
     """moe_lora_backward: (dx, da, db) of lora_forward(..., save=True) from dy and its t
     (not read without need_dw). dx_base [rows, in] is added to dx: the gradient through the
-    shared projection (it may be passed as dx: then it is updated in place). The
-    gradient of base is dy itself. None in the place of a gradient that is not needed.
+    shared projection (it may be passed as dx: then it is updated in place; a dx_base that is
+    dy itself only without need_dw, as da and db read dy behind it). The gradient of base
+    is dy itself. None in the place of a gradient that is not needed.
     Gradients of these gradients are not computed: a dy or dx_base that requires one
     is refused."""
     _no_tangent("lora_backward", "dy x a b scale t dx_base", dy, x, a, b, scale, t, dx_base)

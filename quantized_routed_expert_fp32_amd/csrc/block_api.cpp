@@ -417,6 +417,8 @@ int moe_lora_backward(const moe_lora* a, const void* dy, int64_t lddy, const flo
     return st;
   const LoraPlan p = plan_lora(a, true, da != nullptr);
   if ((st = check_ws(fn, ws, ws_bytes, p.total))) return st;
+  // (dx is written first; dx_base, which it may be, is easily the same tensor as dy)
+  if (da && dx && (dx == a->x || dx == dy)) return bad(std::string(fn) + ": dx is x or dy, which da and db are computed from");
   uint8_t* w = static_cast<uint8_t*>(ws);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch_lora_sort(sort_args(a, p, w), s);
