@@ -542,7 +542,8 @@ int moe_norm_backward(const moe_norm* a, const float* rstd, const void* dy, int6
  *          as it does the formulas. Rows that do not count are not read.
  *   ids    [rows, k] int32 contiguous (moe_route's); outside 0..experts-1: no pick
  *   mask   [rows] bytes, 0 or 1, or NULL
- *   losses [2] fp32; counts [experts + 1] int32, the last one n
+ *   losses [2] fp32 (a thread's own rows of p are added in fp32, the rest of the sums
+ *          in 64 bits); counts [experts + 1] int32, the last one n
  * experts 1..1024, k 1..min(experts, 64). */
 int moe_balance_workspace_size(int rows, int experts, uint64_t* bytes);
 int moe_balance_forward(const void* logits, int dtype, int64_t ldlogits, const int32_t* ids, const uint8_t* mask, int rows,
@@ -588,7 +589,9 @@ int moe_lora_workspace_size(const moe_lora* a, int kind, uint64_t* bytes);
  *     rows with no adapter)
  * t goes into its product as two 16-bit parts, which keep 16 bits of it in bf16 and
  * 22 in fp16 (of the row's largest, for the small ones); for few rows (one launch
- * and no workspace) in fp32: a row's last bits may differ between the two.
+ * and no workspace) in fp32. A row's last bits may differ between the two, and
+ * among calls of other numbers of rows, which the ranges of its first sum follow;
+ * within a call, and between calls of as many rows, a row depends on itself alone.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ESHAPE, MOE_ENOSPACE, MOE_EHIP. */
 int moe_lora_forward(const moe_lora* a, const void* base, int64_t ldbase, void* y, int64_t ldy, float* t, void* ws,
                      uint64_t ws_bytes, void* stream);
@@ -598,7 +601,9 @@ int moe_lora_forward(const moe_lora* a, const void* base, int64_t ldbase, void* 
  *     (dx_base [rows, in] or NULL: the gradient through the shared projection; it
  *     may be dx itself, same address and stride, and without da and db dy too)
  *   da_i = scale_i sum_r u_r x_r^T  [adapters, rank, in], db_i = scale_i sum_r dy_r
- *     t_r^T  [adapters, out, rank], contiguous; zero for adapters with no row
+ *     t_r^T  [adapters, out, rank], contiguous; zero for adapters with no row,
+ *     whatever their a, b and scale hold. u and t enter as in the forward call (fp16:
+ *     22 bits of the largest value among some 256 or more rows of the adapter)
  * dx may be NULL, or da and db both (then t is not read). scale and base have no
  * gradient here (base's is dy). */
 int moe_lora_backward(const moe_lora* a, const void* dy, int64_t lddy, const float* t, const void* dx_base,

@@ -256,9 +256,9 @@ template <int DT> __device__ __forceinline__ u32x4 finite_or_zero(u32x4 v) {
 // ranges, 64 k a step: rows and weights go through LDS, a wave takes 16 rows. The
 // loads of the next two steps are in flight in registers, 16 bytes a lane at any
 // alignment, whole lines of a row. The K ranges' sums go through memory to
-// k_lora_parts. 4096 x 4096 to rank 64: 12.4 us, and 5.7 for k_lora_parts (joined by
+// k_lora_parts. 4096 x 4096 to rank 64: 13 us, and 5.7 for k_lora_parts (joined by
 // the last workgroup of a tile instead, 96: every workgroup's fence writes an L2 back);
-// 8192 rows 22 to 25 us, 2.7 to 3.0 TB/s of x.
+// 8192 rows 25 to 26 us, 2.6 TB/s of x.
 constexpr int SHR_K = 64;
 // a row of sums in memory
 static __host__ __device__ int sum_ld(int rank) { return (rank + 3) & ~3; }
@@ -443,8 +443,8 @@ template <int DT> __global__ __launch_bounds__(256) void k_lora_parts(LoraShrink
 // weights' rows are dealt to the fragments so that a lane ends with 8 consecutive
 // columns of a row, twice (fragment f, place m: column 32 (f / 2) + 8 (m / 4) + 4 (f % 2)
 // + m % 4): base and result move 16 bytes a lane, 64 a row, whole lines in two. 8192 x
-// rank 64 -> 4096: 48 to 50 us, 2.7 TB/s of base and result, where a copy in the same pattern
-// with all loads at the start takes 30; with 2 waves a SIMD instead of 4 it takes 55.
+// rank 64 -> 4096: 45 to 46 us, 2.9 TB/s of base and result, where a copy in the same pattern
+// with all loads at the start takes 30; with 2 waves a SIMD instead of 4 it took 55 for 48.
 template <int DT, bool KM, int KB> __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraExpand a) {
   constexpr int F = 4, WROW = KM ? 144 : KB * 64 + 16, STAGE = KM ? KB * 32 * WROW : 64 * WROW;
   constexpr int CPR = KM ? 8 : KB * 4, WL = KB;    // chunks of a staged row, loads of a thread
@@ -970,7 +970,11 @@ hipError_t launch_lora_grad(int dt, const LoraGrad& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-// Where the rows' own reads of the weights (a row's a and b each) stay few
+// Few rows: one launch, each row's weights through one CU, against the tiles' four. It is the
+// better one while rank (in + out) of a row stays below 256 Ki, whatever the rows: bf16, 16 rows
+// of 4096 -> 4096, rank 16 12 us for 25, rank 32 20 for 25, rank 64 38 for 26; 64 rows of 2048 ->
+// 2048, rank 32 13 for 29. The limit here is on all rows' products, and leaves the worse one on
+// both sides of that: 4 rows of 4096, rank 256 take 124 us for 32, 64 rows of rank 32 35 for 27.
 bool lora_by_row(int rows, int in, int out, int rank) { return rows <= 64 && (int64_t)rows * rank * (in + (int64_t)out) <= 8 << 20; }
 
 template <int DT> static hipError_t by_row(const LoraRow& a, hipStream_t s) {

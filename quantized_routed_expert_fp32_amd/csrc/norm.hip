@@ -113,7 +113,9 @@ __device__ __forceinline__ float row_rstd(const u32x4* held, int cols, float eps
 // A workgroup takes rows blockIdx, blockIdx + gridDim.. one at a time, a chunk (NC,
 // beyond 8192 columns) a thread, the next row's loads in flight while a row is reduced
 // and written; each thread holds its columns' weights. 8192 x 4096 with a residual:
-// 42 to 48 us for 268 MB, 5.6 to 6.4 TB/s (a row without the next one's loads 54 to 62).
+// 42 to 48 us for 268 MB, 5.6 to 6.4 TB/s (a row without the next one's loads 54 to 62); in
+// 8 bits 57. Beyond 16384 columns (NC = 8) a row and the next one are more than the registers
+// hold: as many elements take 187 us through scratch, in 8 bits 254, their gradients 430.
 template <int DT, int XT, bool I8, int TPR, int NC> __global__ __launch_bounds__(TPR) void k_norm(NormArgs a) {
   __shared__ float red[TPR / 64];
   __shared__ uint32_t redm[TPR / 64];
@@ -370,7 +372,9 @@ hipError_t launch_norm(int dt, const NormArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-// Workgroups of the gradients: 16 waves a CU, which keeps their sums at 8 MiB
+// Workgroups of the gradients: 16 waves a CU. Their sums of dw take up to 8 MiB of the
+// workspace for 8192 columns, beyond that (1024 threads a row, so no fewer workgroups) up to
+// 64 MiB for 65536.
 static int norm_grad_parts(int rows, int hidden) {
   const int most = 4096 * 64 / row_threads(hidden);
   return rows < most ? rows : most;
